@@ -17,10 +17,11 @@
 #include "../../include/q1.h"
 #include "../../include/q1_measure.h"
 #include "q1_internal.h"
+#include "q1_status.h"
 
-namespace {
+namespace q1 {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 q1_status fail(q1_status s, const char* fmt, ...) {
   va_list ap;
@@ -35,6 +36,38 @@ q1_status ok() {
   return Q1_OK;
 }
 
+// Device check, cached per device id.
+static std::mutex g_dev_mu;
+static signed char g_dev_ok[256];  // 0 unknown, 1 ok, -1 unsupported
+
+q1_status check_current_device() {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return fail(Q1_ERR_HIP, "hipGetDevice failed");
+  if (dev >= 0 && dev < 256) {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (g_dev_ok[dev] == 1) return Q1_OK;
+  }
+  return q1_device_supported(dev);
+}
+
+q1_status hip_status(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(Q1_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+}  // namespace q1
+
+using q1::check_current_device;
+using q1::fail;
+using q1::hip_status;
+using q1::ok;
+using q1::aligned;
+using q1::align_up;
+using q1::valid_out_dtype;
+using q1::dtype_size;
+
+namespace {
+
 int initial_max_rows() {
   const char* e = getenv("Q1_QMM_MAX_ROWS");
   if (e) {
@@ -45,14 +78,6 @@ int initial_max_rows() {
 }
 
 int g_max_rows = initial_max_rows();
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool valid_out_dtype(int32_t d) { return d == Q1_F32 || d == Q1_F16 || d == Q1_BF16; }
-
-size_t dtype_size(int32_t d) { return d == Q1_F32 ? 4 : 2; }
 
 q1_status check_weight(const q1_weight* w, const char* name) {
   if (w == nullptr) return fail(Q1_ERR_INVALID_ARG, "%s: weight descriptor is NULL", name);
@@ -89,25 +114,6 @@ q1::QMat to_mat(const q1_weight* w) {
   m.N = w->N;
   m.K = w->K;
   return m;
-}
-
-// Device check, cached per device id.
-std::mutex g_dev_mu;
-signed char g_dev_ok[256];  // 0 unknown, 1 ok, -1 unsupported
-
-q1_status check_current_device() {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return fail(Q1_ERR_HIP, "hipGetDevice failed");
-  if (dev >= 0 && dev < 256) {
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    if (g_dev_ok[dev] == 1) return Q1_OK;
-  }
-  return q1_device_supported(dev);
-}
-
-q1_status hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(Q1_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 // ---- workspace layouts --------------------------------------------------
@@ -334,7 +340,7 @@ q1_status qmm_run(const void* x, int64_t M, const q1_weight* w, void* y, int32_t
 
 extern "C" {
 
-const char* q1_last_error(void) { return g_err; }
+const char* q1_last_error(void) { return q1::g_err; }
 
 const char* q1_version(void) { return "q1-gfx950 0.1"; }
 
@@ -353,8 +359,8 @@ q1_status q1_device_supported(int device) {
     return fail(Q1_ERR_UNSUPPORTED, "device %d is %s; the Q1 kernels are built for gfx950 (MI355X) only", device,
                 prop.gcnArchName);
   if (device >= 0 && device < 256) {
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    g_dev_ok[device] = 1;
+    std::lock_guard<std::mutex> lk(q1::g_dev_mu);
+    q1::g_dev_ok[device] = 1;
   }
   return ok();
 }

@@ -1,0 +1,62 @@
+// Internal interface between the C ABI of the decode-step operators
+// (q1_decode_api.cpp) and their HIP kernels.  Not part of the public boundary.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/q1_decode.h"
+
+namespace q1 {
+
+// ---- gated delta rule -------------------------------------------------------
+
+// Sequence s of a launch: tokens [first, first + len) of the packed rows.  With
+// cu == nullptr every sequence has T tokens.
+struct DeltaArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_ld, k_ld, v_ld;
+  const float* g;
+  const float* beta;
+  float* state;
+  const int32_t* slot_ids;
+  void* out;
+  int64_t slots;
+  int32_t Hk, Hv, Dv;
+  int32_t out_dtype, l2norm;
+  float scale;
+  int64_t T;        // tokens per sequence (cu == nullptr)
+  const int32_t* cu;
+  int64_t tokens;   // rows in all (cu != nullptr)
+  int64_t nseq;
+};
+
+hipError_t launch_delta_recurrent(const DeltaArgs& a, bool f16, int Dk, hipStream_t s);
+
+// ---- attention over a shared prefix -----------------------------------------
+
+hipError_t launch_prefix_attn(const q1_attn& a, unsigned char* ws, hipStream_t s);
+
+// ---- sampler ----------------------------------------------------------------
+
+struct SampleArgs {
+  const void* logits;
+  int32_t dtype;
+  int64_t B, V, ld;
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  void* tokens;
+  int32_t tokens_int64;
+  float* logprob;
+};
+
+hipError_t launch_sample(const SampleArgs& a, unsigned char* ws, hipStream_t s);
+
+}  // namespace q1
