@@ -1,6 +1,26 @@
-// Attention of a decode batch over a shared prefix and paged suffixes: one
-// workgroup per (sequence, query head), a pass over the tokens in blocks of 256
-// with a running maximum and sum.
+// Attention of a decode batch over a shared prefix and paged suffixes.
+//
+// Two launches: q1_attn_main computes, per work item, the running maximum m,
+// sum l and unnormalised output o of some query rows over some tokens;
+// q1_attn_join adds the items of a row.  A prefix item holds the rows of all
+// sequences that share a key/value head (B * Hq/Hkv of them, in blocks of 16 NM),
+// so a prefix token is read once per block and not once per sequence; a suffix
+// item holds the Hq/Hkv rows of one sequence.  Tokens are split over items so that
+// the launch has about one workgroup per compute unit (see plan_prefix_attn).
+//
+// In an item each of the 4 waves takes every fourth tile of 32 tokens, by itself,
+// with all the rows:
+//   S^T = K Q^T   keys are the A operand, straight from memory (lane: token l%16,
+//                 8 consecutive elements); queries the B operand, in registers.
+//   softmax       a lane has one query (l%16) and 8 tokens: maximum and sum are
+//                 in-lane, then over 4 lanes.
+//   O^T = V^T P^T the weights come out of S^T as the B operand's layout (tokens
+//                 4(l/16)..+3 of both 16-token halves); values go through a
+//                 wave's own LDS tile and come back transposed (ds_read_tr16).
+// Weights enter the second product as two 16-bit parts (high and remainder), so
+// that their rounding (2^-17) stays below the output's; their sum, the maximum
+// and the output are fp32.  Values and keys of tokens past the length are never
+// loaded: zeros stand for them and their scores are -infinity.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -12,82 +32,386 @@
 namespace q1 {
 namespace {
 
-constexpr int kThreads = 256;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-__global__ __launch_bounds__(kThreads) void q1_attn_plain_kernel(const q1_attn a) {
-  __shared__ float sc[kThreads], qs[256], red[kThreads];
-  const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x / a.Hq;
-  const int h = (int)(blockIdx.x - b * a.Hq), hk = h / (a.Hq / a.Hkv), D = a.D;
-  const bool f16 = a.dtype == Q1_F16;
-  auto cvt = [f16](uint16_t x) { return f16 ? f16_bits_to_f32(x) : bf16_bits_to_f32(x); };
-  const auto* q = static_cast<const uint16_t*>(a.q) + b * a.q_ld + (int64_t)h * D;
-  if (tid < D) qs[tid] = cvt(q[tid]);
-  __syncthreads();
-  int64_t suffix = 0;
-  if (a.max_pages > 0) {
-    suffix = a.suffix_lens[b];
-    const int64_t most = a.max_pages * a.page_size;
-    suffix = suffix < 0 ? 0 : suffix > most ? most : suffix;
+constexpr int kWaves = 4;
+constexpr int kTile = 32;               // tokens of a wave's tile
+constexpr int kStep = kWaves * kTile;   // tokens of a workgroup's iteration
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two floats rounded to the operand type, and what the rounding left.
+template <bool F16>
+__device__ __forceinline__ uint32_t round2(float x, float y, float* rx, float* ry) {
+  if constexpr (F16) {
+    const f16x2 h = __builtin_convertvector(f32x2{x, y}, f16x2);
+    *rx = x - (float)h[0];
+    *ry = y - (float)h[1];
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    const bf16x2 h = __builtin_convertvector(f32x2{x, y}, bf16x2);
+    *rx = x - (float)h[0];
+    *ry = y - (float)h[1];
+    return __builtin_bit_cast(uint32_t, h);
   }
-  const int64_t n = a.P + suffix;
-  auto row = [&](int64_t t, const void* pre, const void* pag) -> const uint16_t* {
-    if (t < a.P) return static_cast<const uint16_t*>(pre) + t * a.prefix_ld + (int64_t)hk * D;
-    const int64_t s = t - a.P, pg = a.page_table[b * a.max_pages + s / a.page_size];
-    if (pg < 0 || pg >= a.pages) return nullptr;
-    return static_cast<const uint16_t*>(pag) + ((pg * a.page_size + s % a.page_size) * a.Hkv + hk) * D;
+}
+
+// Maximum / sum over the four lanes that differ in bits 4 and 5 of the lane id.
+__device__ __forceinline__ float max_groups(float v) {
+  float w = v;
+  asm("" : "+v"(w));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(w), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  w = v;
+  asm("" : "+v"(w));
+  auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(w), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+__device__ __forceinline__ float sum_groups(float v) {
+  float w = v;
+  asm("" : "+v"(w));
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(w), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  w = v;
+  asm("" : "+v"(w));
+  auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(w), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+__device__ __forceinline__ int64_t suffix_len(const q1_attn& a, int64_t b) {
+  if (a.max_pages == 0) return 0;
+  const int64_t n = a.suffix_lens[b], most = a.max_pages * a.page_size;
+  return n < 0 ? 0 : n > most ? most : n;
+}
+
+// Weights are taken relative to 2^kLift of the maximum, so that an fp16 remainder
+// of a small one is still a normal number; bf16 has fp32's range.
+template <bool F16>
+constexpr float kLift = F16 ? 12.0f : 0.0f;
+
+template <bool F16, int D, int NM>
+__global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, const AttnPlan p, float* part_o,
+                                                            float2* part_ml) {
+  constexpr int KS = D / 32, DT = D / 16, VROW = 2 * D + 32;  // LDS bytes of a value row: rows start 8 banks apart
+  constexpr int VCH = D / 8, VPI = 64 / VCH, VN = kTile / VPI;  // 16-byte pieces a row, rows and loads of a value tile
+  extern __shared__ __align__(16) unsigned char lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+  const int group = a.Hq / a.Hkv;
+
+  // The item: its rows, tokens and where its results go.
+  int64_t b0 = 0, t0, t1;  // suffix: the sequence; tokens
+  int hk, R, rb, split;
+  const bool prefix = blockIdx.x < (unsigned)p.prefix_wgs;
+  if (prefix) {
+    // blocks of rows over the same tokens are 8 workgroups apart: the same XCD's L2
+    const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+    rb = y % p.prefix_rb;
+    const int pair = (y / p.prefix_rb) * 8 + x;
+    if (pair >= a.Hkv * p.prefix_splits) return;
+    hk = pair % a.Hkv;
+    split = pair / a.Hkv;
+    R = (int)a.B * group;
+    t0 = (int64_t)split * p.prefix_tokens;
+    t1 = t0 + p.prefix_tokens < a.P ? t0 + p.prefix_tokens : a.P;
+  } else {
+    int64_t i = blockIdx.x - p.prefix_wgs;
+    hk = (int)(i % a.Hkv);
+    i /= a.Hkv;
+    rb = (int)(i % p.suffix_rb);
+    i /= p.suffix_rb;
+    split = (int)(i % p.suffix_splits);
+    b0 = i / p.suffix_splits;
+    R = group;
+    const int64_t n = suffix_len(a, b0);
+    t0 = (int64_t)split * p.suffix_tokens;
+    t1 = t0 + p.suffix_tokens < n ? t0 + p.suffix_tokens : n;
+    split += p.prefix_splits;
+    if (t0 >= t1) return;
+  }
+  const int row0 = rb * 16 * NM, live = (R - row0 + 15) / 16 < NM ? (R - row0 + 15) / 16 : NM;
+  auto out_row = [&](int r) -> int64_t {  // r < R
+    return prefix ? (int64_t)(r / group) * a.Hq + hk * group + r % group : b0 * a.Hq + hk * group + r;
   };
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int64_t t0 = 0; t0 < n; t0 += kThreads) {
-    const int64_t t = t0 + tid;
-    float s = -INFINITY;
-    if (t < n) {
-      const uint16_t* k = row(t, a.k_prefix, a.k_pages);
-      if (k != nullptr) {
-        s = 0.f;
-        for (int i = 0; i < D; ++i) s = __builtin_fmaf(qs[i], cvt(k[i]), s);
-        s *= a.scale;
-      }
-    }
-    red[tid] = s;
-    __syncthreads();
-    for (int w = kThreads / 2; w > 0; w >>= 1) {
-      if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
-      __syncthreads();
-    }
-    const float mn = fmaxf(m, red[0]);
-    __syncthreads();
-    const float p = s == -INFINITY ? 0.f : expf(s - mn);
-    sc[tid] = p;
-    red[tid] = p;
-    __syncthreads();
-    for (int w = kThreads / 2; w > 0; w >>= 1) {
-      if (tid < w) red[tid] += red[tid + w];
-      __syncthreads();
-    }
-    const float keep = m == -INFINITY ? 0.f : expf(m - mn);
-    l = l * keep + red[0];
-    if (tid < D) {
-      o *= keep;
-      for (int j = 0; j < kThreads && t0 + j < n; ++j) {
-        if (sc[j] == 0.f) continue;
-        const uint16_t* v = row(t0 + j, a.v_prefix, a.v_pages);
-        if (v != nullptr) o = __builtin_fmaf(sc[j], cvt(v[tid]), o);
-      }
-    }
-    m = mn;
-    __syncthreads();
+
+  u32x4 Q[NM][KS];
+#pragma unroll
+  for (int n = 0; n < NM; ++n) {
+    const int r = row0 + 16 * n + col;
+    const int64_t b = prefix ? r / group : b0;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ld + (int64_t)(hk * group + (prefix ? r % group : r)) * D + 8 * grp;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      Q[n][s] = r < R ? *reinterpret_cast<const u32x4*>(q + 32 * s) : u32x4{0u, 0u, 0u, 0u};
   }
-  if (tid < D) store_out(a.out, a.out_dtype, (b * a.Hq + h) * D + tid, l > 0.f ? o / l : 0.f);
-  if (tid == 0 && a.lse != nullptr) a.lse[b * a.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+
+  const auto* kb = static_cast<const uint16_t*>(prefix ? a.k_prefix : a.k_pages) + (int64_t)hk * D;
+  const auto* vb = static_cast<const uint16_t*>(prefix ? a.v_prefix : a.v_pages) + (int64_t)hk * D;
+  const int64_t ld = prefix ? a.prefix_ld : (int64_t)a.Hkv * D;
+  // Row of token t0 + (lane % 32) of the tile at t, or -1.
+  auto row_of = [&](int64_t t) -> int {
+    const int64_t tok = t + (lane & 31);
+    if (tok >= t1) return -1;
+    if (prefix) return (int)tok;
+    const uint32_t ps = (uint32_t)a.page_size, pg = (uint32_t)tok / ps;
+    const int id = a.page_table[b0 * a.max_pages + pg];
+    return id < 0 || id >= a.pages ? -1 : (int)((int64_t)id * ps + ((uint32_t)tok - pg * ps));
+  };
+
+  u32x4 K[2][KS], V[VN];
+  int rows = -1;
+  auto load_k = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = __shfl(rows, 16 * h + col);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        K[h][s] = r >= 0 ? *reinterpret_cast<const u32x4*>(kb + r * ld + 32 * s + 8 * grp) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const int r = __shfl(rows, i * VPI + lane / VCH);
+      V[i] = r >= 0 ? *reinterpret_cast<const u32x4*>(vb + r * ld + 8 * (lane % VCH)) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+
+  f32x4 O[DT][NM];
+  float m[NM], l[NM];
+#pragma unroll
+  for (int n = 0; n < NM; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[d][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  unsigned char* vt = lds + wave * (kTile * VROW);
+  unsigned char* vw = vt + (lane / VCH) * VROW + 16 * (lane % VCH);
+  const unsigned char* vr = vt + (4 * grp + col / 4) * VROW + 8 * (col & 3);
+  const float sc = a.scale * kLog2e;
+
+  int64_t t = t0 + wave * kTile;
+  if (t < t1) {
+    rows = row_of(t);
+    load_k();
+    load_v();
+  }
+  for (; t < t1; t += kStep) {
+    const int have = rows;
+    // scores, then the next tile's rows and keys
+    f32x4 S[2][NM];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NM; ++n) {
+        S[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (n < live) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) S[h][n] = mma<F16>(K[h][s], Q[n][s], S[h][n]);
+        }
+      }
+    const int64_t tn = t + kStep;
+    if (tn < t1) {
+      rows = row_of(tn);
+      load_k();
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) *reinterpret_cast<u32x4*>(vw + i * VPI * VROW) = V[i];
+    if (tn < t1) load_v();
+
+    // which of this lane's 8 tokens count
+    const uint64_t in = __ballot(have >= 0);
+    const uint32_t mine = ((uint32_t)in >> (4 * grp) & 15u) | ((uint32_t)in >> (16 + 4 * grp) & 15u) << 4;
+    u32x4 hi[NM], lo[NM];
+#pragma unroll
+    for (int n = 0; n < NM; ++n) {
+      if (n >= live) continue;
+      float s[8], top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j] = (mine >> j) & 1u ? S[j >> 2][n][j & 3] * sc : -INFINITY;
+        top = fmaxf(top, s[j]);
+      }
+      const float mn = fmaxf(m[n], max_groups(top));
+      const float base = mn == -INFINITY ? 0.f : mn;  // no token yet: every exponent below is -infinity
+      if (__any(mn != m[n])) {
+        const float keep = __builtin_amdgcn_exp2f(m[n] - base);
+        l[n] *= keep;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) O[d][n] *= keep;
+        m[n] = mn;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j] = __builtin_amdgcn_exp2f(s[j] - base + kLift<F16>);
+        l[n] += s[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float rx, ry, r0, r1;
+        hi[n][j] = round2<F16>(s[2 * j], s[2 * j + 1], &rx, &ry);
+        lo[n][j] = round2<F16>(rx, ry, &r0, &r1);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vr + 32 * d));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vr + 16 * VROW + 32 * d));
+      const uint2 xw = __builtin_bit_cast(uint2, x), yw = __builtin_bit_cast(uint2, y);
+      const u32x4 vt4 = {xw.x, xw.y, yw.x, yw.y};
+#pragma unroll
+      for (int n = 0; n < NM; ++n)
+        if (n < live) {
+          O[d][n] = mma<F16>(vt4, hi[n], O[d][n]);
+          O[d][n] = mma<F16>(vt4, lo[n], O[d][n]);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // Join the waves in LDS (over the value tiles) and store the item's part.
+  constexpr int OROW = D + 4;
+  float* so = reinterpret_cast<float*>(lds);
+  float2* sml = reinterpret_cast<float2*>(so + kWaves * 16 * NM * OROW);
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NM; ++n) {
+    const int r = wave * 16 * NM + 16 * n + col;
+    const float sum = sum_groups(l[n]);
+    if (grp == 0) sml[r] = float2{m[n], sum};
+#pragma unroll
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = O[d][n];
+  }
+  __syncthreads();
+  const int64_t base = (int64_t)split * a.B * a.Hq;
+  for (int i = threadIdx.x; i < 16 * live * (D / 4); i += 64 * kWaves) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    if (row0 + r >= R) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sml[w * 16 * NM + r].x);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float2 ml = sml[w * 16 * NM + r];
+      const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+      o += f * *reinterpret_cast<const f32x4*>(so + (w * 16 * NM + r) * OROW + c);
+      sum += f * ml.y;
+    }
+    const int64_t at = base + out_row(row0 + r);
+    *reinterpret_cast<f32x4*>(part_o + at * D + c) = o;
+    if (c == 0) part_ml[at] = float2{top, sum};
+  }
+}
+
+// One wave per (sequence, query head): adds its parts.
+template <int D>
+__global__ __launch_bounds__(64) void q1_attn_join(const q1_attn a, const AttnPlan p, const float* part_o,
+                                                   const float2* part_ml, float lift) {
+  constexpr int E = D / 64;
+  const int64_t row = blockIdx.x, rows = a.B * a.Hq;
+  const int lane = threadIdx.x;
+  const int64_t n = suffix_len(a, row / a.Hq);
+  const int parts = p.prefix_splits + (int)((n + p.suffix_tokens - 1) / p.suffix_tokens);
+  float top = -INFINITY;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, part_ml[s * rows + row].x);
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  float o[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float2 ml = part_ml[s * rows + row];
+      const float f = __builtin_amdgcn_exp2f(ml.x - top);
+      sum += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(f, part_o[(s * rows + row) * D + e * 64 + lane], o[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) store_out(a.out, a.out_dtype, row * D + e * 64 + lane, o[e] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? (top - lift) * 0.69314718055994530942f + logf(sum) : -INFINITY;
+}
+
+template <bool F16, int D, int NM>
+hipError_t launch(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
+  constexpr int vt = kWaves * kTile * (2 * D + 32), jo = kWaves * 16 * NM * ((D + 4) * 4 + 8);
+  constexpr int bytes = vt > jo ? vt : jo;
+  static bool set = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_attn_main<F16, D, NM>),
+                                        hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
+  (void)set;
+  if (p.wgs > 0)
+    hipLaunchKernelGGL((q1_attn_main<F16, D, NM>), dim3((unsigned)p.wgs), dim3(64 * kWaves), bytes, s, a, p, po, pml);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((q1_attn_join<D>), dim3((unsigned)(a.B * a.Hq)), dim3(64), 0, s, a, p, po, pml, kLift<F16>);
+  return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_t(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
+  if (a.D == 64) return p.nm == 1 ? launch<F16, 64, 1>(a, p, po, pml, s) : p.nm == 2 ? launch<F16, 64, 2>(a, p, po, pml, s) : launch<F16, 64, 4>(a, p, po, pml, s);
+  if (a.D == 128) return p.nm == 1 ? launch<F16, 128, 1>(a, p, po, pml, s) : p.nm == 2 ? launch<F16, 128, 2>(a, p, po, pml, s) : launch<F16, 128, 4>(a, p, po, pml, s);
+  return p.nm == 1 ? launch<F16, 256, 1>(a, p, po, pml, s) : launch<F16, 256, 2>(a, p, po, pml, s);
 }
 
 }  // namespace
 
-hipError_t launch_prefix_attn(const q1_attn& a, unsigned char* ws, hipStream_t s) {
-  (void)ws;
-  hipLaunchKernelGGL(q1_attn_plain_kernel, dim3((unsigned)(a.B * a.Hq)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+AttnPlan plan_prefix_attn(const q1_attn& a) {
+  AttnPlan p = {};
+  const int64_t group = a.Hq / a.Hkv, R = a.P > 0 ? a.B * group : group;
+  const int64_t tiles = (R + 15) / 16;
+  p.nm = tiles <= 1 ? 1 : tiles <= 2 || a.D == 256 ? 2 : 4;
+  p.prefix_rb = (int)((a.B * group + 16 * p.nm - 1) / (16 * p.nm));
+  p.suffix_rb = (int)((group + 16 * p.nm - 1) / (16 * p.nm));
+  const int64_t most = a.max_pages * a.page_size;
+  const int64_t pit = (a.P + kStep - 1) / kStep, sit = (most + kStep - 1) / kStep;
+  // iterations of kStep tokens, over all items
+  const int64_t total = pit * a.Hkv * p.prefix_rb + sit * a.B * a.Hkv * p.suffix_rb;
+  const int64_t cus = device_cus();
+  int64_t per = (total + cus - 1) / cus;  // iterations per item: about a workgroup per compute unit
+  if (per < 1) per = 1;
+  // at most 64 parts of each kind to add per row
+  int64_t pper = per, sper = per;
+  if ((pit + pper - 1) / pper > 64) pper = (pit + 63) / 64;
+  if ((sit + sper - 1) / sper > 64) sper = (sit + 63) / 64;
+  p.prefix_splits = (int)((pit + pper - 1) / pper);
+  p.prefix_tokens = pper * kStep;
+  p.suffix_splits = (int)((sit + sper - 1) / sper);
+  p.suffix_tokens = sper * kStep;
+  const int64_t pairs = (a.Hkv * (int64_t)p.prefix_splits + 7) / 8 * 8;
+  p.prefix_wgs = pairs * p.prefix_rb;
+  p.wgs = p.prefix_wgs + (int64_t)p.suffix_splits * a.B * a.Hkv * p.suffix_rb;
+  const size_t rows = (size_t)(p.prefix_splits + p.suffix_splits) * a.B * a.Hq;
+  p.ml_off = (rows * a.D * 4 + 255) / 256 * 256;
+  p.ws_bytes = p.ml_off + (rows * 8 + 255) / 256 * 256;
+  return p;
+}
+
+hipError_t launch_prefix_attn(const q1_attn& a, const AttnPlan& p, unsigned char* ws, hipStream_t s) {
+  float* po = reinterpret_cast<float*>(ws);
+  float2* pml = reinterpret_cast<float2*>(ws + p.ml_off);
+  return a.dtype == Q1_F16 ? launch_t<true>(a, p, po, pml, s) : launch_t<false>(a, p, po, pml, s);
 }
 
 }  // namespace q1

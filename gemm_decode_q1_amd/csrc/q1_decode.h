@@ -39,7 +39,18 @@ hipError_t launch_delta_recurrent(const DeltaArgs& a, bool f16, int Dk, hipStrea
 
 // ---- attention over a shared prefix -----------------------------------------
 
-hipError_t launch_prefix_attn(const q1_attn& a, unsigned char* ws, hipStream_t s);
+// How a call is cut into work items (see q1_attn.hip).
+struct AttnPlan {
+  int32_t nm;                            // blocks of 16 query rows per item
+  int32_t prefix_rb, suffix_rb;          // items along the rows
+  int32_t prefix_splits, suffix_splits;  // items along the tokens
+  int64_t prefix_tokens, suffix_tokens;  // tokens per item
+  int64_t prefix_wgs, wgs;
+  size_t ml_off, ws_bytes;
+};
+
+AttnPlan plan_prefix_attn(const q1_attn& a);
+hipError_t launch_prefix_attn(const q1_attn& a, const AttnPlan& p, unsigned char* ws, hipStream_t s);
 
 // ---- sampler ----------------------------------------------------------------
 

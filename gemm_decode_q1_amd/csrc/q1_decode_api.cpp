@@ -101,7 +101,7 @@ q1_status check_attn(const q1_attn* a) {
     return fail(Q1_ERR_UNSUPPORTED, "call too large");
   if (a->max_pages > 0 &&
       (a->page_size >= (int64_t)1 << 31 || a->max_pages >= (int64_t)1 << 31 || a->pages >= (int64_t)1 << 31 ||
-       a->max_pages * a->page_size >= (int64_t)1 << 31 || a->pages * a->page_size > lim / row))
+       a->max_pages * a->page_size >= (int64_t)1 << 31 || a->pages * a->page_size >= (int64_t)1 << 31))
     return fail(Q1_ERR_UNSUPPORTED, "call too large");
   return Q1_OK;
 }
@@ -163,7 +163,7 @@ q1_status q1_delta_prefill(const q1_delta* d, int64_t tokens, int64_t nseq, cons
 size_t q1_prefix_attn_workspace_bytes(const q1_attn* a) {
   if (check_attn(a) != Q1_OK) return 0;
   ok();
-  return 0;
+  return a->B == 0 ? 0 : plan_prefix_attn(*a).ws_bytes;
 }
 
 q1_status q1_prefix_attn(const q1_attn* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -182,13 +182,15 @@ q1_status q1_prefix_attn(const q1_attn* a, void* workspace, size_t workspace_byt
     return fail(Q1_ERR_INVALID_ARG, "q, out, keys and values must be 16-byte aligned");
   if (!aligned(a->page_table, 4) || !aligned(a->suffix_lens, 4) || !aligned(a->lse, 4))
     return fail(Q1_ERR_INVALID_ARG, "page_table, suffix_lens and lse must be 4-byte aligned");
-  const size_t need = q1_prefix_attn_workspace_bytes(a);
+  const AttnPlan plan = plan_prefix_attn(*a);
+  if (plan.wgs > kMaxGrid) return fail(Q1_ERR_UNSUPPORTED, "call too large");
+  const size_t need = plan.ws_bytes;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(Q1_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
   if (need > 0 && !aligned(workspace, 256)) return fail(Q1_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   st = check_current_device();
   if (st != Q1_OK) return st;
-  return hip_status(launch_prefix_attn(*a, static_cast<unsigned char*>(workspace), static_cast<hipStream_t>(stream)),
+  return hip_status(launch_prefix_attn(*a, plan, static_cast<unsigned char*>(workspace), static_cast<hipStream_t>(stream)),
                     "attention launch");
 }
 
