@@ -16,7 +16,8 @@ SOURCES = ([os.path.join(PKG, "csrc", "q1_api.cpp"), os.path.join(PKG, "csrc", "
             os.path.join(PKG, "csrc", "q1_wide.hip"),
             os.path.join(PKG, "csrc", "q1_meta.hip"), os.path.join(PKG, "csrc", "q1_scratch.hip"),
             os.path.join(PKG, "csrc", "q1_gemv.hip"), os.path.join(PKG, "csrc", "q1_decode_api.cpp"),
-            os.path.join(PKG, "csrc", "q1_delta.hip"), os.path.join(PKG, "csrc", "q1_attn.hip"),
+            os.path.join(PKG, "csrc", "q1_delta.hip"),
+            os.path.join(PKG, "csrc", "q1_delta_chunk.hip"), os.path.join(PKG, "csrc", "q1_attn.hip"),
             os.path.join(PKG, "csrc", "q1_sample.hip")])
 # Packed-FP32 instructions are disabled for all device code (see the design
 # notes): hipcc otherwise forms v_pk_*_f32 from plain float code.

@@ -111,7 +111,9 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, con
   constexpr int KS = D / 32, DT = D / 16, VROW = 2 * D + 32;  // LDS bytes of a value row: rows start 8 banks apart
   constexpr int VCH = D / 8, VPI = 64 / VCH, VN = kTile / VPI;  // 16-byte pieces a row, rows and loads of a value tile
   extern __shared__ __align__(16) unsigned char lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
+  // in a scalar register: matrix-core products ignore the lane mask, so the loop they are in must be a scalar one
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = a.Hq / a.Hkv;
 
   // The item: its rows, tokens and where its results go.

@@ -50,6 +50,7 @@ q1_status check_delta(const q1_delta* d, int64_t tokens, int64_t nseq) {
     return fail(Q1_ERR_INVALID_ARG, "%lld sequences need as many state slots (got %lld)", (long long)nseq,
                 (long long)d->slots);
   const int64_t ld = d->q_ld > d->k_ld ? (d->q_ld > d->v_ld ? d->q_ld : d->v_ld) : (d->k_ld > d->v_ld ? d->k_ld : d->v_ld);
+  if (ld >= (int64_t)1 << 23) return fail(Q1_ERR_UNSUPPORTED, "row strides must be below 2^23 elements");
   if (tokens >= (int64_t)1 << 31 || tokens > ((int64_t)1 << 46) / ld || nseq > kMaxGrid / ((int64_t)d->Hv * 16) ||
       d->slots > ((int64_t)1 << 46) / ((int64_t)d->Hv * d->Dk * d->Dv))
     return fail(Q1_ERR_UNSUPPORTED, "call too large");
@@ -132,8 +133,13 @@ size_t q1_delta_prefill_workspace_bytes(const q1_delta* d, int64_t tokens, int64
     fail(Q1_ERR_INVALID_ARG, "tokens and nseq must be >= 0");
     return 0;
   }
+  if (tokens >= (int64_t)1 << 31 || nseq >= (int64_t)1 << 31) {
+    fail(Q1_ERR_UNSUPPORTED, "call too large");
+    return 0;
+  }
   ok();
-  return 0;
+  if (tokens == 0 || nseq == 0) return 0;
+  return (size_t)delta_chunk_slots(tokens, nseq) * d->Hv * kDeltaChunkBytes;
 }
 
 q1_status q1_delta_prefill(const q1_delta* d, int64_t tokens, int64_t nseq, const int32_t* cu_seqlens, void* workspace,
@@ -143,6 +149,7 @@ q1_status q1_delta_prefill(const q1_delta* d, int64_t tokens, int64_t nseq, cons
   if (tokens < 0 || nseq < 0) return fail(Q1_ERR_INVALID_ARG, "tokens and nseq must be >= 0");
   if (tokens == 0 || nseq == 0) return ok();
   st = check_delta(d, tokens, nseq);
+  if (st == Q1_OK && delta_chunk_slots(tokens, nseq) * d->Hv > kMaxGrid) st = fail(Q1_ERR_UNSUPPORTED, "call too large");
   if (st != Q1_OK) return st;
   if (cu_seqlens == nullptr || !aligned(cu_seqlens, 4))
     return fail(Q1_ERR_INVALID_ARG, "cu_seqlens must be a 4-byte aligned device pointer");
@@ -156,7 +163,8 @@ q1_status q1_delta_prefill(const q1_delta* d, int64_t tokens, int64_t nseq, cons
   a.cu = cu_seqlens;
   a.tokens = tokens;
   a.nseq = nseq;
-  return hip_status(launch_delta_recurrent(a, d->dtype == Q1_F16, d->Dk, static_cast<hipStream_t>(stream)),
+  return hip_status(launch_delta_chunk(a, d->dtype == Q1_F16, d->Dk, static_cast<unsigned char*>(workspace),
+                                       static_cast<hipStream_t>(stream)),
                     "delta prefill launch");
 }
 

@@ -1,0 +1,618 @@
+// Gated delta rule over whole prompts: chunks of 64 tokens on the matrix cores.
+//
+// With G_i the running sum of g in a chunk, D_ij = exp(G_i - G_j) (j <= i), S0 the
+// state before it and r_i, s_i the norms' reciprocals of k_i and q_i:
+//   A_ij = beta_i r_i r_j (k_i.k_j) D_ij (j < i),   T = (I + A)^-1 diag(beta)
+//   R = V - diag(r e^G) K S0,   V' = T R
+//   O = scale (diag(s e^G) Q S0 + P V'),   P_ij = s_i r_j (q_i.k_j) D_ij (j <= i)
+//   S1 = e^{G_63} S0 + K^T diag(r e^{G_63 - G}) V'
+// T, P and the factors need no state: q1_chunk_prep makes them for all chunks at
+// once.  q1_chunk_run then goes through a sequence's chunks with the state of 16
+// NS columns in registers (columns are independent).
+//
+// The state is held and returned in fp32 and nothing that reaches it may lose
+// that: an fp32 operand of a matrix-core product is taken as three bf16 parts
+// (8 significant bits each, exact), of which the products down to 2^-24 are
+// summed; k, q and v are exact (bf16, or two parts of an fp16 value).  What only
+// reaches the output (P, and S0 and V' as factors of it) has two parts, 2^-17.
+// G is summed in 64 bits, so that a difference of two sums is as exact as the
+// decays between them whatever came before; the inverse is made by substitution
+// and fp32 products.
+//
+// Operand layouts (16x16x32): lane l has row (or column) l % 16 and eight k
+// indices; a result lane has column l % 16, rows 4 (l / 16) .. +3.  Which k
+// indices a lane has is free as long as both operands agree, so two result
+// tiles (16 rows each) are the operand of the next product as they are: lane l
+// has k = 4 (l / 16) .. +3 of both.  The state, R and V' go from product to
+// product this way, through LDS only to reach the other waves.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "q1_decode.h"
+#include "q1_device.h"
+#include "q1_internal.h"
+
+namespace q1 {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef double f64x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int C = kDeltaChunk;
+
+// Workspace of one (chunk, value head): T and P in 10 tiles (it, jt <= it) of 64
+// lanes x 16 bytes -- T: row 16 it + l%16, columns 16 jt + 4(l/16) .. +3 in fp32;
+// P: the same elements as four high and four low parts -- then the factors.
+struct ChunkWs {
+  f32x4 T[10][64];
+  u32x4 P[10][64];
+  float in[C], out[C], read[C];  // r e^G, r e^{G63-G}, scale s e^G
+  float keep, pad[63];           // e^{G63}
+};
+static_assert(sizeof(ChunkWs) == kDeltaChunkBytes, "workspace of a chunk");
+
+constexpr int tile_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
+
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ f32x4 mma_in(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return mma(a, b, c);
+}
+
+__device__ __forceinline__ f32x4 mma4(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+
+// The upper halves of two words.
+__device__ __forceinline__ uint32_t tops(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+
+__device__ __forceinline__ float rest(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// The leading 8 significant bits of four floats as bf16; x becomes what is left.
+__device__ __forceinline__ u32x2 part(f32x4& x) {
+  const u32x2 r = {tops(__float_as_uint(x[0]), __float_as_uint(x[1])), tops(__float_as_uint(x[2]), __float_as_uint(x[3]))};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = rest(x[i]);
+  return r;
+}
+
+__device__ __forceinline__ void clamp_range(const DeltaArgs& a, int64_t s, int64_t* lo, int64_t* hi) {
+  const int64_t l = a.cu[s], h = a.cu[s + 1];
+  *lo = l < 0 ? 0 : l > a.tokens ? a.tokens : l;
+  *hi = h < 0 ? 0 : h > a.tokens ? a.tokens : h;
+}
+
+// Chunk c of sequence s is slot start/64 + s + c: one slot per chunk, no two the
+// same (sequences do not overlap), below tokens/64 + nseq + 1.
+__device__ __forceinline__ int64_t slot_base(int64_t start, int64_t s) { return start / C + s; }
+
+// Rows [0, n) of a strided operand: loads and stores past them are dropped (loads
+// give zeros), so that a chunk that ends early needs no branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int n, int64_t ld_bytes, int width_bytes) {
+  const int bytes = n > 0 ? (int)((n - 1) * ld_bytes) + width_bytes : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+}
+
+// Workgroups go to the XCDs in turn; each XCD gets a contiguous run of units.
+__device__ __forceinline__ int64_t xcd_unit(int64_t units) {
+  const int64_t per = (units + 7) / 8;
+  return (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+}
+
+constexpr int AS = 68;  // LDS row of A in floats
+
+// One wave per (chunk, value head).
+template <bool F16, int DK>
+__global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* ws, int64_t units) {
+  constexpr int KS = DK / 32;
+  __shared__ __align__(16) float A[C * AS];
+  __shared__ __align__(16) double Gs[C];
+  __shared__ __align__(16) float rks[C], rqs[C], bs[C];
+  const int64_t unit = xcd_unit(units);
+  if (unit >= units) return;
+  const int64_t slot = unit / a.Hv;
+  const int h = (int)(unit - slot * a.Hv), hk = h / (a.Hv / a.Hk);
+  int64_t s0 = 0, s1 = a.nseq;  // the last sequence whose first slot is not past this one
+  while (s1 - s0 > 1) {
+    const int64_t m = (s0 + s1) / 2;
+    int64_t lo, hi;
+    clamp_range(a, m, &lo, &hi);
+    if (slot_base(lo, m) <= slot) s0 = m;
+    else s1 = m;
+  }
+  int64_t lo, hi;
+  clamp_range(a, s0, &lo, &hi);
+  const int64_t c = slot - slot_base(lo, s0);
+  const int64_t t0 = lo + c * C;
+  if (c < 0 || t0 >= hi) return;
+  const int n = hi - t0 < C ? (int)(hi - t0) : C;
+  const int lane = threadIdx.x, col = lane & 15, grp = lane >> 4;
+  ChunkWs* w = ws + unit;
+
+  u32x4 K[4][KS], Q[4][KS];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = 16 * t + col;
+    const uint16_t* kp = a.k + (t0 + r) * a.k_ld + hk * DK + 8 * grp;
+    const uint16_t* qp = a.q + (t0 + r) * a.q_ld + hk * DK + 8 * grp;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      K[t][s] = r < n ? *reinterpret_cast<const u32x4*>(kp + 32 * s) : u32x4{0u, 0u, 0u, 0u};
+      Q[t][s] = r < n ? *reinterpret_cast<const u32x4*>(qp + 32 * s) : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+  // lane = token: decay sums (in units of log2), write strengths
+  const bool in = lane < n;
+  float gv = in ? a.g[(t0 + lane) * a.Hv + h] : 0.f;
+  gv = gv < -1000.f ? -1000.f : gv;  // exp is 0 there and below; a sum with -infinity in it would not be a number
+  double G = (double)gv * 1.4426950408889634074;
+  for (int off = 1; off < 64; off <<= 1) {
+    const double up = __shfl_up(G, off);
+    if (lane >= off) G += up;
+  }
+  const double G63 = __shfl(G, 63);
+  Gs[lane] = G;
+  const float beta = in ? a.beta[(t0 + lane) * a.Hv + h] : 0.f;
+  bs[lane] = beta;
+  if (a.l2norm) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qq = kk;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        kk = mma_in<F16>(K[t][s], K[t][s], kk);
+        qq = mma_in<F16>(Q[t][s], Q[t][s], qq);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col == 4 * grp + i) {
+          rks[16 * t + col] = 1.0f / sqrtf(kk[i] + 1e-6f);
+          rqs[16 * t + col] = 1.0f / sqrtf(qq[i] + 1e-6f);
+        }
+    }
+  } else {
+    rks[lane] = 1.f;
+    rqs[lane] = 1.f;
+  }
+  __syncthreads();
+  {
+    const float rk = rks[lane], eG = __builtin_amdgcn_exp2f((float)G);
+    w->in[lane] = rk * eG;
+    w->out[lane] = rk * __builtin_amdgcn_exp2f((float)(G63 - G));
+    w->read[lane] = a.scale * rqs[lane] * eG;
+    if (lane == 0) w->keep = __builtin_amdgcn_exp2f((float)G63);
+  }
+
+  // A (rows i = l % 16, columns j = 4 (l / 16) .. +3 of a tile) to LDS, P to the workspace
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int i = 16 * it + col;
+    const double Gi = Gs[i];
+    const float bi = bs[i] * rks[i], qi = a.scale * rqs[i];
+#pragma unroll
+    for (int jt = 0; jt <= it; ++jt) {
+      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        kk = mma_in<F16>(K[jt][s], K[it][s], kk);
+        qk = mma_in<F16>(K[jt][s], Q[it][s], qk);
+      }
+      const int j0 = 16 * jt + 4 * grp;
+      const f32x4 rj = *reinterpret_cast<const f32x4*>(&rks[j0]);
+      const f64x2 Ga = *reinterpret_cast<const f64x2*>(&Gs[j0]), Gb = *reinterpret_cast<const f64x2*>(&Gs[j0 + 2]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const double Gj = e < 2 ? Ga[e & 1] : Gb[e & 1];
+        const float d = rj[e] * __builtin_amdgcn_exp2f((float)(Gi - Gj));
+        kk[e] = i > j0 + e ? bi * kk[e] * d : 0.f;
+        qk[e] = i >= j0 + e ? qi * qk[e] * d : 0.f;
+      }
+      *reinterpret_cast<f32x4*>(&A[i * AS + j0]) = kk;
+      const u32x2 ph = part(qk), pl = part(qk);
+      w->P[tile_of(it, jt)][lane] = u32x4{ph[0], ph[1], pl[0], pl[1]};
+    }
+  }
+  __syncthreads();
+
+  // Inverse of I + A in place.  The four diagonal blocks by substitution, a block
+  // per 16 lanes, a column per lane ...
+  {
+    float x[16];
+    const float* Ab = &A[(16 * grp) * AS + 16 * grp];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0v = 0.f, s1v = 0.f;
+#pragma unroll
+      for (int k = 0; k < i; k += 4) {
+        const f32x4 r = *reinterpret_cast<const f32x4*>(Ab + i * AS + k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (k + e < i) {
+            if (e & 1) s1v = __builtin_fmaf(r[e], x[k + e], s1v);
+            else s0v = __builtin_fmaf(r[e], x[k + e], s0v);
+          }
+      }
+      x[i] = (i == col ? 1.f : 0.f) - (s0v + s1v);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) A[(16 * grp + i) * AS + 16 * grp + col] = x[i];
+  }
+  __syncthreads();
+  // ... then, with I, J the blocks of the lower and upper half: T_IJ = -T_II' A_I'J' T_J'J,
+  // first for halves of 16 rows, then of 32.
+  auto row4 = [&](int I, int J) { return *reinterpret_cast<const f32x4*>(&A[(16 * I + col) * AS + 16 * J + 4 * grp]); };
+  auto col4 = [&](int I, int J) {
+    f32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = A[(16 * I + 4 * grp + e) * AS + 16 * J + col];
+    return r;
+  };
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  {
+    const f32x4 y0 = mma4(row4(1, 0), col4(0, 0), zero), y1 = mma4(row4(3, 2), col4(2, 2), zero);
+    const f32x4 x0 = mma4(y0, row4(1, 1), zero), x1 = mma4(y1, row4(3, 3), zero);
+    __syncthreads();
+    *reinterpret_cast<f32x4*>(&A[(16 + col) * AS + 4 * grp]) = -x0;
+    *reinterpret_cast<f32x4*>(&A[(48 + col) * AS + 32 + 4 * grp]) = -x1;
+  }
+  __syncthreads();
+  {
+    f32x4 y[2][2];  // rows 2, 3 x columns 0, 1 of A times the upper half's inverse
+#pragma unroll
+    for (int I = 0; I < 2; ++I)
+#pragma unroll
+      for (int J = 0; J < 2; ++J) {
+        y[I][J] = mma4(row4(2 + I, 1), col4(1, J), zero);
+        if (J == 0) y[I][J] = mma4(row4(2 + I, 0), col4(0, 0), y[I][J]);
+      }
+    f32x4 x[2][2];
+#pragma unroll
+    for (int J = 0; J < 2; ++J) {
+      x[0][J] = mma4(y[0][J], row4(2, 2), zero);
+      x[1][J] = mma4(y[1][J], row4(3, 3), mma4(y[0][J], row4(3, 2), zero));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int I = 0; I < 2; ++I)
+#pragma unroll
+      for (int J = 0; J < 2; ++J) *reinterpret_cast<f32x4*>(&A[(32 + 16 * I + col) * AS + 16 * J + 4 * grp]) = -x[I][J];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int jt = 0; jt <= it; ++jt)
+      w->T[tile_of(it, jt)][lane] = row4(it, jt) * *reinterpret_cast<const f32x4*>(&bs[16 * jt + 4 * grp]);
+}
+
+// One workgroup of 4 waves per (sequence, value head, 16 NS columns of the state).
+// Wave w has tokens 16 w .. +15 of a chunk, and rows w DK/4 .. of the state.
+template <bool F16, int DK, int NS>
+__global__ __launch_bounds__(256) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t units) {
+  constexpr int KS = DK / 32, KP = F16 ? 2 : 1, ST = DK / 64;  // k steps, parts of k and q, state tiles per wave
+  constexpr int KROW = 2 * DK + 32, CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
+  __shared__ __align__(16) unsigned char kt[2][KP][C * KROW];
+  __shared__ __align__(16) u32x4 Ss[KS][3][NS][64], Rs[2][3][NS][64], Ws[2][3][NS][64], Vs[2][2][NS][64];
+  const int64_t unit = xcd_unit(units);
+  if (unit >= units) return;
+  const int slices = a.Dv / (16 * NS);
+  const int64_t sh = unit / slices;
+  const int64_t seq = sh / a.Hv;
+  const int h = (int)(sh - seq * a.Hv), hk = h / (a.Hv / a.Hk);
+  const int c0 = (int)(unit - sh * slices) * 16 * NS;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
+  // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t lo, hi;
+  clamp_range(a, seq, &lo, &hi);
+  if (lo >= hi) return;
+  const int64_t slot = a.slot_ids ? a.slot_ids[seq] : seq;
+  const int esz = a.out_dtype == F32 ? 4 : 2;
+  unsigned char* ob = static_cast<unsigned char*>(a.out);
+  if (slot < 0 || slot >= a.slots) {  // no state: zeros
+    for (int64_t t = lo + wave * 16 + col; t < hi; t += 64)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        unsigned char* o = ob + ((t * a.Hv + h) * a.Dv + c0 + 16 * n + 4 * grp) * esz;
+        if (esz == 4) *reinterpret_cast<u32x4*>(o) = u32x4{0u, 0u, 0u, 0u};
+        else *reinterpret_cast<u32x2*>(o) = u32x2{0u, 0u};
+      }
+    return;
+  }
+  const ChunkWs* w = ws + slot_base(lo, seq) * a.Hv + h;
+
+  // state: tile t of this wave is rows 16 (ST wave + t) + 4 grp .. +3, column col
+  f32x4 S[ST][NS];
+  float* sp = a.state + ((slot * a.Hv + h) * DK + 16 * ST * wave + 4 * grp) * (int64_t)a.Dv + c0 + col;
+#pragma unroll
+  for (int t = 0; t < ST; ++t)
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][n][e] = sp[(int64_t)(16 * t + e) * a.Dv + 16 * n];
+  auto put_state = [&]() {
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const int tile = ST * wave + t;
+        f32x4 x = S[t][n];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Ss[tile >> 1][p][n][lane])[tile & 1] = part(x);
+      }
+  };
+
+  u32x4 Kn[NL], P[4];
+  u32x2 Q[KS][2];
+  f32x4 T[4], in, outf;
+  uint16_t V[NS][4];
+  float read, keep;
+  const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
+  const int q_off = (16 * wave + col) * (int)a.q_ld * 2 + 8 * grp;
+  const int v_off = (16 * wave + 4 * grp) * (int)a.v_ld * 2 + 2 * (c0 + col);
+  auto left = [&](int64_t t0) { return hi - t0 < C ? (int)(hi - t0) : C; };
+  auto load_k = [&](int64_t t0) {
+    const auto r = rows_of(a.k + t0 * a.k_ld + hk * DK, left(t0), a.k_ld * 2, 2 * DK);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) Kn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off + i * k_step, 0, 0);
+  };
+  // two bf16 parts of an fp16 pair (11 bits: exact)
+  auto halves = [](uint32_t w2, uint32_t* hi_, uint32_t* lo_) {
+    const float x = f16_bits_to_f32(w2 & 0xffffu), y = f16_bits_to_f32(w2 >> 16);
+    *hi_ = tops(__float_as_uint(x), __float_as_uint(y));
+    *lo_ = tops(__float_as_uint(rest(x)), __float_as_uint(rest(y)));
+  };
+  auto put_k = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = (i * 256 + tid) / CH, x = (i * 256 + tid) % CH;
+      if constexpr (F16) {
+        u32x4 p0, p1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t x0, x1;
+          halves(Kn[i][e], &x0, &x1);
+          p0[e] = x0;
+          p1[e] = x1;
+        }
+        *reinterpret_cast<u32x4*>(&kt[buf][0][r * KROW + 16 * x]) = p0;
+        *reinterpret_cast<u32x4*>(&kt[buf][KP - 1][r * KROW + 16 * x]) = p1;
+      } else {
+        *reinterpret_cast<u32x4*>(&kt[buf][0][r * KROW + 16 * x]) = Kn[i];
+      }
+    }
+  };
+  auto load_q = [&](int64_t t0) {
+    const auto r = rows_of(a.q + t0 * a.q_ld + hk * DK, left(t0), a.q_ld * 2, 2 * DK);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) Q[s][x] = __builtin_amdgcn_raw_buffer_load_b64(r, q_off + 64 * s + 32 * x, 0, 0);
+  };
+  auto load_v = [&](int64_t t0, const ChunkWs* cw) {
+    const auto r = rows_of(a.v + t0 * a.v_ld + (int64_t)h * a.Dv, left(t0), a.v_ld * 2, 2 * a.Dv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+        V[n][e] = __builtin_amdgcn_raw_buffer_load_b16(r, v_off + e * (int)a.v_ld * 2 + 32 * n, 0, 0);
+    in = *reinterpret_cast<const f32x4*>(&cw->in[16 * wave + 4 * grp]);
+  };
+  auto load_t = [&](const ChunkWs* cw) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      T[j] = j <= wave ? cw->T[wave * (wave + 1) / 2 + j][lane] : f32x4{0.f, 0.f, 0.f, 0.f};
+    outf = *reinterpret_cast<const f32x4*>(&cw->out[16 * wave + 4 * grp]);
+    keep = cw->keep;
+  };
+  auto load_p = [&](const ChunkWs* cw) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) P[j] = j <= wave ? cw->P[wave * (wave + 1) / 2 + j][lane] : u32x4{0u, 0u, 0u, 0u};
+    read = cw->read[16 * wave + col];
+  };
+
+  load_k(lo);
+  load_q(lo);
+  load_v(lo, w);
+  load_t(w);
+  load_p(w);
+  put_state();
+  put_k(0);
+  __syncthreads();
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  int buf = 0;
+  for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
+    const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
+    load_k(t0 + C);
+    // K S0 and (Q S0)^T
+    f32x4 ks[NS], qs[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) ks[n] = qs[n] = zero;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      u32x4 kop[KP], qop[KP];
+#pragma unroll
+      for (int p = 0; p < KP; ++p) {
+        const unsigned char* kr = &kt[buf][p][(16 * wave + col) * KROW + 64 * s + 8 * grp];
+        const u32x2 x = *reinterpret_cast<const u32x2*>(kr), y = *reinterpret_cast<const u32x2*>(kr + 32);
+        kop[p] = u32x4{x[0], x[1], y[0], y[1]};
+      }
+      if constexpr (F16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t x0, x1;
+          halves(Q[s][e >> 1][e & 1], &x0, &x1);
+          qop[0][e] = x0;
+          qop[KP - 1][e] = x1;
+        }
+      } else {
+        qop[0] = u32x4{Q[s][0][0], Q[s][0][1], Q[s][1][0], Q[s][1][1]};
+      }
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const u32x4 s0 = Ss[s][0][n][lane], s1 = Ss[s][1][n][lane], s2 = Ss[s][2][n][lane];
+        ks[n] = mma(kop[0], s0, ks[n]);
+        qs[n] = mma(s0, qop[0], qs[n]);
+        ks[n] = mma(kop[0], s1, ks[n]);
+        qs[n] = mma(s1, qop[0], qs[n]);
+        ks[n] = mma(kop[0], s2, ks[n]);
+        if constexpr (F16) {
+          ks[n] = mma(kop[1], s0, ks[n]);
+          qs[n] = mma(s0, qop[1], qs[n]);
+          ks[n] = mma(kop[1], s1, ks[n]);
+        }
+      }
+    }
+    load_q(t0 + C);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      f32x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        r[e] = (F16 ? f16_bits_to_f32(V[n][e]) : bf16_bits_to_f32(V[n][e])) - in[e] * ks[n][e];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Rs[wave >> 1][p][n][lane])[wave & 1] = part(r);
+    }
+    load_v(t0 + C, wn);
+    u32x4 tp[2][3];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const u32x2 x = part(T[2 * k]), y = part(T[2 * k + 1]);
+        tp[k][p] = u32x4{x[0], x[1], y[0], y[1]};
+      }
+    __syncthreads();
+    // V' = T R
+    f32x4 vn[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) vn[n] = zero;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const u32x4 r0 = Rs[k][0][n][lane], r1 = Rs[k][1][n][lane], r2 = Rs[k][2][n][lane];
+        vn[n] = mma(tp[k][0], r2, vn[n]);
+        vn[n] = mma(tp[k][1], r1, vn[n]);
+        vn[n] = mma(tp[k][2], r0, vn[n]);
+        vn[n] = mma(tp[k][0], r1, vn[n]);
+        vn[n] = mma(tp[k][1], r0, vn[n]);
+        vn[n] = mma(tp[k][0], r0, vn[n]);
+      }
+    }
+    const float keep_now = keep;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      f32x4 x = outf * vn[n];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Ws[wave >> 1][p][n][lane])[wave & 1] = part(x);
+      x = vn[n];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) reinterpret_cast<u32x2*>(&Vs[wave >> 1][p][n][lane])[wave & 1] = part(x);
+    }
+    load_t(wn);
+    __syncthreads();
+    // S1 = e^{G63} S0 + K^T W
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+      for (int n = 0; n < NS; ++n) S[t][n] *= keep_now;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        u32x4 kop[KP];
+#pragma unroll
+        for (int p = 0; p < KP; ++p) {
+          const unsigned char* kr = &kt[buf][p][(32 * k + 4 * grp + col / 4) * KROW + 32 * (ST * wave + t) + 8 * (col & 3)];
+          const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)kr);
+          const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(kr + 16 * KROW));
+          const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
+          kop[p] = u32x4{xw[0], xw[1], yw[0], yw[1]};
+        }
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const u32x4 w0 = Ws[k][0][n][lane], w1 = Ws[k][1][n][lane], w2 = Ws[k][2][n][lane];
+          S[t][n] = mma(kop[0], w2, S[t][n]);
+          S[t][n] = mma(kop[0], w1, S[t][n]);
+          S[t][n] = mma(kop[0], w0, S[t][n]);
+          if constexpr (F16) {
+            S[t][n] = mma(kop[1], w1, S[t][n]);
+            S[t][n] = mma(kop[1], w0, S[t][n]);
+          }
+        }
+      }
+    put_state();
+    put_k(buf ^ 1);
+    __syncthreads();
+    // O^T = scale s e^G (Q S0)^T + V'^T P^T; a lane has token 16 wave + col
+    const auto ores = rows_of(ob + (t0 * a.Hv + h) * a.Dv * esz, left(t0), (int64_t)a.Hv * a.Dv * esz, a.Dv * esz);
+    const int o_off = ((16 * wave + col) * a.Hv * a.Dv + c0 + 4 * grp) * esz;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      f32x4 o = read * qs[n];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const u32x4 ph = {P[2 * k][0], P[2 * k][1], P[2 * k + 1][0], P[2 * k + 1][1]};
+        const u32x4 pl = {P[2 * k][2], P[2 * k][3], P[2 * k + 1][2], P[2 * k + 1][3]};
+        const u32x4 v0 = Vs[k][0][n][lane], v1 = Vs[k][1][n][lane];
+        o = mma(v1, ph, o);
+        o = mma(v0, pl, o);
+        o = mma(v0, ph, o);
+      }
+      if (a.out_dtype == F32) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), ores, o_off + 16 * n * esz, 0, 0);
+      } else {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = a.out_dtype == BF16 ? f32_to_bf16_bits(o[e]) : f32_to_f16_bits(o[e]);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16}, ores, o_off + 16 * n * esz, 0, 0);
+      }
+    }
+    load_p(wn);
+    w = wn;
+  }
+#pragma unroll
+  for (int t = 0; t < ST; ++t)
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sp[(int64_t)(16 * t + e) * a.Dv + 16 * n] = S[t][n][e];
+}
+
+template <bool F16, int DK>
+hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
+  const int64_t prep = delta_chunk_slots(a.tokens, a.nseq) * a.Hv;
+  hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(64), 0, s, a, ws, prep);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t units = a.nseq * a.Hv * (a.Dv / 16);
+  hipLaunchKernelGGL((q1_chunk_run<F16, DK, 1>), dim3((unsigned)((units + 7) / 8 * 8)), dim3(256), 0, s, a, ws, units);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_chunk(const DeltaArgs& a, bool f16, int Dk, unsigned char* ws, hipStream_t s) {
+  ChunkWs* w = reinterpret_cast<ChunkWs*>(ws);
+  if (f16) return Dk == 128 ? launch_t<true, 128>(a, w, s) : launch_t<true, 64>(a, w, s);
+  return Dk == 128 ? launch_t<false, 128>(a, w, s) : launch_t<false, 64>(a, w, s);
+}
+
+}  // namespace q1
