@@ -7,8 +7,8 @@
 //   O = scale (diag(s e^G) Q S0 + P V'),   P_ij = s_i r_j (q_i.k_j) D_ij (j <= i)
 //   S1 = e^{G_63} S0 + K^T diag(r e^{G_63 - G}) V'
 // T, P and the factors need no state: q1_chunk_prep makes them for all chunks at
-// once.  q1_chunk_run then goes through a sequence's chunks with the state of 16
-// NS columns in registers (columns are independent).
+// once.  q1_chunk_run then goes through a sequence's chunks with the state of 32
+// columns in registers (columns are independent).
 //
 // The state is held and returned in fp32 and nothing that reaches it may lose
 // that: an fp32 operand of a matrix-core product is taken as three bf16 parts
@@ -42,23 +42,26 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef double f64x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int C = kDeltaChunk;
 
-// Workspace of one (chunk, value head): T and P in 10 tiles (it, jt <= it) of 64
-// lanes x 16 bytes -- T: row 16 it + l%16, columns 16 jt + 4(l/16) .. +3 in fp32;
-// P: the same elements as four high and four low parts -- then the factors.
+// Workspace of one (chunk, value head): T and P as operands -- for 16 rows it and
+// 32 columns k, lane l has row 16 it + l%16 and columns 32 k + 4(l/16) .. +3 and
+// 16 further; T in three parts, P in two -- then the factors.  Pairs (it, k) above
+// the diagonal are left out.
 struct ChunkWs {
-  f32x4 T[10][64];
-  u32x4 P[10][64];
+  u32x4 T[6][3][64];
+  u32x4 P[6][2][64];
   float in[C], out[C], read[C];  // r e^G, r e^{G63-G}, scale s e^G
   float keep, pad[63];           // e^{G63}
 };
 static_assert(sizeof(ChunkWs) == kDeltaChunkBytes, "workspace of a chunk");
 
-constexpr int tile_of(int it, int jt) { return it * (it + 1) / 2 + jt; }
+constexpr int pair_of(int it, int k) { return it < 2 ? it : 2 * it - 2 + k; }
 
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -204,6 +207,7 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
     const int i = 16 * it + col;
     const double Gi = Gs[i];
     const float bi = bs[i] * rks[i], qi = a.scale * rqs[i];
+    u32x2 ph[2], pl[2];
 #pragma unroll
     for (int jt = 0; jt <= it; ++jt) {
       f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
@@ -223,8 +227,13 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
         qk[e] = i >= j0 + e ? qi * qk[e] * d : 0.f;
       }
       *reinterpret_cast<f32x4*>(&A[i * AS + j0]) = kk;
-      const u32x2 ph = part(qk), pl = part(qk);
-      w->P[tile_of(it, jt)][lane] = u32x4{ph[0], ph[1], pl[0], pl[1]};
+      ph[jt & 1] = part(qk);
+      pl[jt & 1] = part(qk);
+      if (jt == it && !(jt & 1)) ph[1] = pl[1] = u32x2{0u, 0u};
+      if (jt == it || (jt & 1)) {
+        w->P[pair_of(it, jt >> 1)][0][lane] = u32x4{ph[0][0], ph[0][1], ph[1][0], ph[1][1]};
+        w->P[pair_of(it, jt >> 1)][1][lane] = u32x4{pl[0][0], pl[0][1], pl[1][0], pl[1][1]};
+      }
     }
   }
   __syncthreads();
@@ -297,303 +306,368 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
 #pragma unroll
   for (int it = 0; it < 4; ++it)
 #pragma unroll
-    for (int jt = 0; jt <= it; ++jt)
-      w->T[tile_of(it, jt)][lane] = row4(it, jt) * *reinterpret_cast<const f32x4*>(&bs[16 * jt + 4 * grp]);
+    for (int k = 0; 2 * k <= it; ++k) {
+      f32x4 x = row4(it, 2 * k) * *reinterpret_cast<const f32x4*>(&bs[32 * k + 4 * grp]);
+      f32x4 y = 2 * k + 1 <= it ? row4(it, 2 * k + 1) * *reinterpret_cast<const f32x4*>(&bs[32 * k + 16 + 4 * grp]) : zero;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const u32x2 xp = part(x), yp = part(y);
+        w->T[pair_of(it, k)][p][lane] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+      }
+    }
 }
 
-// One workgroup of 4 waves per (sequence, value head, 16 NS columns of the state).
-// Wave w has tokens 16 w .. +15 of a chunk, and rows w DK/4 .. of the state.
-template <bool F16, int DK, int NS>
-__global__ __launch_bounds__(256) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t units) {
-  constexpr int KS = DK / 32, KP = F16 ? 2 : 1, ST = DK / 64;  // k steps, parts of k and q, state tiles per wave
+// One workgroup of 8 waves per (sequence, value head, 32 columns of the state).
+// Waves 0..3 carry the state, waves 4..7 make the output; of each, wave (sl, hf) has
+// the 16 columns sl, the tokens 32 hf .. +31 of a chunk and (state) the rows
+// hf DK/2 .. of the state.  What a wave makes itself it uses from its registers;
+// LDS only carries the other half.  Loads are those of the next chunk, into the
+// registers that a product has just read.
+constexpr int kRunThreads = 512;
+
+template <bool F16, int DK, bool OUT32>
+__global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t units) {
+  constexpr int KS = DK / 32, HS = KS / 2, KP = F16 ? 2 : 1, ST = DK / 32;  // k steps (a half), parts of k and q, state tiles
   constexpr int KROW = 2 * DK + 32, CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
   __shared__ __align__(16) unsigned char kt[2][KP][C * KROW];
-  __shared__ __align__(16) u32x4 Ss[KS][3][NS][64], Rs[2][3][NS][64], Ws[2][3][NS][64], Vs[2][2][NS][64];
+  __shared__ __align__(16) unsigned char qt[C * KROW];
+  __shared__ __align__(16) u32x4 Ss[2][KS][3][64], Rs[2][3][64], Ws[2][2][3][64];
+  __shared__ __align__(16) f32x4 Vs[2][4][64];
   const int64_t unit = xcd_unit(units);
   if (unit >= units) return;
-  const int slices = a.Dv / (16 * NS);
+  const int slices = (a.Dv + 31) / 32;
   const int64_t sh = unit / slices;
   const int64_t seq = sh / a.Hv;
   const int h = (int)(sh - seq * a.Hv), hk = h / (a.Hv / a.Hk);
-  const int c0 = (int)(unit - sh * slices) * 16 * NS;
-  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sl = (wave >> 1) & 1, hf = wave & 1;
+  const int c0 = (int)(unit - sh * slices) * 32 + 16 * sl;
+  const bool live = c0 < a.Dv;  // Dv may end with the first 16 columns
   int64_t lo, hi;
   clamp_range(a, seq, &lo, &hi);
   if (lo >= hi) return;
   const int64_t slot = a.slot_ids ? a.slot_ids[seq] : seq;
-  const int esz = a.out_dtype == F32 ? 4 : 2;
-  unsigned char* ob = static_cast<unsigned char*>(a.out);
+  constexpr int esz = OUT32 ? 4 : 2;
+  unsigned char* ob = static_cast<unsigned char*>(a.out) + (int64_t)h * a.Dv * esz;
+  const int64_t o_ld = (int64_t)a.Hv * a.Dv * esz;
+  constexpr int kNone = 1 << 30;  // an offset past every range
   if (slot < 0 || slot >= a.slots) {  // no state: zeros
-    for (int64_t t = lo + wave * 16 + col; t < hi; t += 64)
+    for (int64_t t = lo + (threadIdx.x >> 2); t < hi; t += kRunThreads / 4) {
+      const int c = (c0 & ~31) + 8 * (threadIdx.x & 3);
+      if (c < a.Dv)
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        unsigned char* o = ob + ((t * a.Hv + h) * a.Dv + c0 + 16 * n + 4 * grp) * esz;
-        if (esz == 4) *reinterpret_cast<u32x4*>(o) = u32x4{0u, 0u, 0u, 0u};
-        else *reinterpret_cast<u32x2*>(o) = u32x2{0u, 0u};
-      }
+        for (int e = 0; e < 8 * esz / 16; ++e)
+          *reinterpret_cast<u32x4*>(ob + t * o_ld + c * esz + 16 * e) = u32x4{0u, 0u, 0u, 0u};
+    }
     return;
   }
   const ChunkWs* w = ws + slot_base(lo, seq) * a.Hv + h;
-
-  // state: tile t of this wave is rows 16 (ST wave + t) + 4 grp .. +3, column col
-  f32x4 S[ST][NS];
-  float* sp = a.state + ((slot * a.Hv + h) * DK + 16 * ST * wave + 4 * grp) * (int64_t)a.Dv + c0 + col;
-#pragma unroll
-  for (int t = 0; t < ST; ++t)
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][n][e] = sp[(int64_t)(16 * t + e) * a.Dv + 16 * n];
-  auto put_state = [&]() {
-#pragma unroll
-    for (int t = 0; t < ST; ++t)
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const int tile = ST * wave + t;
-        f32x4 x = S[t][n];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Ss[tile >> 1][p][n][lane])[tile & 1] = part(x);
-      }
-  };
-
-  u32x4 Kn[NL], P[4];
-  u32x2 Q[KS][2];
-  f32x4 T[4], in, outf;
-  uint16_t V[NS][4];
-  float read, keep;
-  const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
-  const int q_off = (16 * wave + col) * (int)a.q_ld * 2 + 8 * grp;
-  const int v_off = (16 * wave + 4 * grp) * (int)a.v_ld * 2 + 2 * (c0 + col);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   auto left = [&](int64_t t0) { return hi - t0 < C ? (int)(hi - t0) : C; };
-  auto load_k = [&](int64_t t0) {
-    const auto r = rows_of(a.k + t0 * a.k_ld + hk * DK, left(t0), a.k_ld * 2, 2 * DK);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) Kn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off + i * k_step, 0, 0);
-  };
-  // two bf16 parts of an fp16 pair (11 bits: exact)
+  // k's fp16 pairs as two bf16 parts (11 bits: exact)
   auto halves = [](uint32_t w2, uint32_t* hi_, uint32_t* lo_) {
     const float x = f16_bits_to_f32(w2 & 0xffffu), y = f16_bits_to_f32(w2 >> 16);
     *hi_ = tops(__float_as_uint(x), __float_as_uint(y));
     *lo_ = tops(__float_as_uint(rest(x)), __float_as_uint(rest(y)));
   };
-  auto put_k = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int r = (i * 256 + tid) / CH, x = (i * 256 + tid) % CH;
-      if constexpr (F16) {
-        u32x4 p0, p1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t x0, x1;
-          halves(Kn[i][e], &x0, &x1);
-          p0[e] = x0;
-          p1[e] = x1;
-        }
-        *reinterpret_cast<u32x4*>(&kt[buf][0][r * KROW + 16 * x]) = p0;
-        *reinterpret_cast<u32x4*>(&kt[buf][KP - 1][r * KROW + 16 * x]) = p1;
-      } else {
-        *reinterpret_cast<u32x4*>(&kt[buf][0][r * KROW + 16 * x]) = Kn[i];
-      }
-    }
-  };
-  auto load_q = [&](int64_t t0) {
-    const auto r = rows_of(a.q + t0 * a.q_ld + hk * DK, left(t0), a.q_ld * 2, 2 * DK);
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) Q[s][x] = __builtin_amdgcn_raw_buffer_load_b64(r, q_off + 64 * s + 32 * x, 0, 0);
-  };
-  auto load_v = [&](int64_t t0, const ChunkWs* cw) {
-    const auto r = rows_of(a.v + t0 * a.v_ld + (int64_t)h * a.Dv, left(t0), a.v_ld * 2, 2 * a.Dv);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-        V[n][e] = __builtin_amdgcn_raw_buffer_load_b16(r, v_off + e * (int)a.v_ld * 2 + 32 * n, 0, 0);
-    in = *reinterpret_cast<const f32x4*>(&cw->in[16 * wave + 4 * grp]);
-  };
-  auto load_t = [&](const ChunkWs* cw) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      T[j] = j <= wave ? cw->T[wave * (wave + 1) / 2 + j][lane] : f32x4{0.f, 0.f, 0.f, 0.f};
-    outf = *reinterpret_cast<const f32x4*>(&cw->out[16 * wave + 4 * grp]);
-    keep = cw->keep;
-  };
-  auto load_p = [&](const ChunkWs* cw) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) P[j] = j <= wave ? cw->P[wave * (wave + 1) / 2 + j][lane] : u32x4{0u, 0u, 0u, 0u};
-    read = cw->read[16 * wave + col];
-  };
 
-  load_k(lo);
-  load_q(lo);
-  load_v(lo, w);
-  load_t(w);
-  load_p(w);
-  put_state();
-  put_k(0);
-  __syncthreads();
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  int buf = 0;
-  for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
-    const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
-    load_k(t0 + C);
-    // K S0 and (Q S0)^T
-    f32x4 ks[NS], qs[NS];
-#pragma unroll
-    for (int n = 0; n < NS; ++n) ks[n] = qs[n] = zero;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 kop[KP], qop[KP];
-#pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        const unsigned char* kr = &kt[buf][p][(16 * wave + col) * KROW + 64 * s + 8 * grp];
-        const u32x2 x = *reinterpret_cast<const u32x2*>(kr), y = *reinterpret_cast<const u32x2*>(kr + 32);
-        kop[p] = u32x4{x[0], x[1], y[0], y[1]};
-      }
-      if constexpr (F16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t x0, x1;
-          halves(Q[s][e >> 1][e & 1], &x0, &x1);
-          qop[0][e] = x0;
-          qop[KP - 1][e] = x1;
-        }
-      } else {
-        qop[0] = u32x4{Q[s][0][0], Q[s][0][1], Q[s][1][0], Q[s][1][1]};
-      }
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const u32x4 s0 = Ss[s][0][n][lane], s1 = Ss[s][1][n][lane], s2 = Ss[s][2][n][lane];
-        ks[n] = mma(kop[0], s0, ks[n]);
-        qs[n] = mma(s0, qop[0], qs[n]);
-        ks[n] = mma(kop[0], s1, ks[n]);
-        qs[n] = mma(s1, qop[0], qs[n]);
-        ks[n] = mma(kop[0], s2, ks[n]);
-        if constexpr (F16) {
-          ks[n] = mma(kop[1], s0, ks[n]);
-          qs[n] = mma(s0, qop[1], qs[n]);
-          ks[n] = mma(kop[1], s1, ks[n]);
-        }
-      }
-    }
-    load_q(t0 + C);
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      f32x4 r;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        r[e] = (F16 ? f16_bits_to_f32(V[n][e]) : bf16_bits_to_f32(V[n][e])) - in[e] * ks[n][e];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Rs[wave >> 1][p][n][lane])[wave & 1] = part(r);
-    }
-    load_v(t0 + C, wn);
-    u32x4 tp[2][3];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const u32x2 x = part(T[2 * k]), y = part(T[2 * k + 1]);
-        tp[k][p] = u32x4{x[0], x[1], y[0], y[1]};
-      }
-    __syncthreads();
-    // V' = T R
-    f32x4 vn[NS];
-#pragma unroll
-    for (int n = 0; n < NS; ++n) vn[n] = zero;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        const u32x4 r0 = Rs[k][0][n][lane], r1 = Rs[k][1][n][lane], r2 = Rs[k][2][n][lane];
-        vn[n] = mma(tp[k][0], r2, vn[n]);
-        vn[n] = mma(tp[k][1], r1, vn[n]);
-        vn[n] = mma(tp[k][2], r0, vn[n]);
-        vn[n] = mma(tp[k][0], r1, vn[n]);
-        vn[n] = mma(tp[k][1], r0, vn[n]);
-        vn[n] = mma(tp[k][0], r0, vn[n]);
-      }
-    }
-    const float keep_now = keep;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      f32x4 x = outf * vn[n];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&Ws[wave >> 1][p][n][lane])[wave & 1] = part(x);
-      x = vn[n];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) reinterpret_cast<u32x2*>(&Vs[wave >> 1][p][n][lane])[wave & 1] = part(x);
-    }
-    load_t(wn);
-    __syncthreads();
-    // S1 = e^{G63} S0 + K^T W
+  if (wave < 4) {
+    // ---- state ----
+    // tile t is rows hf DK/2 + 16 t + 4 grp .. +3, column col
+    f32x4 S[ST];
+    u32x4 Sp[HS][3];
+    float* sp = a.state + ((slot * a.Hv + h) * DK + hf * (DK / 2) + 4 * grp) * (int64_t)a.Dv + c0 + col;
 #pragma unroll
     for (int t = 0; t < ST; ++t)
 #pragma unroll
-      for (int n = 0; n < NS; ++n) S[t][n] *= keep_now;
+      for (int e = 0; e < 4; ++e) S[t][e] = live ? sp[(int64_t)(16 * t + e) * a.Dv] : 0.f;
+    auto put_state = [&]() {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+      for (int s = 0; s < HS; ++s) {
+        f32x4 x = S[2 * s], y = S[2 * s + 1];
 #pragma unroll
-      for (int t = 0; t < ST; ++t) {
-        u32x4 kop[KP];
-#pragma unroll
-        for (int p = 0; p < KP; ++p) {
-          const unsigned char* kr = &kt[buf][p][(32 * k + 4 * grp + col / 4) * KROW + 32 * (ST * wave + t) + 8 * (col & 3)];
-          const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)kr);
-          const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(kr + 16 * KROW));
-          const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
-          kop[p] = u32x4{xw[0], xw[1], yw[0], yw[1]};
+        for (int p = 0; p < 3; ++p) {
+          const u32x2 xp = part(x), yp = part(y);
+          Sp[s][p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+          Ss[sl][hf * HS + s][p][lane] = Sp[s][p];
         }
+      }
+    };
+    u32x4 T[2][2][3];  // rows 32 hf + 16 r, columns 32 hf (own), 0 (the other half; hf = 1)
+    f32x4 in[2], outf[2];
+    uint16_t V[2][4];
+    float keep;
+    const int v_off = live ? (32 * hf + 4 * grp) * (int)a.v_ld * 2 + 2 * (c0 + col) : kNone;
+    auto load_v = [&](int64_t t0, const ChunkWs* cw) {
+      const auto r = rows_of(a.v + t0 * a.v_ld + (int64_t)h * a.Dv, left(t0), a.v_ld * 2, 2 * a.Dv);
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-          const u32x4 w0 = Ws[k][0][n][lane], w1 = Ws[k][1][n][lane], w2 = Ws[k][2][n][lane];
-          S[t][n] = mma(kop[0], w2, S[t][n]);
-          S[t][n] = mma(kop[0], w1, S[t][n]);
-          S[t][n] = mma(kop[0], w0, S[t][n]);
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          V[i][e] = __builtin_amdgcn_raw_buffer_load_b16(r, v_off + (16 * i + e) * (int)a.v_ld * 2, 0, 0);
+        in[i] = *reinterpret_cast<const f32x4*>(&cw->in[32 * hf + 16 * i + 4 * grp]);
+      }
+    };
+    // own pairs: (0,0) (1,0) or (2,1) (3,1); the others: none or (2,0) (3,0)
+    const int t_own = (hf ? 3 : 0) * 3072 + 16 * lane, t_oth = hf ? 2 * 3072 + 16 * lane : kNone, t_step = hf ? 6144 : 3072;
+    auto load_t = [&](const ChunkWs* cw) {
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<u32x4*>(&cw->T[0][0][0]), (short)0, (int)sizeof(cw->T), 0x00020000);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          T[i][0][p] = __builtin_amdgcn_raw_buffer_load_b128(r, t_own + i * t_step + 1024 * p, 0, 0);
+          T[i][1][p] = __builtin_amdgcn_raw_buffer_load_b128(r, t_oth + i * t_step + 1024 * p, 0, 0);
+        }
+        outf[i] = *reinterpret_cast<const f32x4*>(&cw->out[32 * hf + 16 * i + 4 * grp]);
+      }
+      keep = cw->keep;
+    };
+    load_v(lo, w);
+    load_t(w);
+    put_state();
+    __syncthreads();
+    int buf = 0;
+    for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
+      const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
+      // K S0: this half's state from registers, the other's from LDS
+      f32x4 ks[2] = {zero, zero};
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int s = 0; s < HS; ++s) {
+          const int kk = (o ? 1 - hf : hf) * HS + s;
+          u32x4 sv[3];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) sv[p] = o ? Ss[sl][kk][p][lane] : Sp[s][p];
+          u32x4 kop[2][KP];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int p = 0; p < KP; ++p) {
+              const unsigned char* kr = &kt[buf][p][(32 * hf + 16 * i + col) * KROW + 64 * kk + 8 * grp];
+              const u32x2 x = *reinterpret_cast<const u32x2*>(kr), y = *reinterpret_cast<const u32x2*>(kr + 32);
+              kop[i][p] = u32x4{x[0], x[1], y[0], y[1]};
+            }
+#pragma unroll
+          for (int p = 2; p >= 0; --p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][0], sv[p], ks[i]);
           if constexpr (F16) {
-            S[t][n] = mma(kop[1], w1, S[t][n]);
-            S[t][n] = mma(kop[1], w0, S[t][n]);
+#pragma unroll
+            for (int p = 1; p >= 0; --p)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][KP - 1], sv[p], ks[i]);
+          }
+        }
+      f32x4 rr[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          rr[i][e] = (F16 ? f16_bits_to_f32(V[i][e]) : bf16_bits_to_f32(V[i][e])) - in[i][e] * ks[i][e];
+      load_v(t0 + C, wn);
+      u32x4 R[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const u32x2 x = part(rr[0]), y = part(rr[1]);
+        R[p] = u32x4{x[0], x[1], y[0], y[1]};
+        if (hf == 0) Rs[sl][p][lane] = R[p];
+      }
+      // V' = T R: the six products of parts down to 2^-24
+      f32x4 vn[2] = {zero, zero};
+      auto times = [&](int o, const u32x4* r) {
+#pragma unroll
+        for (int x = 2; x >= 0; --x)
+#pragma unroll
+          for (int p = 0; p <= x; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) vn[i] = mma(T[i][o][p], r[x - p], vn[i]);
+      };
+      times(0, R);
+      __syncthreads();
+      if (hf == 1) {
+        u32x4 r0[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) r0[p] = Rs[sl][p][lane];
+        times(1, r0);
+      }
+      u32x4 W[3];
+      {
+        f32x4 x = outf[0] * vn[0], y = outf[1] * vn[1];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const u32x2 xp = part(x), yp = part(y);
+          W[p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+          Ws[sl][hf][p][lane] = W[p];
+        }
+        Vs[sl][2 * hf][lane] = vn[0];
+        Vs[sl][2 * hf + 1][lane] = vn[1];
+      }
+#pragma unroll
+      for (int t = 0; t < ST; ++t) S[t] *= keep;
+      load_t(wn);
+      // S1 = e^{G63} S0 + K^T W
+      auto update = [&](int k, const u32x4* wv) {
+        u32x4 kop[ST][KP];
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+          for (int p = 0; p < KP; ++p) {
+            const unsigned char* kr = &kt[buf][p][(32 * k + 4 * grp + col / 4) * KROW + 32 * (hf * ST + t) + 8 * (col & 3)];
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)kr);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(kr + 16 * KROW));
+            const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
+            kop[t][p] = u32x4{xw[0], xw[1], yw[0], yw[1]};
+          }
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int t = 0; t < ST; ++t) S[t] = mma(kop[t][0], wv[p], S[t]);
+        if constexpr (F16) {
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int t = 0; t < ST; ++t) S[t] = mma(kop[t][KP - 1], wv[p], S[t]);
+        }
+      };
+      update(hf, W);
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < 3; ++p) W[p] = Ws[sl][1 - hf][p][lane];
+      update(1 - hf, W);
+      put_state();
+      __syncthreads();
+      w = wn;
+    }
+    if (live)
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sp[(int64_t)(16 * t + e) * a.Dv] = S[t][e];
+  } else {
+    // ---- output, and the next chunk's keys ----
+    const int tid = threadIdx.x & 255;
+    u32x4 Kn[NL], Qn[NL], P[2][2][2];
+    float read[2];
+    const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
+    const int q_off = (tid / CH) * (int)a.q_ld * 2 + 16 * (tid % CH), q_step = (256 / CH) * (int)a.q_ld * 2;
+    auto load_kq = [&](int64_t t0) {
+      const auto r = rows_of(a.k + t0 * a.k_ld + hk * DK, left(t0), a.k_ld * 2, 2 * DK);
+      const auto rq = rows_of(a.q + t0 * a.q_ld + hk * DK, left(t0), a.q_ld * 2, 2 * DK);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        Kn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off + i * k_step, 0, 0);
+        Qn[i] = __builtin_amdgcn_raw_buffer_load_b128(rq, q_off + i * q_step, 0, 0);
+      }
+    };
+    auto put_kq = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int at = ((i * 256 + tid) / CH) * KROW + 16 * (tid % CH);
+        *reinterpret_cast<u32x4*>(&qt[at]) = Qn[i];
+        if constexpr (F16) {
+          u32x4 p0, p1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t x0, x1;
+            halves(Kn[i][e], &x0, &x1);
+            p0[e] = x0;
+            p1[e] = x1;
+          }
+          *reinterpret_cast<u32x4*>(&kt[b][0][at]) = p0;
+          *reinterpret_cast<u32x4*>(&kt[b][KP - 1][at]) = p1;
+        } else {
+          *reinterpret_cast<u32x4*>(&kt[b][0][at]) = Kn[i];
+        }
+      }
+    };
+    // pairs (2 hf + i, k): 0 1 without k = 1, or 2 3, 4 5
+    const int p_off = (hf ? 2 : 0) * 2048 + 16 * lane, p_step = hf ? 4096 : 2048, p_k = hf ? 2048 : kNone;
+    auto load_p = [&](const ChunkWs* cw) {
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<u32x4*>(&cw->P[0][0][0]), (short)0, (int)sizeof(cw->P), 0x00020000);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            P[i][k][p] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off + i * p_step + k * p_k + 1024 * p, 0, 0);
+        read[i] = cw->read[32 * hf + 16 * i + col];
+      }
+    };
+    const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
+    load_kq(lo);
+    load_p(w);
+    put_kq(0);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
+      const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
+      load_kq(t0 + C);
+      // (Q S0)^T; a lane has token 32 hf + 16 i + col
+      f32x4 qs[2] = {zero, zero};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const u32x4 s0 = Ss[sl][s][0][lane], s1 = Ss[sl][s][1][lane];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const unsigned char* qr = &qt[(32 * hf + 16 * i + col) * KROW + 64 * s + 8 * grp];
+          const u32x2 x = *reinterpret_cast<const u32x2*>(qr), y = *reinterpret_cast<const u32x2*>(qr + 32);
+          const u32x4 q = {x[0], x[1], y[0], y[1]};
+          if constexpr (F16) {
+            u32x4 q0, q1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t h0, h1;
+              halves(q[e], &h0, &h1);
+              q0[e] = h0;
+              q1[e] = h1;
+            }
+            qs[i] = mma(s0, q1, qs[i]);
+            qs[i] = mma(s1, q0, qs[i]);
+            qs[i] = mma(s0, q0, qs[i]);
+          } else {
+            qs[i] = mma(s1, q, qs[i]);
+            qs[i] = mma(s0, q, qs[i]);
           }
         }
       }
-    put_state();
-    put_k(buf ^ 1);
-    __syncthreads();
-    // O^T = scale s e^G (Q S0)^T + V'^T P^T; a lane has token 16 wave + col
-    const auto ores = rows_of(ob + (t0 * a.Hv + h) * a.Dv * esz, left(t0), (int64_t)a.Hv * a.Dv * esz, a.Dv * esz);
-    const int o_off = ((16 * wave + col) * a.Hv * a.Dv + c0 + 4 * grp) * esz;
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      f32x4 o = read * qs[n];
+      __syncthreads();
+      __syncthreads();
+      // O^T = scale s e^G (Q S0)^T + V'^T P^T
+      f32x4 o[2] = {read[0] * qs[0], read[1] * qs[1]};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const u32x4 ph = {P[2 * k][0], P[2 * k][1], P[2 * k + 1][0], P[2 * k + 1][1]};
-        const u32x4 pl = {P[2 * k][2], P[2 * k][3], P[2 * k + 1][2], P[2 * k + 1][3]};
-        const u32x4 v0 = Vs[k][0][n][lane], v1 = Vs[k][1][n][lane];
-        o = mma(v1, ph, o);
-        o = mma(v0, pl, o);
-        o = mma(v0, ph, o);
-      }
-      if (a.out_dtype == F32) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), ores, o_off + 16 * n * esz, 0, 0);
-      } else {
-        uint32_t b[4];
+        f32x4 x = Vs[sl][2 * k][lane], y = Vs[sl][2 * k + 1][lane];
+        const u32x2 x0 = part(x), x1 = part(x), y0 = part(y), y1 = part(y);
+        const u32x4 v0 = {x0[0], x0[1], y0[0], y0[1]}, v1 = {x1[0], x1[1], y1[0], y1[1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = a.out_dtype == BF16 ? f32_to_bf16_bits(o[e]) : f32_to_f16_bits(o[e]);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16}, ores, o_off + 16 * n * esz, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+          o[i] = mma(v1, P[i][k][0], o[i]);
+          o[i] = mma(v0, P[i][k][1], o[i]);
+          o[i] = mma(v0, P[i][k][0], o[i]);
+        }
       }
+      load_p(wn);
+      put_kq(buf ^ 1);
+      const auto ores = rows_of(ob + t0 * o_ld, left(t0), o_ld, a.Dv * esz);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (OUT32) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), ores, o_off + 16 * i * (int)o_ld, 0, 0);
+        } else {
+          const u32x2 b16 = __builtin_bit_cast(u32x2, __builtin_convertvector(o[i], bf16x4));
+          const u32x2 h16 = __builtin_bit_cast(u32x2, __builtin_convertvector(o[i], f16x4));
+          __builtin_amdgcn_raw_buffer_store_b64(a.out_dtype == BF16 ? b16 : h16, ores, o_off + 16 * i * (int)o_ld, 0, 0);
+        }
+      }
+      __syncthreads();
+      w = wn;
     }
-    load_p(wn);
-    w = wn;
   }
-#pragma unroll
-  for (int t = 0; t < ST; ++t)
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sp[(int64_t)(16 * t + e) * a.Dv + 16 * n] = S[t][n][e];
 }
 
 template <bool F16, int DK>
@@ -602,8 +676,12 @@ hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
   hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(64), 0, s, a, ws, prep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t units = a.nseq * a.Hv * (a.Dv / 16);
-  hipLaunchKernelGGL((q1_chunk_run<F16, DK, 1>), dim3((unsigned)((units + 7) / 8 * 8)), dim3(256), 0, s, a, ws, units);
+  const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
+  const dim3 grid((unsigned)((units + 7) / 8 * 8));
+  if (a.out_dtype == F32)
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, true>), grid, dim3(kRunThreads), 0, s, a, ws, units);
+  else
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, false>), grid, dim3(kRunThreads), 0, s, a, ws, units);
   return hipGetLastError();
 }
 
