@@ -324,13 +324,13 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
 // LDS only carries the other half.  Loads are those of the next chunk, into the
 // registers that a product has just read.
 constexpr int kRunThreads = 512;
+constexpr int kVRow = 64 + 16;  // LDS bytes of a row of 32 values
 
 template <bool F16, int DK, bool OUT32>
 __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t units) {
   constexpr int KS = DK / 32, HS = KS / 2, KP = F16 ? 2 : 1, ST = DK / 32;  // k steps (a half), parts of k and q, state tiles
   constexpr int KROW = 2 * DK + 32, CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
-  __shared__ __align__(16) unsigned char kt[2][KP][C * KROW];
-  __shared__ __align__(16) unsigned char qt[C * KROW];
+  __shared__ __align__(16) unsigned char kt[2][KP][C * KROW], qt[C * KROW], vt[C * kVRow];
   __shared__ __align__(16) u32x4 Ss[2][KS][3][64], Rs[2][3][64], Ws[2][2][3][64];
   __shared__ __align__(16) f32x4 Vs[2][4][64];
   const int64_t unit = xcd_unit(units);
@@ -375,14 +375,15 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 
   if (wave < 4) {
     // ---- state ----
-    // tile t is rows hf DK/2 + 16 t + 4 grp .. +3, column col
+    // tile t is rows hf DK/2 + 32 (t/2) + 4 (t%2) + 8 grp .. +3, column col
     f32x4 S[ST];
     u32x4 Sp[HS][3];
-    float* sp = a.state + ((slot * a.Hv + h) * DK + hf * (DK / 2) + 4 * grp) * (int64_t)a.Dv + c0 + col;
+    float* sp = a.state + ((slot * a.Hv + h) * DK + hf * (DK / 2) + 8 * grp) * (int64_t)a.Dv + c0 + col;
+    auto row = [](int t, int e) { return 32 * (t >> 1) + 4 * (t & 1) + e; };
 #pragma unroll
     for (int t = 0; t < ST; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][e] = live ? sp[(int64_t)(16 * t + e) * a.Dv] : 0.f;
+      for (int e = 0; e < 4; ++e) S[t][e] = live ? sp[(int64_t)row(t, e) * a.Dv] : 0.f;
     auto put_state = [&]() {
 #pragma unroll
       for (int s = 0; s < HS; ++s) {
@@ -397,18 +398,10 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     };
     u32x4 T[2][2][3];  // rows 32 hf + 16 r, columns 32 hf (own), 0 (the other half; hf = 1)
     f32x4 in[2], outf[2];
-    uint16_t V[2][4];
     float keep;
-    const int v_off = live ? (32 * hf + 4 * grp) * (int)a.v_ld * 2 + 2 * (c0 + col) : kNone;
-    auto load_v = [&](int64_t t0, const ChunkWs* cw) {
-      const auto r = rows_of(a.v + t0 * a.v_ld + (int64_t)h * a.Dv, left(t0), a.v_ld * 2, 2 * a.Dv);
+    auto load_in = [&](const ChunkWs* cw) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          V[i][e] = __builtin_amdgcn_raw_buffer_load_b16(r, v_off + (16 * i + e) * (int)a.v_ld * 2, 0, 0);
-        in[i] = *reinterpret_cast<const f32x4*>(&cw->in[32 * hf + 16 * i + 4 * grp]);
-      }
+      for (int i = 0; i < 2; ++i) in[i] = *reinterpret_cast<const f32x4*>(&cw->in[32 * hf + 16 * i + 4 * grp]);
     };
     // own pairs: (0,0) (1,0) or (2,1) (3,1); the others: none or (2,0) (3,0)
     const int t_own = (hf ? 3 : 0) * 3072 + 16 * lane, t_oth = hf ? 2 * 3072 + 16 * lane : kNone, t_step = hf ? 6144 : 3072;
@@ -425,7 +418,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       }
       keep = cw->keep;
     };
-    load_v(lo, w);
+    load_in(w);
     load_t(w);
     put_state();
     __syncthreads();
@@ -446,11 +439,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int p = 0; p < KP; ++p) {
-              const unsigned char* kr = &kt[buf][p][(32 * hf + 16 * i + col) * KROW + 64 * kk + 8 * grp];
-              const u32x2 x = *reinterpret_cast<const u32x2*>(kr), y = *reinterpret_cast<const u32x2*>(kr + 32);
-              kop[i][p] = u32x4{x[0], x[1], y[0], y[1]};
-            }
+            for (int p = 0; p < KP; ++p)
+              kop[i][p] = *reinterpret_cast<const u32x4*>(&kt[buf][p][(32 * hf + 16 * i + col) * KROW + 64 * kk + 16 * grp]);
 #pragma unroll
           for (int p = 2; p >= 0; --p)
 #pragma unroll
@@ -464,11 +454,14 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         }
       f32x4 rr[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)&vt[(32 * hf + 16 * i + 4 * grp + col / 4) * kVRow + 32 * sl + 8 * (col & 3)]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          rr[i][e] = (F16 ? f16_bits_to_f32(V[i][e]) : bf16_bits_to_f32(V[i][e])) - in[i][e] * ks[i][e];
-      load_v(t0 + C, wn);
+          rr[i][e] = (F16 ? f16_bits_to_f32((uint16_t)v[e]) : bf16_bits_to_f32((uint16_t)v[e])) - in[i][e] * ks[i][e];
+      }
+      load_in(wn);
       u32x4 R[3];
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
@@ -516,7 +509,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         for (int t = 0; t < ST; ++t)
 #pragma unroll
           for (int p = 0; p < KP; ++p) {
-            const unsigned char* kr = &kt[buf][p][(32 * k + 4 * grp + col / 4) * KROW + 32 * (hf * ST + t) + 8 * (col & 3)];
+            const unsigned char* kr = &kt[buf][p][(32 * k + 4 * grp + col / 4) * KROW + DK * hf + 64 * (t >> 1) + 8 * (t & 1) + 16 * (col & 3)];
             const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)kr);
             const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(kr + 16 * KROW));
             const u32x2 xw = __builtin_bit_cast(u32x2, x), yw = __builtin_bit_cast(u32x2, y);
@@ -546,28 +539,38 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
       for (int t = 0; t < ST; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sp[(int64_t)(16 * t + e) * a.Dv] = S[t][e];
+        for (int e = 0; e < 4; ++e) sp[(int64_t)row(t, e) * a.Dv] = S[t][e];
   } else {
     // ---- output, and the next chunk's keys ----
     const int tid = threadIdx.x & 255;
-    u32x4 Kn[NL], Qn[NL], P[2][2][2];
+    u32x4 Kn[NL], Qn[NL], Vn, P[2][2][2];
     float read[2];
     const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
     const int q_off = (tid / CH) * (int)a.q_ld * 2 + 16 * (tid % CH), q_step = (256 / CH) * (int)a.q_ld * 2;
-    auto load_kq = [&](int64_t t0) {
+    const int vc = (c0 & ~31) + 8 * (tid & 3);
+    const int v_off = vc < a.Dv ? (tid >> 2) * (int)a.v_ld * 2 + 2 * vc : kNone;
+    auto load_k = [&](int64_t t0) {
       const auto r = rows_of(a.k + t0 * a.k_ld + hk * DK, left(t0), a.k_ld * 2, 2 * DK);
-      const auto rq = rows_of(a.q + t0 * a.q_ld + hk * DK, left(t0), a.q_ld * 2, 2 * DK);
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        Kn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off + i * k_step, 0, 0);
-        Qn[i] = __builtin_amdgcn_raw_buffer_load_b128(rq, q_off + i * q_step, 0, 0);
-      }
+      for (int i = 0; i < NL; ++i) Kn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, k_off + i * k_step, 0, 0);
+      const auto rv = rows_of(a.v + t0 * a.v_ld + (int64_t)h * a.Dv, left(t0), a.v_ld * 2, 2 * a.Dv);
+      Vn = __builtin_amdgcn_raw_buffer_load_b128(rv, v_off, 0, 0);
     };
-    auto put_kq = [&](int b) {
+    auto load_q = [&](int64_t t0) {
+      const auto r = rows_of(a.q + t0 * a.q_ld + hk * DK, left(t0), a.q_ld * 2, 2 * DK);
+#pragma unroll
+      for (int i = 0; i < NL; ++i) Qn[i] = __builtin_amdgcn_raw_buffer_load_b128(r, q_off + i * q_step, 0, 0);
+    };
+    auto put_q = [&]() {
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        *reinterpret_cast<u32x4*>(&qt[((i * 256 + tid) / CH) * KROW + 16 * (tid % CH)]) = Qn[i];
+    };
+    auto put_kv = [&](int b) {
+      *reinterpret_cast<u32x4*>(&vt[(tid >> 2) * kVRow + 16 * (tid & 3)]) = Vn;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int at = ((i * 256 + tid) / CH) * KROW + 16 * (tid % CH);
-        *reinterpret_cast<u32x4*>(&qt[at]) = Qn[i];
         if constexpr (F16) {
           u32x4 p0, p1;
 #pragma unroll
@@ -599,45 +602,9 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       }
     };
     const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
-    load_kq(lo);
-    load_p(w);
-    put_kq(0);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
-      const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
-      load_kq(t0 + C);
-      // (Q S0)^T; a lane has token 32 hf + 16 i + col
-      f32x4 qs[2] = {zero, zero};
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const u32x4 s0 = Ss[sl][s][0][lane], s1 = Ss[sl][s][1][lane];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const unsigned char* qr = &qt[(32 * hf + 16 * i + col) * KROW + 64 * s + 8 * grp];
-          const u32x2 x = *reinterpret_cast<const u32x2*>(qr), y = *reinterpret_cast<const u32x2*>(qr + 32);
-          const u32x4 q = {x[0], x[1], y[0], y[1]};
-          if constexpr (F16) {
-            u32x4 q0, q1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t h0, h1;
-              halves(q[e], &h0, &h1);
-              q0[e] = h0;
-              q1[e] = h1;
-            }
-            qs[i] = mma(s0, q1, qs[i]);
-            qs[i] = mma(s1, q0, qs[i]);
-            qs[i] = mma(s0, q0, qs[i]);
-          } else {
-            qs[i] = mma(s1, q, qs[i]);
-            qs[i] = mma(s0, q, qs[i]);
-          }
-        }
-      }
-      __syncthreads();
-      __syncthreads();
-      // O^T = scale s e^G (Q S0)^T + V'^T P^T
+    f32x4 qs[2] = {zero, zero};
+    // O^T = scale s e^G (Q S0)^T + V'^T P^T of the chunk at t; a lane has token 32 hf + 16 i + col
+    auto finish = [&](int64_t t, int n) {
       f32x4 o[2] = {read[0] * qs[0], read[1] * qs[1]};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -645,15 +612,13 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         const u32x2 x0 = part(x), x1 = part(x), y0 = part(y), y1 = part(y);
         const u32x4 v0 = {x0[0], x0[1], y0[0], y0[1]}, v1 = {x1[0], x1[1], y1[0], y1[1]};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          o[i] = mma(v1, P[i][k][0], o[i]);
-          o[i] = mma(v0, P[i][k][1], o[i]);
-          o[i] = mma(v0, P[i][k][0], o[i]);
-        }
+        for (int i = 0; i < 2; ++i) o[i] = mma(v1, P[i][k][0], o[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = mma(v0, P[i][k][1], o[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = mma(v0, P[i][k][0], o[i]);
       }
-      load_p(wn);
-      put_kq(buf ^ 1);
-      const auto ores = rows_of(ob + t0 * o_ld, left(t0), o_ld, a.Dv * esz);
+      const auto ores = rows_of(ob + t * o_ld, n, o_ld, a.Dv * esz);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if constexpr (OUT32) {
@@ -664,9 +629,64 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
           __builtin_amdgcn_raw_buffer_store_b64(a.out_dtype == BF16 ? b16 : h16, ores, o_off + 16 * i * (int)o_ld, 0, 0);
         }
       }
+    };
+    load_k(lo);
+    load_q(lo);
+    load_p(w);
+    put_kv(0);
+    put_q();
+    load_k(lo + C);
+    load_q(lo + C);
+    __syncthreads();
+    int buf = 0, done = 0;  // rows of the chunk before that wait for finish(): none at first
+    for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
+      // while the state waves make R: the output of the chunk before
+      finish(t0 - done, done);
+      load_p(w);
+      done = C;
       __syncthreads();
-      w = wn;
+      // while they make V' and the new state: (Q S0)^T and the next keys
+      qs[0] = qs[1] = zero;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const u32x4 s0 = Ss[sl][s][0][lane], s1 = Ss[sl][s][1][lane];
+        u32x4 Q[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) Q[i] = *reinterpret_cast<const u32x4*>(&qt[(32 * hf + 16 * i + col) * KROW + 64 * s + 16 * grp]);
+        if constexpr (F16) {
+          u32x4 q0[2], q1[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t h0, h1;
+              halves(Q[i][e], &h0, &h1);
+              q0[i][e] = h0;
+              q1[i][e] = h1;
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qs[i] = mma(s0, q1[i], qs[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qs[i] = mma(s1, q0[i], qs[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qs[i] = mma(s0, q0[i], qs[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qs[i] = mma(s1, Q[i], qs[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qs[i] = mma(s0, Q[i], qs[i]);
+        }
+      }
+      put_kv(buf ^ 1);
+      load_k(t0 + 2 * C);
+      __syncthreads();
+      put_q();
+      load_q(t0 + 2 * C);
+      __syncthreads();
+      if (t0 + C < hi) w += a.Hv;
     }
+    const int64_t last = lo + (hi - lo - 1) / C * C;
+    finish(last, (int)(hi - last));
   }
 }
 
