@@ -49,7 +49,8 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int C = kDeltaChunk;
 
-// Workspace of one (chunk, value head): T and P as operands -- for 16 rows it and
+// Workspace of one (value head, chunk), a head's chunks one after another (the run
+// walks through them; a chunk's heads together cost it a new page every chunk): T and P as operands -- for 16 rows it and
 // 32 columns k, lane l has row 16 it + l%16 and columns 32 k + 4(l/16) .. +3 and
 // 16 further; T in three parts, P in two -- then the factors.  Pairs (it, k) above
 // the diagonal are left out.
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
   if (c < 0 || t0 >= hi) return;
   const int n = hi - t0 < C ? (int)(hi - t0) : C;
   const int lane = threadIdx.x, col = lane & 15, grp = lane >> 4;
-  ChunkWs* w = ws + unit;
+  ChunkWs* w = ws + (int64_t)h * (units / a.Hv) + slot;
 
   u32x4 K[4][KS], Q[4][KS];
 #pragma unroll
@@ -327,7 +328,7 @@ constexpr int kRunThreads = 512;
 constexpr int kVRow = 64 + 16;  // LDS bytes of a row of 32 values
 
 template <bool F16, int DK, bool OUT32>
-__global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t units) {
+__global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t slots, int64_t units) {
   constexpr int KS = DK / 32, HS = KS / 2, KP = F16 ? 2 : 1, ST = DK / 32;  // k steps (a half), parts of k and q, state tiles
   constexpr int KROW = 2 * DK + 32, CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
   __shared__ __align__(16) unsigned char kt[2][KP][C * KROW], qt[C * KROW], vt[C * kVRow];
@@ -363,7 +364,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     }
     return;
   }
-  const ChunkWs* w = ws + slot_base(lo, seq) * a.Hv + h;
+  const ChunkWs* w = ws + h * slots + slot_base(lo, seq);
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   auto left = [&](int64_t t0) { return hi - t0 < C ? (int)(hi - t0) : C; };
   // k's fp16 pairs as two bf16 parts (11 bits: exact)
@@ -404,27 +405,27 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       for (int i = 0; i < 2; ++i) in[i] = *reinterpret_cast<const f32x4*>(&cw->in[32 * hf + 16 * i + 4 * grp]);
     };
     // own pairs: (0,0) (1,0) or (2,1) (3,1); the others: none or (2,0) (3,0)
-    const int t_own = (hf ? 3 : 0) * 3072 + 16 * lane, t_oth = hf ? 2 * 3072 + 16 * lane : kNone, t_step = hf ? 6144 : 3072;
-    auto load_t = [&](const ChunkWs* cw) {
-      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<u32x4*>(&cw->T[0][0][0]), (short)0, (int)sizeof(cw->T), 0x00020000);
+    const int t_own = hf ? 3 : 0, t_oth = 2, t_step = hf ? 2 : 1;
+    auto load_t = [&](const ChunkWs* cw, int o) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          T[i][0][p] = __builtin_amdgcn_raw_buffer_load_b128(r, t_own + i * t_step + 1024 * p, 0, 0);
-          T[i][1][p] = __builtin_amdgcn_raw_buffer_load_b128(r, t_oth + i * t_step + 1024 * p, 0, 0);
-        }
-        outf[i] = *reinterpret_cast<const f32x4*>(&cw->out[32 * hf + 16 * i + 4 * grp]);
-      }
+        for (int p = 0; p < 3; ++p) T[i][o][p] = cw->T[(o ? t_oth : t_own) + i * t_step][p][lane];
+    };
+    auto load_out = [&](const ChunkWs* cw) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) outf[i] = *reinterpret_cast<const f32x4*>(&cw->out[32 * hf + 16 * i + 4 * grp]);
       keep = cw->keep;
     };
     load_in(w);
-    load_t(w);
+    load_t(w, 0);
+    load_t(w, 1);  // (of use to hf = 1 only)
+    load_out(w);
     put_state();
     __syncthreads();
     int buf = 0;
     for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
-      const ChunkWs* wn = t0 + C < hi ? w + a.Hv : w;
+      const ChunkWs* wn = t0 + C < hi ? w + 1 : w;
       // K S0: this half's state from registers, the other's from LDS
       f32x4 ks[2] = {zero, zero};
 #pragma unroll
@@ -480,12 +481,14 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
             for (int i = 0; i < 2; ++i) vn[i] = mma(T[i][o][p], r[x - p], vn[i]);
       };
       times(0, R);
+      load_t(wn, 0);
       __syncthreads();
       if (hf == 1) {
         u32x4 r0[3];
 #pragma unroll
         for (int p = 0; p < 3; ++p) r0[p] = Rs[sl][p][lane];
         times(1, r0);
+        load_t(wn, 1);
       }
       u32x4 W[3];
       {
@@ -501,7 +504,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       }
 #pragma unroll
       for (int t = 0; t < ST; ++t) S[t] *= keep;
-      load_t(wn);
+      load_out(wn);
       // S1 = e^{G63} S0 + K^T W
       auto update = [&](int k, const u32x4* wv) {
         u32x4 kop[ST][KP];
@@ -543,8 +546,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
   } else {
     // ---- output, and the next chunk's keys ----
     const int tid = threadIdx.x & 255;
-    u32x4 Kn[NL], Qn[NL], Vn, P[2][2][2];
-    float read[2];
+    u32x4 Kn[NL], Qn[NL], Vn, P[2][2][2], Pn[2][2][2];  // (n: the next chunk's)
+    float read[2], readn[2];
     const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
     const int q_off = (tid / CH) * (int)a.q_ld * 2 + 16 * (tid % CH), q_step = (256 / CH) * (int)a.q_ld * 2;
     const int vc = (c0 & ~31) + 8 * (tid & 3);
@@ -597,8 +600,18 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int p = 0; p < 2; ++p)
-            P[i][k][p] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off + i * p_step + k * p_k + 1024 * p, 0, 0);
-        read[i] = cw->read[32 * hf + 16 * i + col];
+            Pn[i][k][p] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off + i * p_step + k * p_k + 1024 * p, 0, 0);
+        readn[i] = cw->read[32 * hf + 16 * i + col];
+      }
+    };
+    auto take_p = [&]() {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) P[i][k][p] = Pn[i][k][p];
+        read[i] = readn[i];
       }
     };
     const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
@@ -633,6 +646,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     load_k(lo);
     load_q(lo);
     load_p(w);
+    take_p();
     put_kv(0);
     put_q();
     load_k(lo + C);
@@ -642,7 +656,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
       // while the state waves make R: the output of the chunk before
       finish(t0 - done, done);
-      load_p(w);
+      take_p();
       done = C;
       __syncthreads();
       // while they make V' and the new state: (Q S0)^T and the next keys
@@ -682,8 +696,9 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       __syncthreads();
       put_q();
       load_q(t0 + 2 * C);
+      if (t0 + C < hi) ++w;
+      load_p(w);
       __syncthreads();
-      if (t0 + C < hi) w += a.Hv;
     }
     const int64_t last = lo + (hi - lo - 1) / C * C;
     finish(last, (int)(hi - last));
@@ -692,16 +707,16 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 
 template <bool F16, int DK>
 hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
-  const int64_t prep = delta_chunk_slots(a.tokens, a.nseq) * a.Hv;
+  const int64_t slots = delta_chunk_slots(a.tokens, a.nseq), prep = slots * a.Hv;
   hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(64), 0, s, a, ws, prep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
   const dim3 grid((unsigned)((units + 7) / 8 * 8));
   if (a.out_dtype == F32)
-    hipLaunchKernelGGL((q1_chunk_run<F16, DK, true>), grid, dim3(kRunThreads), 0, s, a, ws, units);
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, true>), grid, dim3(kRunThreads), 0, s, a, ws, slots, units);
   else
-    hipLaunchKernelGGL((q1_chunk_run<F16, DK, false>), grid, dim3(kRunThreads), 0, s, a, ws, units);
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, false>), grid, dim3(kRunThreads), 0, s, a, ws, slots, units);
   return hipGetLastError();
 }
 
