@@ -75,6 +75,7 @@ struct SampleArgs {
   float* logprob;
 };
 
+size_t sample_ws_bytes(int64_t B, int64_t V);
 hipError_t launch_sample(const SampleArgs& a, unsigned char* ws, hipStream_t s);
 
 }  // namespace q1

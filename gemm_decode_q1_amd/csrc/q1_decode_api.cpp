@@ -207,8 +207,12 @@ size_t q1_sample_workspace_bytes(int64_t B, int64_t V) {
     fail(Q1_ERR_INVALID_ARG, "B must be >= 0 and V >= 1");
     return 0;
   }
+  if (B > (int64_t)1 << 20 || V > (int64_t)1 << 22) {
+    fail(Q1_ERR_UNSUPPORTED, "call too large");
+    return 0;
+  }
   ok();
-  return 0;
+  return B == 0 ? 0 : sample_ws_bytes(B, V);
 }
 
 q1_status q1_sample(const void* logits, int32_t dtype, int64_t B, int64_t V, int64_t ld, const float* u,

@@ -1,11 +1,26 @@
 // Sampler: temperature, top-k, top-p, min-p and one draw per row, from a given
-// random number.  One workgroup per row.
+// random number.
 //
-// The kept set is a threshold (key, ties): every logit with a larger key, and
-// the first `ties` logits, in index order, of those that equal it.  Both
-// thresholds come from a radix select over order-preserving 32-bit keys, by
-// count (top-k) and by weight (top-p).  Weights are whole multiples of 2^-40,
-// so all sums are exact and do not depend on the order of the additions.
+// A row is cut into contiguous chunks, one per wave; four launches:
+//   q1_sample_top     largest logit of each workgroup's chunks (and a cleared histogram)
+//   q1_sample_hist    e = exp((x - top)/T), weight w = floor(e 2^40); rows with top-k or
+//                     top-p: counts and weights in 2048 bins of (top - x)/T; other rows:
+//                     each chunk's sum of kept weights
+//   q1_sample_cut     the bins in which the top-k and the top-p cut fall, from the
+//                     histogram; each chunk's sum of the weights above them, and the
+//                     elements in them as candidates
+//   q1_sample_draw    one workgroup per row: the exact cut among the candidates, the
+//                     draw, the chunk it falls into, the token in that chunk
+// so a row is read two or three times (once from HBM, then from the caches), never
+// sorted, and any number of workgroups share it.  Weights are whole multiples of
+// 2^-40, so sums are exact: no result depends on the order of the additions.
+//
+// Order of logits: composite = 32-bit key (larger logit, larger key) over the
+// complement of the index, so equal logits go lowest index first and all
+// composites differ; a cut is one composite, and kept are those not below it.
+//
+// Where a cut's bins hold more than kMost candidates (rows that are flat, or full
+// of equal logits) the draw falls back to a radix select over the row itself.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -17,16 +32,49 @@
 namespace q1 {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kBins = 2048;            // of (top - x) / T in [0, 27.75): beyond, weights are zero
+constexpr float kBinsPerUnit = 73.8f;
+constexpr int kMost = 4096;            // candidates of one cut
 typedef unsigned long long u64;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+struct Hist {
+  u64 weight[kBins];
+  uint32_t count[kBins];
+};
+
+// Where a row's cuts fall (written by q1_sample_cut for q1_sample_draw).
+struct Cut {
+  u64 total;               // weight of the row
+  u64 above_k, above_p;    // weight above the bins of the cut
+  u64 want_k;              // elements to keep of the top-k bin
+  uint32_t n_k, n_p;       // candidates (from the histogram)
+  int32_t bin_k, lo_p, hi_p;  // -1: not in use
+  uint32_t first;          // greedy: the lowest index of the largest logit
+  uint32_t got_k, got_p;   // candidates written
+};
+
+struct Ws {
+  float* top;      // [B][S]
+  Hist* hist;      // [B]
+  Cut* cut;        // [B]
+  u64* sums;       // [B][S * kWaves]
+  ulonglong2* cand;  // [B][2][kMost]: composite, weight (top bit: below min_p)
+};
+
+template <int DT>
+constexpr int kSize = DT == F32 ? 4 : 2;
+
+template <int DT>
+__device__ __forceinline__ float clean(uint32_t bits) {
+  const float x = DT == F32 ? __uint_as_float(bits) : DT == BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32(bits);
+  return x != x ? -INFINITY : x + 0.0f;  // -0 and +0 are equal logits
+}
 
 template <int DT>
 __device__ __forceinline__ float logit(const void* p, int64_t i) {
-  float x;
-  if (DT == F32) x = static_cast<const float*>(p)[i];
-  else if (DT == BF16) x = bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else x = f16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-  return x != x ? -INFINITY : x + 0.0f;  // -0 and +0 are equal logits
+  return clean<DT>(DT == F32 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i]);
 }
 
 // Larger logits have larger keys.
@@ -35,60 +83,416 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+__device__ __forceinline__ u64 composite(float x, int i) { return (u64)key_of(x) << 32 | (uint32_t)~i; }
+
 __device__ __forceinline__ float exp_of(float x, float top, float T) { return x == top ? 1.0f : expf((x - top) / T); }
 
-__device__ __forceinline__ u64 weight_of(float e) { return (u64)(e * 1099511627776.0f); }
+// floor(e 2^40) for 0 <= e <= 1, from the bits of e.
+__device__ __forceinline__ u64 weight_of(float e) {
+  const uint32_t u = __float_as_uint(e), s = 127u - (u >> 23);
+  const u64 m = (u64)((u & 0x7fffffu) | 0x800000u) << 17;
+  return m >> (s < 63u ? s : 63u);
+}
 
-// Sum over the workgroup; every thread gets it.
-__device__ u64 block_sum(u64 v, u64* s) {
-  __syncthreads();
-  s[threadIdx.x] = v;
-  __syncthreads();
-  for (int w = kThreads / 2; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) s[threadIdx.x] += s[threadIdx.x + w];
-    __syncthreads();
-  }
-  const u64 r = s[0];
-  __syncthreads();
+__device__ __forceinline__ u64 bound_of(float p, u64 total) {
+  const double want = (double)p * (double)total;
+  return want >= 1.0 ? (u64)want : 1;
+}
+
+struct Row {
+  float T, p, mp;
+  int64_t k;
+  bool greedy, use_k, use_p;
+};
+
+__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
+  Row r;
+  r.T = a.temperature ? a.temperature[b] : 1.0f;
+  r.greedy = !(r.T > 0.f);
+  if (r.greedy) r.T = 1.f;
+  r.k = a.top_k ? a.top_k[b] : 0;
+  r.p = a.top_p ? a.top_p[b] : 1.f;
+  r.mp = a.min_p ? a.min_p[b] : 0.f;
+  r.mp = r.mp > 0.f ? fminf(r.mp, 1.f) : 0.f;
+  r.use_k = !r.greedy && r.k > 0 && r.k < a.V;
+  r.use_p = !r.greedy && r.p < 1.f;
   return r;
 }
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void q1_sample_row_kernel(const SampleArgs a) {
-  __shared__ u64 sw[kThreads], hist[256];
-  __shared__ uint32_t pick;
-  __shared__ u64 over;
-  const int64_t b = blockIdx.x;
-  const int tid = threadIdx.x;
-  const void* row = static_cast<const unsigned char*>(a.logits) + b * a.ld * (DT == F32 ? 4 : 2);
-  const int V = (int)a.V;
-  float T = a.temperature ? a.temperature[b] : 1.0f;
-  const bool greedy = !(T > 0.f);
-  if (greedy) T = 1.f;
-  const int64_t k = greedy ? 1 : a.top_k && a.top_k[b] > 0 ? a.top_k[b] : V;
-  const float p = a.top_p ? a.top_p[b] : 1.f;
-  float mp = a.min_p ? a.min_p[b] : 0.f;
-  mp = mp > 0.f ? fminf(mp, 1.f) : 0.f;
-
-  float top = -INFINITY;
-  for (int i = tid; i < V; i += kThreads) top = fmaxf(top, logit<DT>(row, i));
-  float* sf = reinterpret_cast<float*>(sw);
-  sf[tid] = top;
-  __syncthreads();
-  for (int w = kThreads / 2; w > 0; w >>= 1) {
-    if (tid < w) sf[tid] = fmaxf(sf[tid], sf[tid + w]);
-    __syncthreads();
+// e, weight and bin (at least kBins where the weight is zero) of one logit.
+// The quotient by T has to be the correctly rounded one.  With inv the correctly
+// rounded reciprocal, two corrections by the exact remainder give it (Markstein);
+// outside +-2^40 for T the division itself is used.  Quotients below -64 all have
+// weight zero.
+struct Scale {
+  float top, T, inv, least;
+  bool plain;
+  __device__ Scale(float top_, float T_) : top(top_), T(T_), inv(1.0f / T_), least(-64.0f * T_), plain(!(T_ > 9e-13f && T_ < 1e12f)) {}
+  __device__ __forceinline__ float exponent(float x) const {
+    if (x == top) return 0.f;
+    const float d = fmaxf(x - top, least);
+    if (plain) return d / T;
+    float q = d * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
+    return __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
   }
-  top = sf[0];
+};
+
+__device__ __forceinline__ int bin_of(float t) { return (int)(-t * kBinsPerUnit); }
+
+// Chunk c of a row: [c len, (c + 1) len), len = V over all chunks, rounded up.
+__device__ __forceinline__ int chunk_len(int64_t V, int chunks) { return (int)((V + chunks - 1) / chunks); }
+
+// f(index, logit) for every element of [lo, hi), by one wave: 16-byte loads, four
+// in flight, between the first and the last aligned element.
+template <int DT, class F>
+__device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
+  constexpr int E = 16 / kSize<DT>;
+  const int lane = threadIdx.x & 63;
+  if (lo >= hi) return;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (int64_t)lo * kSize<DT>;
+  int head = (int)((16 - at % 16) % 16) / kSize<DT>;
+  if (head > hi - lo) head = hi - lo;
+  if (lane < head) f(lo + lane, logit<DT>(row, lo + lane));
+  const int a0 = lo + head, nv = (hi - a0) / E;
+  const u32x4* v = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(row) + (int64_t)a0 * kSize<DT>);
+  for (int i = lane; i < nv; i += 256) {
+    u32x4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 64 * u < nv) x[u] = v[i + 64 * u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 64 * u < nv) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          f(a0 + (i + 64 * u) * E + e, clean<DT>(DT == F32 ? x[u][e] : (x[u][e >> 1] >> (16 * (e & 1))) & 0xffffu));
+      }
+  }
+  const int tail = a0 + nv * E + lane;
+  if (tail < hi) f(tail, logit<DT>(row, tail));
+}
+
+__device__ __forceinline__ u64 wave_sum(u64 v) {
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+  return v;
+}
+
+// Exclusive sum over the workgroup's threads in order; *total: of all of them.
+__device__ u64 block_scan(u64 v, u64* s, u64* total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  u64 x = v;
+  for (int off = 1; off < 64; off <<= 1) {
+    const u64 y = __shfl_up(x, off);
+    if (lane >= off) x += y;
+  }
   __syncthreads();
-  if (top == -INFINITY) {
-    if (tid == 0) {
-      if (a.tokens_int64) static_cast<int64_t*>(a.tokens)[b] = -1;
-      else static_cast<int32_t*>(a.tokens)[b] = -1;
-      if (a.logprob) a.logprob[b] = -INFINITY;
-    }
+  if (lane == 63) s[w] = x;
+  __syncthreads();
+  u64 before = 0, all = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < w) before += s[i];
+    all += s[i];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ void put_token(const SampleArgs& a, int64_t b, int64_t token, float logprob) {
+  if (a.tokens_int64) static_cast<int64_t*>(a.tokens)[b] = token;
+  else static_cast<int32_t*>(a.tokens)[b] = (int32_t)token;
+  if (a.logprob) a.logprob[b] = logprob;
+}
+
+template <int DT>
+__device__ __forceinline__ const void* row_ptr(const SampleArgs& a, int64_t b) {
+  return static_cast<const unsigned char*>(a.logits) + b * a.ld * kSize<DT>;
+}
+
+__device__ __forceinline__ float row_top(const Ws& ws, int64_t b, int S) {
+  float top = -INFINITY;
+  for (int i = 0; i < S; ++i) top = fmaxf(top, ws.top[b * S + i]);
+  return top;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void q1_sample_top(const SampleArgs a, const Ws ws, int S) {
+  __shared__ float part[kWaves];
+  const int64_t b = blockIdx.x / S;
+  const int s = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
+  const int len = chunk_len(a.V, S * kWaves), lo = (s * kWaves + wave) * len, end = lo + len;
+  float top = -INFINITY;
+  each<DT>(row_ptr<DT>(a, b), lo, end < a.V ? end : (int)a.V, [&](int, float x) { top = fmaxf(top, x); });
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) part[wave] = top;
+  for (int i = s * kThreads + threadIdx.x; i < kBins; i += S * kThreads) {
+    ws.hist[b].weight[i] = 0;
+    ws.hist[b].count[i] = 0;
+  }
+  if (s == 0 && threadIdx.x == 0) {
+    ws.cut[b].first = ~0u;
+    ws.cut[b].got_k = ws.cut[b].got_p = 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, part[i]);
+    ws.top[b * S + s] = top;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void q1_sample_hist(const SampleArgs a, const Ws ws, int S) {
+  __shared__ Hist h;
+  const int64_t b = blockIdx.x / S;
+  const int s = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
+  const Row r = row_of(a, b);
+  const float top = row_top(ws, b, S);
+  if (top == -INFINITY) return;
+  const int len = chunk_len(a.V, S * kWaves), c = s * kWaves + wave, lo = c * len;
+  const int hi = lo + len < a.V ? lo + len : (int)a.V;
+  const void* row = row_ptr<DT>(a, b);
+  if (r.greedy) {
+    int first = 0x7fffffff;
+    each<DT>(row, lo, hi, [&](int i, float x) {
+      if (x == top && i < first) first = i;
+    });
+    if (first != 0x7fffffff) atomicMin(&ws.cut[b].first, (uint32_t)first);
     return;
   }
+  const Scale sc(top, r.T);
+  if (!r.use_k && !r.use_p) {
+    u64 sum = 0;
+    each<DT>(row, lo, hi, [&](int, float x) {
+      const float e = expf(sc.exponent(x));
+      if (!(e < r.mp)) sum += weight_of(e);
+    });
+    sum = wave_sum(sum);
+    if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + c] = sum;
+    return;
+  }
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    h.weight[i] = 0;
+    h.count[i] = 0;
+  }
+  __syncthreads();
+  each<DT>(row, lo, hi, [&](int, float x) {
+    const float t = sc.exponent(x);
+    const u64 w = weight_of(expf(t));
+    if (w != 0) {
+      const int bin = bin_of(t);
+      atomicAdd(&h.weight[bin], w);
+      atomicAdd(&h.count[bin], 1u);
+    }
+  });
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads)
+    if (h.count[i] != 0) {
+      atomicAdd(&ws.hist[b].weight[i], h.weight[i]);
+      atomicAdd(&ws.hist[b].count[i], h.count[i]);
+    }
+}
+
+// The bins of the cuts, from the histogram; every thread of the workgroup gets them.
+__device__ Cut find_cut(const Hist& h, const Row& r, u64* s, Cut* out) {
+  const int t = threadIdx.x;
+  static_assert(kBins == 2 * kThreads, "two bins a thread");
+  const u64 w0 = h.weight[2 * t], w1 = h.weight[2 * t + 1];
+  const uint32_t n0 = h.count[2 * t], n1 = h.count[2 * t + 1];
+  Cut c;
+  u64 all;
+  const u64 wb = block_scan(w0 + w1, s, &c.total), nb = block_scan((u64)n0 + n1, s, &all);
+  if (t == 0) {
+    out->bin_k = out->lo_p = out->hi_p = -1;
+    out->n_k = out->n_p = 0;
+    out->above_k = out->above_p = out->want_k = 0;
+  }
+  __syncthreads();
+  const bool use_k = r.use_k && (u64)r.k < all;  // else every element with a weight is kept
+  u64 least = c.total, most = c.total;           // of the weight that top-k keeps
+  if (use_k) {
+    const u64 k = (u64)r.k;
+    if (nb < k && k <= nb + n0 + n1) {
+      const bool second = nb + n0 < k;
+      out->bin_k = 2 * t + second;
+      out->n_k = second ? n1 : n0;
+      out->above_k = wb + (second ? w0 : 0);
+      out->want_k = k - nb - (second ? n0 : 0);
+      s[kWaves] = second ? w1 : w0;
+    }
+    __syncthreads();
+    least = out->above_k;
+    most = least + s[kWaves];
+  }
+  if (r.use_p) {
+    const u64 p0 = bound_of(r.p, least), p1 = bound_of(r.p, most);
+    if (wb < p0 && p0 <= wb + w0 + w1) {
+      const bool second = wb + w0 < p0;
+      out->lo_p = 2 * t + second;
+      out->above_p = wb + (second ? w0 : 0);
+    }
+    if (wb < p1 && p1 <= wb + w0 + w1) out->hi_p = 2 * t + (wb + w0 < p1);
+    __syncthreads();
+    const int lo = out->lo_p, hi = out->hi_p;
+    u64 n;
+    block_scan((2 * t >= lo && 2 * t <= hi ? n0 : 0) + (u64)(2 * t + 1 >= lo && 2 * t + 1 <= hi ? n1 : 0), s, &n);
+    if (t == 0) out->n_p = (uint32_t)n;
+  }
+  __syncthreads();
+  c.bin_k = out->bin_k;
+  c.lo_p = out->lo_p;
+  c.hi_p = out->hi_p;
+  c.n_k = out->n_k;
+  c.n_p = out->n_p;
+  c.above_k = out->above_k;
+  c.above_p = out->above_p;
+  c.want_k = out->want_k;
+  return c;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void q1_sample_cut(const SampleArgs a, const Ws ws, int S) {
+  __shared__ u64 s[kWaves + 1];
+  __shared__ Cut found;
+  const int64_t b = blockIdx.x / S;
+  const int sl = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
+  const Row r = row_of(a, b);
+  if (!r.use_k && !r.use_p) return;
+  const float top = row_top(ws, b, S);
+  if (top == -INFINITY) return;
+  const Cut c = find_cut(ws.hist[b], r, s, &found);
+  if (sl == 0 && threadIdx.x == 0) {
+    Cut* o = &ws.cut[b];
+    o->total = c.total;
+    o->above_k = c.above_k;
+    o->above_p = c.above_p;
+    o->want_k = c.want_k;
+    o->n_k = c.n_k;
+    o->n_p = c.n_p;
+    o->bin_k = c.bin_k;
+    o->lo_p = c.lo_p;
+    o->hi_p = c.hi_p;
+  }
+  if (c.n_k > kMost || c.n_p > kMost) return;
+  // below the first bin of the deciding cut, everything is kept
+  const int sure = r.use_p ? c.lo_p : c.bin_k >= 0 ? c.bin_k : kBins;
+  const int last = c.bin_k > c.hi_p ? c.bin_k : c.hi_p;  // past it nothing is (none in use: -1, and sure has all)
+  const Scale sc(top, r.T);
+  const int len = chunk_len(a.V, S * kWaves), ch = sl * kWaves + wave, lo = ch * len;
+  const int hi = lo + len < a.V ? lo + len : (int)a.V;
+  u64 sum = 0;
+  each<DT>(row_ptr<DT>(a, b), lo, hi, [&](int i, float x) {
+    const float t = sc.exponent(x);
+    const int bin = bin_of(t);
+    if (bin >= sure && bin > last) return;
+    const float e = expf(t);
+    const u64 w = weight_of(e);
+    if (w == 0) return;
+    const bool low = e < r.mp;
+    if (bin < sure && !low) sum += w;
+    const ulonglong2 entry = {composite(x, i), w | (low ? 1ull << 63 : 0)};
+    if (bin == c.bin_k) {
+      const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
+      if (at < kMost) ws.cand[(b * 2) * kMost + at] = entry;
+    }
+    if (bin >= c.lo_p && bin <= c.hi_p) {
+      const uint32_t at = atomicAdd(&ws.cut[b].got_p, 1u);
+      if (at < kMost) ws.cand[(b * 2 + 1) * kMost + at] = entry;
+    }
+  });
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + ch] = sum;
+}
+
+struct DrawShared {
+  u64 comp[kMost], weight[kMost];
+  u64 bins[kThreads];
+  u64 s[kWaves + 1];
+  u64 pick, over;
+  uint32_t left;
+};
+
+// Of the n candidates in LDS (weights with the min-p bit), largest composite
+// first: the one at which the running sum of ones or weights reaches `want`.
+// Digits of 10 bits, from the highest bit in which those left differ.
+__device__ u64 select_candidate(DrawShared& d, int n, bool weighted, u64 want) {
+  const int t = threadIdx.x;
+  u64 mask = 0, prefix = 0, before = 0;
+  for (;;) {
+    u64 ones = 0, zeros = 0;  // bits seen set and seen clear among those left
+    for (int i = t; i < n; i += kThreads)
+      if ((d.comp[i] & mask) == prefix) {
+        ones |= d.comp[i];
+        zeros |= ~d.comp[i];
+      }
+    for (int off = 32; off > 0; off >>= 1) {
+      ones |= __shfl_xor(ones, off);
+      zeros |= __shfl_xor(zeros, off);
+    }
+    __syncthreads();
+    if ((t & 63) == 0) {
+      d.bins[t >> 6] = ones;
+      d.bins[kWaves + (t >> 6)] = zeros;
+    }
+    __syncthreads();
+    ones = zeros = 0;
+    for (int i = 0; i < kWaves; ++i) {
+      ones |= d.bins[i];
+      zeros |= d.bins[kWaves + i];
+    }
+    const u64 differ = ones & zeros;
+    if (differ == 0) return ones;  // one left
+    const int high = 63 - __builtin_clzll(differ), shift = high > 9 ? high - 9 : 0;
+    __syncthreads();
+    d.bins[t] = 0;
+    __syncthreads();
+    for (int i = t; i < n; i += kThreads)
+      if ((d.comp[i] & mask) == prefix)
+        atomicAdd(&d.bins[(kThreads - 1) - ((d.comp[i] >> shift) & (kThreads - 1))],
+                  weighted ? d.weight[i] & ~(1ull << 63) : 1ull);
+    __syncthreads();
+    const u64 mine = d.bins[t];
+    u64 all;
+    const u64 at = before + block_scan(mine, d.s, &all);
+    if (t == 0) d.pick = ~0ull;
+    __syncthreads();
+    if (at < want && want <= at + mine) {
+      d.pick = (u64)(kThreads - 1 - t);
+      d.over = at;
+    }
+    __syncthreads();
+    if (d.pick == ~0ull) return prefix;  // the sum stays below: all are kept
+    // (a 1024-wide window may start above the highest differing bit: those bits agree)
+    mask = ~0ull << shift;
+    prefix = (ones & ~((2ull << high) - 1)) | ((d.pick << shift) & ((2ull << high) - 1));
+    before = d.over;
+    __syncthreads();
+  }
+}
+
+__device__ void load_candidates(DrawShared& d, const ulonglong2* from, int n) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    d.comp[i] = from[i].x;
+    d.weight[i] = from[i].y;
+  }
+  __syncthreads();
+}
+
+// A row's token by radix selects over the row itself (see the top of the file).
+template <int DT>
+__device__ void draw_from_row(const SampleArgs& a, int64_t b, const void* row, const Row& r, float top, u64* sw) {
+  __shared__ u64 hist[256];
+  __shared__ uint32_t pick;
+  __shared__ u64 over;
+  const int tid = threadIdx.x;
+  const int V = (int)a.V;
+  const float T = r.T, p = r.p, mp = r.mp;
+  const int64_t k = r.use_k ? r.k : V;
 
   // Radix select, largest key first: the key at which the running sum of
   // `amount` (1 or the weight, counting at most `kties` of the key kthr)
@@ -147,7 +551,8 @@ __global__ __launch_bounds__(kThreads) void q1_sample_row_kernel(const SampleArg
       const float x = logit<DT>(row, i);
       if (kties == ~0ull || key_of(x) > kthr) mine += weight_of(exp_of(x, top, T));
     }
-    u64 total = block_sum(mine, sw);
+    u64 total;
+    block_scan(mine, sw, &total);
     if (kties != ~0ull) {
       const uint32_t bits = kthr >> 31 ? kthr ^ 0x80000000u : ~kthr;
       total += kties * weight_of(exp_of(__uint_as_float(bits), top, T));
@@ -192,17 +597,15 @@ __global__ __launch_bounds__(kThreads) void q1_sample_row_kernel(const SampleArg
     total += sw[j];
   }
   const float u = a.u[b];
-  u64 r = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
-  if (r >= total) r = total - 1;
-  if (r >= start && r < start + mine) {
+  u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
+  if (at >= total) at = total - 1;
+  if (at >= start && at < start + mine) {
     u64 c = start;
     rank = rank0;
     for (int i = i0; i < i1; ++i) {
       const u64 w = kept(i, &rank);
-      if (r < c + w) {
-        if (a.tokens_int64) static_cast<int64_t*>(a.tokens)[b] = i;
-        else static_cast<int32_t*>(a.tokens)[b] = i;
-        if (a.logprob) a.logprob[b] = logf((float)((double)w / (double)total));
+      if (at < c + w) {
+        put_token(a, b, i, logf((float)((double)w / (double)total)));
         break;
       }
       c += w;
@@ -210,15 +613,136 @@ __global__ __launch_bounds__(kThreads) void q1_sample_row_kernel(const SampleArg
   }
 }
 
+template <int DT>
+__global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, const Ws ws, int S) {
+  __shared__ DrawShared d;
+  const int64_t b = blockIdx.x;
+  const int t = threadIdx.x, chunks = S * kWaves;
+  const Row r = row_of(a, b);
+  const float top = row_top(ws, b, S);
+  if (top == -INFINITY) {
+    if (t == 0) put_token(a, b, -1, -INFINITY);
+    return;
+  }
+  if (r.greedy) {
+    if (t == 0) put_token(a, b, ws.cut[b].first, 0.f);
+    return;
+  }
+  const void* row = row_ptr<DT>(a, b);
+  u64 cut = 0;  // the lowest kept composite
+  int n = 0;    // candidates in LDS
+  if (r.use_k || r.use_p) {
+    const Cut c = ws.cut[b];
+    if (c.n_k > kMost || c.n_p > kMost) {
+      draw_from_row<DT>(a, b, row, r, top, d.comp);
+      return;
+    }
+    u64 kept = c.total;
+    if (c.bin_k >= 0) {
+      n = (int)c.n_k;
+      load_candidates(d, ws.cand + (b * 2) * kMost, n);
+      cut = select_candidate(d, n, false, c.want_k);
+      u64 mine = 0;
+      for (int i = t; i < n; i += kThreads)
+        if (d.comp[i] >= cut) mine += d.weight[i] & ~(1ull << 63);
+      block_scan(mine, d.s, &kept);
+      kept += c.above_k;
+    }
+    if (r.use_p) {
+      n = (int)c.n_p;
+      load_candidates(d, ws.cand + (b * 2 + 1) * kMost, n);
+      cut = select_candidate(d, n, true, bound_of(r.p, kept) - c.above_p);
+    }
+  }
+  // weights by chunk: what is sure, and the kept candidates
+  const int len = chunk_len(a.V, chunks);
+  __syncthreads();
+  d.bins[t] = t < chunks ? ws.sums[b * chunks + t] : 0;
+  __syncthreads();
+  for (int i = t; i < n; i += kThreads)
+    if (d.comp[i] >= cut && !(d.weight[i] >> 63)) atomicAdd(&d.bins[~(uint32_t)d.comp[i] / (uint32_t)len], d.weight[i]);
+  __syncthreads();
+  u64 total;
+  const u64 mine = d.bins[t], start = block_scan(mine, d.s, &total);
+  const float u = a.u[b];
+  u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
+  if (at >= total) at = total - 1;
+  if (at >= start && at < start + mine) {
+    d.left = (uint32_t)t;
+    d.over = at - start;
+  }
+  __syncthreads();
+  // the token: consecutive elements of the chunk, a few per thread
+  const int lo = (int)d.left * len, hi = lo + len < a.V ? lo + len : (int)a.V;
+  const u64 want = d.over;
+  const int per = (hi - lo + kThreads - 1) / kThreads;
+  const int i0 = lo + t * per < hi ? lo + t * per : hi, i1 = i0 + per < hi ? i0 + per : hi;
+  const Scale sc(top, r.T);
+  auto weight = [&](int i) -> u64 {
+    const float x = logit<DT>(row, i);
+    const float e = expf(sc.exponent(x));
+    return composite(x, i) >= cut && !(e < r.mp) ? weight_of(e) : 0;
+  };
+  u64 sum = 0;
+  for (int i = i0; i < i1; ++i) sum += weight(i);
+  u64 all;
+  u64 c = block_scan(sum, d.s, &all);
+  if (want >= c && want < c + sum)
+    for (int i = i0; i < i1; ++i) {
+      const u64 w = weight(i);
+      if (want < c + w) {
+        put_token(a, b, i, logf((float)((double)w / (double)total)));
+        break;
+      }
+      c += w;
+    }
+}
+
+template <int DT>
+hipError_t launch_t(const SampleArgs& a, const Ws& w, int S, hipStream_t s) {
+  const dim3 grid((unsigned)(a.B * S)), block(kThreads);
+  hipLaunchKernelGGL((q1_sample_top<DT>), grid, block, 0, s, a, w, S);
+  hipLaunchKernelGGL((q1_sample_hist<DT>), grid, block, 0, s, a, w, S);
+  if (a.top_k != nullptr || a.top_p != nullptr) hipLaunchKernelGGL((q1_sample_cut<DT>), grid, block, 0, s, a, w, S);
+  hipLaunchKernelGGL((q1_sample_draw<DT>), dim3((unsigned)a.B), block, 0, s, a, w, S);
+  return hipGetLastError();
+}
+
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
+
 }  // namespace
 
+// Workgroups per row: about two per compute unit in all, at least 4096 elements
+// each, and no more chunks than the draw has threads.
+int sample_split(int64_t B, int64_t V) {
+  int64_t S = (512 + B - 1) / B, most = (V + 4095) / 4096;
+  if (S > most) S = most;
+  if (S > kThreads / kWaves) S = kThreads / kWaves;
+  return S < 1 ? 1 : (int)S;
+}
+
+size_t sample_ws_bytes(int64_t B, int64_t V) {
+  const size_t S = (size_t)sample_split(B, V), b = (size_t)B;
+  return up(b * sizeof(Hist)) + up(b * 2 * kMost * sizeof(ulonglong2)) + up(b * sizeof(Cut)) +
+         up(b * S * kWaves * sizeof(u64)) + up(b * S * sizeof(float));
+}
+
 hipError_t launch_sample(const SampleArgs& a, unsigned char* ws, hipStream_t s) {
-  (void)ws;
-  const dim3 grid((unsigned)a.B), block(kThreads);
-  if (a.dtype == F32) hipLaunchKernelGGL((q1_sample_row_kernel<F32>), grid, block, 0, s, a);
-  else if (a.dtype == BF16) hipLaunchKernelGGL((q1_sample_row_kernel<BF16>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((q1_sample_row_kernel<F16>), grid, block, 0, s, a);
-  return hipGetLastError();
+  const int S = sample_split(a.B, a.V);
+  const size_t b = (size_t)a.B;
+  Ws w;
+  w.hist = reinterpret_cast<Hist*>(ws);
+  ws += up(b * sizeof(Hist));
+  w.cand = reinterpret_cast<ulonglong2*>(ws);
+  ws += up(b * 2 * kMost * sizeof(ulonglong2));
+  w.cut = reinterpret_cast<Cut*>(ws);
+  ws += up(b * sizeof(Cut));
+  w.sums = reinterpret_cast<u64*>(ws);
+  ws += up(b * (size_t)S * kWaves * sizeof(u64));
+  w.top = reinterpret_cast<float*>(ws);
+  if (a.dtype == F32) return launch_t<F32>(a, w, S, s);
+  if (a.dtype == BF16) return launch_t<BF16>(a, w, S, s);
+  return launch_t<F16>(a, w, S, s);
 }
 
 }  // namespace q1
