@@ -3,9 +3,9 @@
 //
 // A row is cut into contiguous chunks, one per wave; four launches:
 //   q1_sample_top     largest logit of each workgroup's chunks (and a cleared histogram)
-//   q1_sample_hist    e = exp((x - top)/T), weight w = floor(e 2^40); rows with top-k or
-//                     top-p: counts and weights in 2048 bins of (top - x)/T; other rows:
-//                     each chunk's sum of kept weights
+//   q1_sample_hist    e = exp((x - top)/T), weight w = floor(e 2^40); rows with top-k:
+//                     counts in 2048 bins of (top - x)/T, with top-p: weights in them;
+//                     other rows: each chunk's sum of kept weights
 //   q1_sample_cut     the bins in which the top-k and the top-p cut fall, from the
 //                     histogram; each chunk's sum of the weights above them, and the
 //                     elements in them as candidates
@@ -49,7 +49,7 @@ struct Cut {
   u64 total;               // weight of the row
   u64 above_k, above_p;    // weight above the bins of the cut
   u64 want_k;              // elements to keep of the top-k bin
-  uint32_t n_k, n_p;       // candidates (from the histogram)
+  uint32_t n_k, n_p;       // candidates, at most (from the histogram)
   int32_t bin_k, lo_p, hi_p;  // -1: not in use
   uint32_t first;          // greedy: the lowest index of the largest logit
   uint32_t got_k, got_p;   // candidates written
@@ -67,14 +67,16 @@ template <int DT>
 constexpr int kSize = DT == F32 ? 4 : 2;
 
 template <int DT>
-__device__ __forceinline__ float clean(uint32_t bits) {
-  const float x = DT == F32 ? __uint_as_float(bits) : DT == BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32(bits);
-  return x != x ? -INFINITY : x + 0.0f;  // -0 and +0 are equal logits
+__device__ __forceinline__ float value_of(uint32_t bits) {
+  return DT == F32 ? __uint_as_float(bits) : DT == BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32(bits);
 }
+
+// NaN counts as -infinity, -0 and +0 are equal logits.
+__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : x + 0.0f; }
 
 template <int DT>
 __device__ __forceinline__ float logit(const void* p, int64_t i) {
-  return clean<DT>(DT == F32 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i]);
+  return clean(value_of<DT>(DT == F32 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i]));
 }
 
 // Larger logits have larger keys.
@@ -87,11 +89,12 @@ __device__ __forceinline__ u64 composite(float x, int i) { return (u64)key_of(x)
 
 __device__ __forceinline__ float exp_of(float x, float top, float T) { return x == top ? 1.0f : expf((x - top) / T); }
 
-// floor(e 2^40) for 0 <= e <= 1, from the bits of e.
+// floor(e 2^40) for 0 <= e <= 1: the scaling is exact and the conversion cuts off;
+// weights from 2^32 on (few) are shifted out of the bits of e.
 __device__ __forceinline__ u64 weight_of(float e) {
-  const uint32_t u = __float_as_uint(e), s = 127u - (u >> 23);
-  const u64 m = (u64)((u & 0x7fffffu) | 0x800000u) << 17;
-  return m >> (s < 63u ? s : 63u);
+  u64 w = (uint32_t)(e * 1099511627776.0f);
+  if (e >= 0.00390625f) w = (u64)((__float_as_uint(e) & 0x7fffffu) | 0x800000u) << 17 >> (127u - (__float_as_uint(e) >> 23));
+  return w;
 }
 
 __device__ __forceinline__ u64 bound_of(float p, u64 total) {
@@ -119,22 +122,25 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
   return r;
 }
 
-// e, weight and bin (at least kBins where the weight is zero) of one logit.
-// The quotient by T has to be the correctly rounded one.  With inv the correctly
+// (x - top) / T of one logit, not below -64 (where weights are zero long since).
+// The quotient has to be the correctly rounded one.  With inv the correctly
 // rounded reciprocal, two corrections by the exact remainder give it (Markstein);
-// outside +-2^40 for T the division itself is used.  Quotients below -64 all have
-// weight zero.
+// outside 2^+-40 for T the division itself is used.  NaN comes out as -64.
 struct Scale {
   float top, T, inv, least;
   bool plain;
-  __device__ Scale(float top_, float T_) : top(top_), T(T_), inv(1.0f / T_), least(-64.0f * T_), plain(!(T_ > 9e-13f && T_ < 1e12f)) {}
+  __device__ Scale(float top_, float T_)
+      : top(top_), T(T_), inv(1.0f / T_), least(-64.0f * T_), plain(!(T_ > 9e-13f && T_ < 1e12f) || top_ == INFINITY) {}
   __device__ __forceinline__ float exponent(float x) const {
-    if (x == top) return 0.f;
     const float d = fmaxf(x - top, least);
-    if (plain) return d / T;
+    if (plain) return x == top ? 0.f : fmaxf(d / T, -64.f);
     float q = d * inv;
     q = __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
     return __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
+  }
+  // Below it, every logit's bin is past `bin`.
+  __device__ __forceinline__ float past(int bin) const {
+    return plain ? -INFINITY : top - T * ((float)(bin + 1) / kBinsPerUnit) * 1.0001f - fabsf(top) * 1e-6f;
   }
 };
 
@@ -143,7 +149,7 @@ __device__ __forceinline__ int bin_of(float t) { return (int)(-t * kBinsPerUnit)
 // Chunk c of a row: [c len, (c + 1) len), len = V over all chunks, rounded up.
 __device__ __forceinline__ int chunk_len(int64_t V, int chunks) { return (int)((V + chunks - 1) / chunks); }
 
-// f(index, logit) for every element of [lo, hi), by one wave: 16-byte loads, four
+// f(index, logit as it is) for every element of [lo, hi), by one wave: 16-byte loads, four
 // in flight, between the first and the last aligned element.
 template <int DT, class F>
 __device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
@@ -153,7 +159,8 @@ __device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (int64_t)lo * kSize<DT>;
   int head = (int)((16 - at % 16) % 16) / kSize<DT>;
   if (head > hi - lo) head = hi - lo;
-  if (lane < head) f(lo + lane, logit<DT>(row, lo + lane));
+  auto raw = [&](int i) { return value_of<DT>(DT == F32 ? static_cast<const uint32_t*>(row)[i] : static_cast<const uint16_t*>(row)[i]); };
+  if (lane < head) f(lo + lane, raw(lo + lane));
   const int a0 = lo + head, nv = (hi - a0) / E;
   const u32x4* v = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(row) + (int64_t)a0 * kSize<DT>);
   for (int i = lane; i < nv; i += 256) {
@@ -166,41 +173,68 @@ __device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
       if (i + 64 * u < nv) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          f(a0 + (i + 64 * u) * E + e, clean<DT>(DT == F32 ? x[u][e] : (x[u][e >> 1] >> (16 * (e & 1))) & 0xffffu));
+          f(a0 + (i + 64 * u) * E + e, value_of<DT>(DT == F32 ? x[u][e] : (x[u][e >> 1] >> (16 * (e & 1))) & 0xffffu));
       }
   }
   const int tail = a0 + nv * E + lane;
-  if (tail < hi) f(tail, logit<DT>(row, tail));
+  if (tail < hi) f(tail, raw(tail));
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+// One step of a scan over a wave's lanes: v plus (or the larger of v and) the value
+// that the DPP control brings from another lane, where the row mask has this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 step_add(u64 v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return v + ((u64)hi << 32 | lo);
 }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float step_max(float v) {
+  const int none = (int)0xff800000u;  // -infinity
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(none, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false)));
+}
+
+// Inclusive sum over the lanes of a wave: rows of 16 by shifts of 1, 2, 4, 8, then
+// the last lane of a row to the next one, and of the lower half to the upper.
+__device__ __forceinline__ u64 wave_scan(u64 v) {
+  v = step_add<0x111, 0xf>(v);
+  v = step_add<0x112, 0xf>(v);
+  v = step_add<0x114, 0xf>(v);
+  v = step_add<0x118, 0xf>(v);
+  v = step_add<0x142, 0xa>(v);
+  return step_add<0x143, 0xc>(v);
+}
+
+__device__ __forceinline__ u64 last_lane(u64 v) {
+  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
+}
+
+__device__ __forceinline__ u64 wave_sum(u64 v) { return last_lane(wave_scan(v)); }
 
 __device__ __forceinline__ float wave_max(float v) {
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+  v = step_max<0x111, 0xf>(v);
+  v = step_max<0x112, 0xf>(v);
+  v = step_max<0x114, 0xf>(v);
+  v = step_max<0x118, 0xf>(v);
+  v = step_max<0x142, 0xa>(v);
+  v = step_max<0x143, 0xc>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Exclusive sum over the workgroup's threads in order; *total: of all of them.
-__device__ u64 block_scan(u64 v, u64* s, u64* total) {
+// s: kWaves words that no thread reads or writes meanwhile.
+__device__ __forceinline__ u64 block_scan(u64 v, u64* s, u64* total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  u64 x = v;
-  for (int off = 1; off < 64; off <<= 1) {
-    const u64 y = __shfl_up(x, off);
-    if (lane >= off) x += y;
-  }
-  __syncthreads();
+  const u64 x = wave_scan(v);
   if (lane == 63) s[w] = x;
   __syncthreads();
-  u64 before = 0, all = 0;
-  for (int i = 0; i < kWaves; ++i) {
-    if (i < w) before += s[i];
-    all += s[i];
-  }
-  *total = all;
-  return before + x - v;
+  const u64 waves = wave_scan(lane < kWaves ? s[lane] : 0);
+  *total = last_lane(waves);
+  const u64 upto = (u64)__shfl((int64_t)waves, w);  // through wave w
+  const u64 own = last_lane(x);
+  return upto - own + x - v;
 }
 
 __device__ __forceinline__ void put_token(const SampleArgs& a, int64_t b, int64_t token, float logprob) {
@@ -214,10 +248,10 @@ __device__ __forceinline__ const void* row_ptr(const SampleArgs& a, int64_t b) {
   return static_cast<const unsigned char*>(a.logits) + b * a.ld * kSize<DT>;
 }
 
+// S is at most a wave's lanes.
 __device__ __forceinline__ float row_top(const Ws& ws, int64_t b, int S) {
-  float top = -INFINITY;
-  for (int i = 0; i < S; ++i) top = fmaxf(top, ws.top[b * S + i]);
-  return top;
+  const int lane = threadIdx.x & 63;
+  return wave_max(lane < S ? ws.top[b * S + lane] : -INFINITY);
 }
 
 template <int DT>
@@ -246,12 +280,12 @@ __global__ __launch_bounds__(kThreads) void q1_sample_top(const SampleArgs a, co
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void q1_sample_hist(const SampleArgs a, const Ws ws, int S) {
+__global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a, const Ws ws, int S) {
   __shared__ Hist h;
   const int64_t b = blockIdx.x / S;
   const int s = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
-  const Row r = row_of(a, b);
   const float top = row_top(ws, b, S);
+  const Row r = row_of(a, b);
   if (top == -INFINITY) return;
   const int len = chunk_len(a.V, S * kWaves), c = s * kWaves + wave, lo = c * len;
   const int hi = lo + len < a.V ? lo + len : (int)a.V;
@@ -280,53 +314,64 @@ __global__ __launch_bounds__(kThreads) void q1_sample_hist(const SampleArgs a, c
     h.count[i] = 0;
   }
   __syncthreads();
-  each<DT>(row, lo, hi, [&](int, float x) {
-    const float t = sc.exponent(x);
-    const u64 w = weight_of(expf(t));
-    if (w != 0) {
+  if (!r.use_p) {
+    each<DT>(row, lo, hi, [&](int, float x) {
+      const int bin = bin_of(sc.exponent(x));
+      if (bin < kBins) atomicAdd(&h.count[bin], 1u);
+    });
+  } else {
+    each<DT>(row, lo, hi, [&](int, float x) {
+      const float t = sc.exponent(x);
+      const u64 w = weight_of(expf(t));
+      if (w == 0) return;
       const int bin = bin_of(t);
       atomicAdd(&h.weight[bin], w);
-      atomicAdd(&h.count[bin], 1u);
-    }
-  });
+      if (r.use_k) atomicAdd(&h.count[bin], 1u);
+    });
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads)
-    if (h.count[i] != 0) {
-      atomicAdd(&ws.hist[b].weight[i], h.weight[i]);
-      atomicAdd(&ws.hist[b].count[i], h.count[i]);
-    }
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    if (h.weight[i] != 0) atomicAdd(&ws.hist[b].weight[i], h.weight[i]);
+    if (h.count[i] != 0) atomicAdd(&ws.hist[b].count[i], h.count[i]);
+  }
 }
 
 // The bins of the cuts, from the histogram; every thread of the workgroup gets them.
-__device__ Cut find_cut(const Hist& h, const Row& r, u64* s, Cut* out) {
+// With both filters the top-p cut is known only once the top-k one is: its bins
+// are those it can fall in, whatever of its bin top-k keeps.
+struct Bins {  // a thread's two
+  ulonglong2 w;
+  uint2 n;
+};
+
+__device__ __forceinline__ Cut find_cut(const Bins& h, const Row& r, u64* s, Cut* out) {
   const int t = threadIdx.x;
   static_assert(kBins == 2 * kThreads, "two bins a thread");
-  const u64 w0 = h.weight[2 * t], w1 = h.weight[2 * t + 1];
-  const uint32_t n0 = h.count[2 * t], n1 = h.count[2 * t + 1];
-  Cut c;
-  u64 all;
-  const u64 wb = block_scan(w0 + w1, s, &c.total), nb = block_scan((u64)n0 + n1, s, &all);
+  u64 wb = 0, nb = 0, all = 0, total = 0;
+  const u64 w0 = h.w.x, w1 = h.w.y;
+  const uint32_t n0 = h.n.x, n1 = h.n.y;
   if (t == 0) {
     out->bin_k = out->lo_p = out->hi_p = -1;
     out->n_k = out->n_p = 0;
     out->above_k = out->above_p = out->want_k = 0;
   }
-  __syncthreads();
-  const bool use_k = r.use_k && (u64)r.k < all;  // else every element with a weight is kept
-  u64 least = c.total, most = c.total;           // of the weight that top-k keeps
+  if (r.use_p) wb = block_scan(w0 + w1, s, &total);
+  if (r.use_k) nb = block_scan((u64)n0 + n1, s + kWaves, &all);
+  const u64 k = (u64)r.k;
+  const bool use_k = r.use_k && k < all;  // else every element with a weight is kept
+  u64 least = total, most = total;        // of the weight that top-k keeps
   if (use_k) {
-    const u64 k = (u64)r.k;
     if (nb < k && k <= nb + n0 + n1) {
       const bool second = nb + n0 < k;
       out->bin_k = 2 * t + second;
       out->n_k = second ? n1 : n0;
       out->above_k = wb + (second ? w0 : 0);
       out->want_k = k - nb - (second ? n0 : 0);
-      s[kWaves] = second ? w1 : w0;
+      s[2 * kWaves] = second ? w1 : w0;
     }
     __syncthreads();
     least = out->above_k;
-    most = least + s[kWaves];
+    most = least + s[2 * kWaves];
   }
   if (r.use_p) {
     const u64 p0 = bound_of(r.p, least), p1 = bound_of(r.p, most);
@@ -337,12 +382,22 @@ __device__ Cut find_cut(const Hist& h, const Row& r, u64* s, Cut* out) {
     }
     if (wb < p1 && p1 <= wb + w0 + w1) out->hi_p = 2 * t + (wb + w0 < p1);
     __syncthreads();
+    // at most: the bins' weights over the least weight in each
     const int lo = out->lo_p, hi = out->hi_p;
-    u64 n;
-    block_scan((2 * t >= lo && 2 * t <= hi ? n0 : 0) + (u64)(2 * t + 1 >= lo && 2 * t + 1 <= hi ? n1 : 0), s, &n);
-    if (t == 0) out->n_p = (uint32_t)n;
+    if (2 * t + 1 >= lo && 2 * t <= hi) {
+      u64 n = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (2 * t + j >= lo && 2 * t + j <= hi) {
+          const u64 least_w = weight_of(0.999f * expf(-(float)(2 * t + j + 1) / kBinsPerUnit));
+          n += (j ? w1 : w0) / (least_w > 0 ? least_w : 1);
+        }
+      atomicAdd(&out->n_p, (uint32_t)(n < (1u << 24) ? n : 1u << 24));
+    }
   }
   __syncthreads();
+  Cut c;
+  c.total = total;
   c.bin_k = out->bin_k;
   c.lo_p = out->lo_p;
   c.hi_p = out->hi_p;
@@ -355,16 +410,17 @@ __device__ Cut find_cut(const Hist& h, const Row& r, u64* s, Cut* out) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void q1_sample_cut(const SampleArgs a, const Ws ws, int S) {
-  __shared__ u64 s[kWaves + 1];
+__global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a, const Ws ws, int S) {
+  __shared__ u64 s[2 * kWaves + 1];
   __shared__ Cut found;
   const int64_t b = blockIdx.x / S;
   const int sl = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
-  const Row r = row_of(a, b);
-  if (!r.use_k && !r.use_p) return;
   const float top = row_top(ws, b, S);
-  if (top == -INFINITY) return;
-  const Cut c = find_cut(ws.hist[b], r, s, &found);
+  const Bins bins = {reinterpret_cast<const ulonglong2*>(ws.hist[b].weight)[threadIdx.x],
+                     reinterpret_cast<const uint2*>(ws.hist[b].count)[threadIdx.x]};
+  const Row r = row_of(a, b);
+  if ((!r.use_k && !r.use_p) || top == -INFINITY) return;
+  const Cut c = find_cut(bins, r, s, &found);
   if (sl == 0 && threadIdx.x == 0) {
     Cut* o = &ws.cut[b];
     o->total = c.total;
@@ -385,21 +441,22 @@ __global__ __launch_bounds__(kThreads) void q1_sample_cut(const SampleArgs a, co
   const int len = chunk_len(a.V, S * kWaves), ch = sl * kWaves + wave, lo = ch * len;
   const int hi = lo + len < a.V ? lo + len : (int)a.V;
   u64 sum = 0;
+  const float past = sc.past(sure > last ? sure : last);
   each<DT>(row_ptr<DT>(a, b), lo, hi, [&](int i, float x) {
+    if (!(x >= past)) return;
     const float t = sc.exponent(x);
     const int bin = bin_of(t);
     if (bin >= sure && bin > last) return;
     const float e = expf(t);
     const u64 w = weight_of(e);
-    if (w == 0) return;
     const bool low = e < r.mp;
     if (bin < sure && !low) sum += w;
-    const ulonglong2 entry = {composite(x, i), w | (low ? 1ull << 63 : 0)};
+    const ulonglong2 entry = {composite(clean(x), i), w | (low ? 1ull << 63 : 0)};
     if (bin == c.bin_k) {
       const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
       if (at < kMost) ws.cand[(b * 2) * kMost + at] = entry;
     }
-    if (bin >= c.lo_p && bin <= c.hi_p) {
+    if (w != 0 && bin >= c.lo_p && bin <= c.hi_p) {
       const uint32_t at = atomicAdd(&ws.cut[b].got_p, 1u);
       if (at < kMost) ws.cand[(b * 2 + 1) * kMost + at] = entry;
     }
@@ -408,19 +465,44 @@ __global__ __launch_bounds__(kThreads) void q1_sample_cut(const SampleArgs a, co
   if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + ch] = sum;
 }
 
+constexpr int kFew = 256;  // candidates that are ranked by comparing all pairs
+
 struct DrawShared {
   u64 comp[kMost], weight[kMost];
   u64 bins[kThreads];
-  u64 s[kWaves + 1];
+
+  u64 s[4][kWaves];  // one for each scan between barriers
   u64 pick, over;
   uint32_t left;
 };
 
 // Of the n candidates in LDS (weights with the min-p bit), largest composite
-// first: the one at which the running sum of ones or weights reaches `want`.
-// Digits of 10 bits, from the highest bit in which those left differ.
+// first: the one at which the running sum of ones or weights reaches `want`; 0 if
+// the sum stays below.  Up to kFew: each against each, four waves' shares a
+// candidate.  More: digits of 10 bits, from the highest bit in which those left differ.
 __device__ u64 select_candidate(DrawShared& d, int n, bool weighted, u64 want) {
   const int t = threadIdx.x;
+  constexpr u64 kWeight = ~(1ull << 63);
+  if (n <= kFew) {
+    const int i = t & (kFew - 1), share = t / kFew;
+    if (t < kFew) d.bins[t] = 0;
+    if (t == 0) d.pick = 0;
+    __syncthreads();
+    if (i < n) {
+      const u64 mine = d.comp[i];
+      u64 sum = 0;
+      for (int j = share; j < n; j += kThreads / kFew)
+        if (d.comp[j] > mine) sum += weighted ? d.weight[j] & kWeight : 1ull;
+      if (sum != 0) atomicAdd(&d.bins[i], sum);
+    }
+    __syncthreads();
+    if (t < n) {
+      const u64 w = weighted ? d.weight[t] & kWeight : 1ull;
+      if (d.bins[t] < want && want <= d.bins[t] + w) d.pick = d.comp[t];
+    }
+    __syncthreads();
+    return d.pick;
+  }
   u64 mask = 0, prefix = 0, before = 0;
   for (;;) {
     u64 ones = 0, zeros = 0;  // bits seen set and seen clear among those left
@@ -457,7 +539,7 @@ __device__ u64 select_candidate(DrawShared& d, int n, bool weighted, u64 want) {
     __syncthreads();
     const u64 mine = d.bins[t];
     u64 all;
-    const u64 at = before + block_scan(mine, d.s, &all);
+    const u64 at = before + block_scan(mine, d.s[0], &all);
     if (t == 0) d.pick = ~0ull;
     __syncthreads();
     if (at < want && want <= at + mine) {
@@ -552,7 +634,9 @@ __device__ void draw_from_row(const SampleArgs& a, int64_t b, const void* row, c
       if (kties == ~0ull || key_of(x) > kthr) mine += weight_of(exp_of(x, top, T));
     }
     u64 total;
+    __syncthreads();
     block_scan(mine, sw, &total);
+    __syncthreads();
     if (kties != ~0ull) {
       const uint32_t bits = kthr >> 31 ? kthr ^ 0x80000000u : ~kthr;
       total += kties * weight_of(exp_of(__uint_as_float(bits), top, T));
@@ -642,14 +726,16 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
       n = (int)c.n_k;
       load_candidates(d, ws.cand + (b * 2) * kMost, n);
       cut = select_candidate(d, n, false, c.want_k);
-      u64 mine = 0;
-      for (int i = t; i < n; i += kThreads)
-        if (d.comp[i] >= cut) mine += d.weight[i] & ~(1ull << 63);
-      block_scan(mine, d.s, &kept);
-      kept += c.above_k;
+      if (r.use_p) {
+        u64 mine = 0;
+        for (int i = t; i < n; i += kThreads)
+          if (d.comp[i] >= cut) mine += d.weight[i] & ~(1ull << 63);
+        block_scan(mine, d.s[1], &kept);
+        kept += c.above_k;
+      }
     }
     if (r.use_p) {
-      n = (int)c.n_p;
+      n = (int)c.got_p;
       load_candidates(d, ws.cand + (b * 2 + 1) * kMost, n);
       cut = select_candidate(d, n, true, bound_of(r.p, kept) - c.above_p);
     }
@@ -663,7 +749,7 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
     if (d.comp[i] >= cut && !(d.weight[i] >> 63)) atomicAdd(&d.bins[~(uint32_t)d.comp[i] / (uint32_t)len], d.weight[i]);
   __syncthreads();
   u64 total;
-  const u64 mine = d.bins[t], start = block_scan(mine, d.s, &total);
+  const u64 mine = d.bins[t], start = block_scan(mine, d.s[2], &total);
   const float u = a.u[b];
   u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
   if (at >= total) at = total - 1;
@@ -686,7 +772,7 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
   u64 sum = 0;
   for (int i = i0; i < i1; ++i) sum += weight(i);
   u64 all;
-  u64 c = block_scan(sum, d.s, &all);
+  u64 c = block_scan(sum, d.s[3], &all);
   if (want >= c && want < c + sum)
     for (int i = i0; i < i1; ++i) {
       const u64 w = weight(i);
