@@ -2,17 +2,21 @@
 delta rule, attention over a shared prefix and the sampler.
 
 Argument marshalling only, like ``q1.py``: every operation runs in the library's
-HIP kernels on the current stream of its tensors' device.
+HIP kernels on the current stream of its tensors' device.  The calls are as short
+as the kernels of a single token, so what the checks of the operands' shapes,
+strides and types found is kept by those (never by a tensor or its address), and
+descriptors are packed at once.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
 
-from .q1 import _TORCH_TO_Q1, _check, _stream, load_library
+from .q1 import _TORCH_TO_Q1, _check, _raw_stream, load_library
 
 
 class _Delta(ctypes.Structure):
@@ -35,23 +39,29 @@ class _Attn(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
-class _Scratch:
-    """Device workspaces of these calls (no initial contents needed), one per
+_DELTA_PACK = struct.Struct("@3P3q5Pq7if").pack  # the fields of _Delta
+_ATTN_PACK = struct.Struct("@9P7q5if").pack      # the fields of _Attn
+
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty
+
+
+def _stream_of(index: int) -> int:
+    """The current HIP stream of a device."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+_scratch = {}
+
+
+def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
+    """Device workspace of these calls (no initial contents needed), one per
     (device, stream), grown on demand."""
-
-    def __init__(self):
-        self._ws = {}
-
-    def get(self, nbytes: int, device: torch.device) -> torch.Tensor:
-        key = (device.index, _stream(device).value)
-        t = self._ws.get(key)
-        if t is None or t.numel() < nbytes:
-            t = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
-            self._ws[key] = t
-        return t
-
-
-_SCRATCH = _Scratch()
+    t = _scratch.get((index, stream))
+    if t is None or t.numel() < nbytes:
+        t = _empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", index))
+        _scratch[index, stream] = t
+    return t
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -100,31 +110,56 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype):
+def _check_delta(q, k, v, g, beta, state, slots, nseq, out, out_dtype):
+    """The descriptor's fields that follow from the operands' layouts."""
     _same_device(q, k=k, v=v, g=g, beta=beta, state=state, slots=slots, out=out)
     lead = q.dim() - 2
     rows, Hk, Dk = q.shape[:lead], q.shape[-2], q.shape[-1]
-    Hv, Dv = v.shape[-2], v.shape[-1]
     if k.shape != q.shape:
         raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
     if v.dim() != q.dim() or v.shape[:lead] != rows:
         raise ValueError(f"v has shape {tuple(v.shape)}, q {tuple(q.shape)}")
+    Hv, Dv = v.shape[-2], v.shape[-1]
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype")
     _dense(g, "g", torch.float32, (*rows, Hv))
     _dense(beta, "beta", torch.float32, (*rows, Hv))
+    if state.dim() != 4:
+        raise ValueError("state must be [slots, Hv, Dk, Dv]")
     _dense(state, "state", torch.float32, (state.shape[0], Hv, Dk, Dv))
     if slots is not None:
         _dense(slots, "slots", torch.int32, (nseq,))
-    if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype if out_dtype is None else out_dtype, device=v.device)
-    else:
+    if out is not None:
         _dense(out, "out", out.dtype if out_dtype is None else out_dtype, v.shape)
-    d = _Delta(q.data_ptr(), k.data_ptr(), v.data_ptr(), _row_stride(q, "q", lead), _row_stride(k, "k", lead),
-               _row_stride(v, "v", lead), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _ptr(slots), out.data_ptr(),
-               state.shape[0], Hk, Hv, Dk, Dv, _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out.dtype, -1),
-               1 if l2norm else 0, Dk ** -0.5 if scale is None else scale)
-    return d, out
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = v.dtype
+    lds = (_row_stride(q, "q", lead), _row_stride(k, "k", lead), _row_stride(v, "v", lead))
+    return (lds, (state.shape[0], Hk, Hv, Dk, Dv, _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out_dtype, -1)),
+            out_dtype, Dk ** -0.5, q.get_device())
+
+
+_delta_layouts = {}
+
+
+def _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype):
+    key = (q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, g.shape,
+           g.stride(), g.dtype, beta.shape, beta.stride(), beta.dtype, state.shape, state.stride(), state.dtype,
+           q.get_device(), k.get_device(), v.get_device(), g.get_device(), beta.get_device(), state.get_device(),
+           None if slots is None else (slots.shape, slots.stride(), slots.dtype, slots.get_device()), nseq,
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()), out_dtype, _device())
+    found = _delta_layouts.get(key)
+    if found is None:
+        found = _check_delta(q, k, v, g, beta, state, slots, nseq, out, out_dtype)
+        if len(_delta_layouts) > 4096:
+            _delta_layouts.clear()
+        _delta_layouts[key] = found
+    lds, ints, dtype, usual, index = found
+    if out is None:
+        out = _empty(v.shape, dtype=dtype, device=v.device)
+    return _DELTA_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), *lds, g.data_ptr(), beta.data_ptr(), state.data_ptr(),
+                       0 if slots is None else slots.data_ptr(), out.data_ptr(), *ints, 1 if l2norm else 0,
+                       usual if scale is None else scale), out, index
 
 
 def q1_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -141,8 +176,10 @@ def q1_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hk, Dk]")
     B, T = q.shape[0], q.shape[1]
-    d, out = _delta(q, k, v, g, beta, state, slots, B, scale, l2norm, out, out_dtype)
-    _check(load_library().q1_delta_step(ctypes.byref(d), B, T, _stream(q.device)))
+    d, out, index = _delta(q, k, v, g, beta, state, slots, B, scale, l2norm, out, out_dtype)
+    status = load_library().q1_delta_step(d, B, T, _stream_of(index))
+    if status:
+        _check(status)
     return out
 
 
@@ -158,15 +195,21 @@ def q1_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
         raise ValueError("q must be [tokens, Hk, Dk]")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [nseq + 1]")
-    nseq = cu_seqlens.numel() - 1
-    _dense(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,))
-    _same_device(q, cu_seqlens=cu_seqlens)
-    d, out = _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype)
+    nseq, tokens = cu_seqlens.numel() - 1, q.shape[0]
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32")
+    d, out, index = _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype)
+    if cu_seqlens.get_device() != index:
+        raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, q on {q.device}")
     L = load_library()
-    need = L.q1_delta_prefill_workspace_bytes(ctypes.byref(d), q.shape[0], nseq)
-    ws = workspace if workspace is not None else (_SCRATCH.get(need, q.device) if need else None)
-    _check(L.q1_delta_prefill(ctypes.byref(d), q.shape[0], nseq, cu_seqlens.data_ptr(), _ptr(ws),
-                              0 if ws is None else ws.numel(), _stream(q.device)))
+    stream = _stream_of(index)
+    if workspace is None:
+        need = L.q1_delta_prefill_workspace_bytes(d, tokens, nseq)
+        workspace = _workspace(need, index, stream) if need else None
+    status = L.q1_delta_prefill(d, tokens, nseq, cu_seqlens.data_ptr(), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), stream)
+    if status:
+        _check(status)
     return out
 
 
@@ -189,6 +232,47 @@ def q1_prefix_attn(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix: 
     spaced rows) or None; k_pages, v_pages ``[pages, page_size, Hkv, D]``,
     page_table int32 ``[B, max_pages]`` and suffix_lens int32 ``[B]``, or None.
     ``scale`` defaults to D^-1/2."""
+    key = (q.shape, q.stride(), q.dtype, q.get_device(), out_dtype, _device(),
+           None if k_prefix is None else (k_prefix.shape, k_prefix.stride(), k_prefix.dtype, k_prefix.get_device()),
+           None if v_prefix is None else (v_prefix.shape, v_prefix.stride(), v_prefix.dtype, v_prefix.get_device()),
+           None if k_pages is None else (k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device()),
+           None if v_pages is None else (v_pages.shape, v_pages.stride(), v_pages.dtype, v_pages.get_device()),
+           None if page_table is None else (page_table.shape, page_table.stride(), page_table.dtype, page_table.get_device()),
+           None if suffix_lens is None else (suffix_lens.shape, suffix_lens.stride(), suffix_lens.dtype, suffix_lens.get_device()),
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()),
+           None if lse is None else (lse.shape, lse.stride(), lse.dtype, lse.get_device()))
+    found = _attn_layouts.get(key)
+    if found is None:
+        found = _check_attn(q, k_prefix, v_prefix, k_pages, v_pages, page_table, suffix_lens, out, out_dtype, lse)
+        if len(_attn_layouts) > 4096:
+            _attn_layouts.clear()
+        _attn_layouts[key] = found
+    longs, ints, dtype, usual, index = found
+    P, pages, max_pages = longs[3], longs[4], longs[5]
+    if out is None:
+        out = _empty(q.shape, dtype=dtype, device=q.device)
+    if lse is None:
+        lse = _empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    a = _ATTN_PACK(q.data_ptr(), k_prefix.data_ptr() if P else 0, v_prefix.data_ptr() if P else 0,
+                   k_pages.data_ptr() if pages else 0, v_pages.data_ptr() if pages else 0,
+                   page_table.data_ptr() if max_pages else 0, suffix_lens.data_ptr() if max_pages else 0,
+                   out.data_ptr(), lse.data_ptr(), *longs, *ints, usual if scale is None else scale)
+    L = load_library()
+    stream = _stream_of(index)
+    if workspace is None:
+        need = L.q1_prefix_attn_workspace_bytes(a)
+        workspace = _workspace(need, index, stream) if need else None
+    status = L.q1_prefix_attn(a, _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
+    if status:
+        _check(status)
+    return out, lse
+
+
+_attn_layouts = {}
+
+
+def _check_attn(q, k_prefix, v_prefix, k_pages, v_pages, page_table, suffix_lens, out, out_dtype, lse):
+    """The descriptor's fields that follow from the operands' layouts."""
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
     _same_device(q, k_prefix=k_prefix, v_prefix=v_prefix, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
@@ -220,25 +304,15 @@ def q1_prefix_attn(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix: 
         _dense(suffix_lens, "suffix_lens", torch.int32, (B,))
     if any(t is not None and t.dtype != q.dtype for t in (k_prefix, v_prefix)):
         raise ValueError("q, keys and values must have one dtype")
-    if out is None:
-        out = torch.empty(B, Hq, D, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
-    else:
+    if out is not None:
         _dense(out, "out", out.dtype if out_dtype is None else out_dtype, (B, Hq, D))
-    if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-    else:
-        _dense(lse, "lse", torch.float32, (B, Hq))
-    a = _Attn(q.data_ptr(), _ptr(k_prefix) if P else None, _ptr(v_prefix) if P else None,
-              _ptr(k_pages) if pages else None, _ptr(v_pages) if pages else None,
-              _ptr(page_table) if max_pages else None, _ptr(suffix_lens) if max_pages else None, out.data_ptr(),
-              lse.data_ptr(), _row_stride(q, "q", 1), prefix_ld, B, P, pages, max_pages, page_size, Hq, Hkv, D,
-              _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out.dtype, -1),
-              1.0 / math.sqrt(D) if scale is None else scale)
-    L = load_library()
-    need = L.q1_prefix_attn_workspace_bytes(ctypes.byref(a))
-    ws = workspace if workspace is not None else (_SCRATCH.get(need, q.device) if need else None)
-    _check(L.q1_prefix_attn(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream(q.device)))
-    return out, lse
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = q.dtype
+    _dense(lse, "lse", torch.float32, (B, Hq))
+    return ((_row_stride(q, "q", 1), prefix_ld, B, P, pages, max_pages, page_size),
+            (Hq, Hkv, D, _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out_dtype, -1)), out_dtype, 1.0 / math.sqrt(D),
+            q.get_device())
 
 
 def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
@@ -250,6 +324,42 @@ def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch
     ``[B]`` int64, or the dtype of ``tokens``; logprob fp32 ``[B]``).  The
     filters are per row: temperature, top_p, min_p fp32 and top_k int32, all
     ``[B]`` on the device, or None for off."""
+    key = (logits.shape, logits.stride(), logits.dtype, logits.get_device(), u.shape, u.stride(), u.dtype,
+           u.get_device(), _device(),
+           None if temperature is None else (temperature.shape, temperature.stride(), temperature.dtype, temperature.get_device()),
+           None if top_k is None else (top_k.shape, top_k.stride(), top_k.dtype, top_k.get_device()),
+           None if top_p is None else (top_p.shape, top_p.stride(), top_p.dtype, top_p.get_device()),
+           None if min_p is None else (min_p.shape, min_p.stride(), min_p.dtype, min_p.get_device()),
+           None if tokens is None else (tokens.shape, tokens.stride(), tokens.dtype, tokens.get_device()),
+           None if logprob is None else (logprob.shape, logprob.stride(), logprob.dtype, logprob.get_device()))
+    L = load_library()
+    found = _sample_layouts.get(key)
+    if found is None:
+        found = _check_sample(L, logits, u, temperature, top_k, top_p, min_p, tokens, logprob)
+        if len(_sample_layouts) > 4096:
+            _sample_layouts.clear()
+        _sample_layouts[key] = found
+    B, V, ld, dtype, need, index = found
+    if tokens is None:
+        tokens = _empty(B, dtype=torch.int64, device=logits.device)
+    if logprob is None:
+        logprob = _empty(B, dtype=torch.float32, device=logits.device)
+    stream = _stream_of(index)
+    if workspace is None and need:
+        workspace = _workspace(need, index, stream)
+    status = L.q1_sample(logits.data_ptr(), dtype, B, V, ld, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                         _ptr(min_p), tokens.data_ptr(), 1 if tokens.dtype == torch.int64 else 0, logprob.data_ptr(),
+                         _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
+    if status:
+        _check(status)
+    return tokens, logprob
+
+
+_sample_layouts = {}
+
+
+def _check_sample(L, logits, u, temperature, top_k, top_p, min_p, tokens, logprob):
+    """What follows from the operands' layouts: (B, V, row stride, dtype, workspace bytes, device)."""
     if logits.dim() != 2:
         raise ValueError("logits must be [B, V]")
     _same_device(logits, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
@@ -260,21 +370,10 @@ def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch
     _dense(top_k, "top_k", torch.int32, (B,))
     _dense(top_p, "top_p", torch.float32, (B,))
     _dense(min_p, "min_p", torch.float32, (B,))
-    if tokens is None:
-        tokens = torch.empty(B, dtype=torch.int64, device=logits.device)
-    elif tokens.dtype not in (torch.int32, torch.int64):
-        raise ValueError("tokens must be int32 or int64")
-    else:
+    if tokens is not None:
+        if tokens.dtype not in (torch.int32, torch.int64):
+            raise ValueError("tokens must be int32 or int64")
         _dense(tokens, "tokens", tokens.dtype, (B,))
-    if logprob is None:
-        logprob = torch.empty(B, dtype=torch.float32, device=logits.device)
-    else:
-        _dense(logprob, "logprob", torch.float32, (B,))
-    L = load_library()
-    need = L.q1_sample_workspace_bytes(B, V)
-    ws = workspace if workspace is not None else (_SCRATCH.get(need, logits.device) if need else None)
-    _check(L.q1_sample(logits.data_ptr(), _TORCH_TO_Q1.get(logits.dtype, -1), B, V, _row_stride(logits, "logits", 1),
-                       u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), tokens.data_ptr(),
-                       1 if tokens.dtype == torch.int64 else 0, logprob.data_ptr(), _ptr(ws),
-                       0 if ws is None else ws.numel(), _stream(logits.device)))
-    return tokens, logprob
+    _dense(logprob, "logprob", torch.float32, (B,))
+    return (B, V, _row_stride(logits, "logits", 1), _TORCH_TO_Q1.get(logits.dtype, -1),
+            L.q1_sample_workspace_bytes(B, V) if V > 0 else 0, logits.get_device())
