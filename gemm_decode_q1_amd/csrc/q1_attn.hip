@@ -3,20 +3,22 @@
 // Two launches: q1_attn_main computes, per work item, the running maximum m,
 // sum l and unnormalised output o of some query rows over some tokens;
 // q1_attn_join adds the items of a row.  A prefix item holds the rows of all
-// sequences that share a key/value head (B * Hq/Hkv of them, in blocks of 16 NM),
-// so a prefix token is read once per block and not once per sequence; a suffix
-// item holds the Hq/Hkv rows of one sequence.  Tokens are split over items so that
-// the launch has about one workgroup per compute unit (see plan_prefix_attn).
+// sequences that share a key/value head (B * Hq/Hkv of them, in blocks), so a
+// prefix token is read once per block and not once per sequence; a suffix item
+// holds the Hq/Hkv rows of one sequence.  Tokens are split over items so that the
+// launch fills the compute units (see plan_prefix_attn).
 //
-// In an item each of the 4 waves takes every fourth tile of 32 tokens, by itself,
-// with all the rows:
-//   S^T = K Q^T   keys are the A operand, straight from memory (lane: token l%16,
-//                 8 consecutive elements); queries the B operand, in registers.
+// An item has one of two forms.  By tokens (few rows: the bound is reading): each
+// of the 4 waves takes every fourth tile of 32 tokens, by itself, with all the
+// rows, and the waves are joined in LDS.  By rows (many): the waves share a tile
+// in LDS, two tiles in turn, and each has rows of its own.  Either way, per tile:
+//   S^T = K Q^T   keys are the A operand (lane: token l%16, 8 consecutive
+//                 elements), queries the B operand.
 //   softmax       a lane has one query (l%16) and 8 tokens: maximum and sum are
 //                 in-lane, then over 4 lanes.
 //   O^T = V^T P^T the weights come out of S^T as the B operand's layout (tokens
-//                 4(l/16)..+3 of both 16-token halves); values go through a
-//                 wave's own LDS tile and come back transposed (ds_read_tr16).
+//                 4(l/16)..+3 of both 16-token halves); values lie in LDS as rows
+//                 and come back transposed (ds_read_tr16).
 // Weights enter the second product as two 16-bit parts (high and remainder), so
 // that their rounding (2^-17) stays below the output's; their sum, the maximum
 // and the output are fp32.  Values and keys of tokens past the length are never
@@ -105,73 +107,118 @@ __device__ __forceinline__ int64_t suffix_len(const q1_attn& a, int64_t b) {
 template <bool F16>
 constexpr float kLift = F16 ? 12.0f : 0.0f;
 
+// The softmax of one tile for a block of 16 queries: scores of this lane's 8 tokens
+// (those of `mine`) in, weights out as two operands; m, l and the output so far
+// are brought to the new maximum.
+template <bool F16, int DT>
+__device__ __forceinline__ void weigh(const f32x4* S, uint32_t mine, float sc, float& m, float& l, f32x4* O, int stride,
+                                      u32x4& hi, u32x4& lo) {
+  float s[8], top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s[j] = (mine >> j) & 1u ? S[j >> 2][j & 3] * sc : -INFINITY;
+    top = fmaxf(top, s[j]);
+  }
+  const float mn = fmaxf(m, max_groups(top));
+  const float base = mn == -INFINITY ? 0.f : mn;  // no token yet: every exponent below is -infinity
+  if (__any(mn != m)) {
+    const float keep = __builtin_amdgcn_exp2f(m - base);
+    l *= keep;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[d * stride] *= keep;
+    m = mn;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    s[j] = __builtin_amdgcn_exp2f(s[j] - base + kLift<F16>);
+    l += s[j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float rx, ry, r0, r1;
+    hi[j] = round2<F16>(s[2 * j], s[2 * j + 1], &rx, &ry);
+    lo[j] = round2<F16>(rx, ry, &r0, &r1);
+  }
+}
+
+// 16 columns of 32 value rows as the A operand V^T; `at`: this lane's place in rows
+// 4 (l/16) .. +3 (of 16), `next16`: bytes to the other 16 rows.
+__device__ __forceinline__ u32x4 transposed(const unsigned char* at, int next16) {
+  const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+  const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + next16));
+  const uint2 xw = __builtin_bit_cast(uint2, x), yw = __builtin_bit_cast(uint2, y);
+  return u32x4{xw.x, xw.y, yw.x, yw.y};
+}
+
+// Rows of an item: row r of its R belongs to (sequence, query head).
+struct Rows {
+  int64_t b0;
+  int hk, group, R, row0;
+  bool prefix;
+  __device__ __forceinline__ int64_t seq(int r) const { return prefix ? r / group : b0; }
+  __device__ __forceinline__ int head(int r) const { return hk * group + (prefix ? r % group : r); }
+};
+
+template <int D>
+__device__ __forceinline__ u32x4 load_q(const q1_attn& a, const Rows& w, int r, int s, int grp) {
+  if (r >= w.R) return u32x4{0u, 0u, 0u, 0u};
+  return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + w.seq(r) * a.q_ld + (int64_t)w.head(r) * D +
+                                         32 * s + 8 * grp);
+}
+
+// Queries stay in registers where they fit beside the output (D = 256: in LDS).
+template <int D>
+constexpr bool kQueriesInLds = D == 256;
+
+template <int D, int NM>
+constexpr int kTokenLds() {
+  constexpr int q = kQueriesInLds<D> ? 16 * NM * (2 * D + 16) : 0;
+  constexpr int vt = kWaves * kTile * (2 * D + 32) + q, jo = kWaves * 16 * NM * ((D + 4) * 4 + 8);
+  return vt > jo ? vt : jo;
+}
+
+template <int D>
+constexpr int kRowLds() {
+  return 2 * kTile * ((2 * D + 16) + (2 * D + 32));
+}
+
+// An item by tokens.
 template <bool F16, int D, int NM>
-__global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, const AttnPlan p, float* part_o,
-                                                            float2* part_ml) {
+__device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, int64_t t0, int64_t t1, int64_t base,
+                                               float* part_o, float2* part_ml, unsigned char* lds) {
   constexpr int KS = D / 32, DT = D / 16, VROW = 2 * D + 32;  // LDS bytes of a value row: rows start 8 banks apart
   constexpr int VCH = D / 8, VPI = 64 / VCH, VN = kTile / VPI;  // 16-byte pieces a row, rows and loads of a value tile
-  extern __shared__ __align__(16) unsigned char lds[];
+  constexpr bool QL = kQueriesInLds<D>;
+  constexpr int QROW = 2 * D + 16;
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so the loop they are in must be a scalar one
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = a.Hq / a.Hkv;
-
-  // The item: its rows, tokens and where its results go.
-  int64_t b0 = 0, t0, t1;  // suffix: the sequence; tokens
-  int hk, R, rb, split;
-  const bool prefix = blockIdx.x < (unsigned)p.prefix_wgs;
-  if (prefix) {
-    // blocks of rows over the same tokens are 8 workgroups apart: the same XCD's L2
-    const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
-    rb = y % p.prefix_rb;
-    const int pair = (y / p.prefix_rb) * 8 + x;
-    if (pair >= a.Hkv * p.prefix_splits) return;
-    hk = pair % a.Hkv;
-    split = pair / a.Hkv;
-    R = (int)a.B * group;
-    t0 = (int64_t)split * p.prefix_tokens;
-    t1 = t0 + p.prefix_tokens < a.P ? t0 + p.prefix_tokens : a.P;
+  const int live = (w.R - w.row0 + 15) / 16 < NM ? (w.R - w.row0 + 15) / 16 : NM;
+  unsigned char* const ql = lds + kWaves * kTile * VROW;
+  u32x4 Q[QL ? 1 : NM][QL ? 1 : KS];
+  if constexpr (QL) {
+    for (int i = threadIdx.x; i < 16 * NM * VCH; i += 64 * kWaves) {
+      const int r = i / VCH, c = i % VCH;
+      *reinterpret_cast<u32x4*>(ql + r * QROW + 16 * c) = load_q<D>(a, w, w.row0 + r, c >> 2, c & 3);
+    }
+    __syncthreads();
   } else {
-    int64_t i = blockIdx.x - p.prefix_wgs;
-    hk = (int)(i % a.Hkv);
-    i /= a.Hkv;
-    rb = (int)(i % p.suffix_rb);
-    i /= p.suffix_rb;
-    split = (int)(i % p.suffix_splits);
-    b0 = i / p.suffix_splits;
-    R = group;
-    const int64_t n = suffix_len(a, b0);
-    t0 = (int64_t)split * p.suffix_tokens;
-    t1 = t0 + p.suffix_tokens < n ? t0 + p.suffix_tokens : n;
-    split += p.prefix_splits;
-    if (t0 >= t1) return;
-  }
-  const int row0 = rb * 16 * NM, live = (R - row0 + 15) / 16 < NM ? (R - row0 + 15) / 16 : NM;
-  auto out_row = [&](int r) -> int64_t {  // r < R
-    return prefix ? (int64_t)(r / group) * a.Hq + hk * group + r % group : b0 * a.Hq + hk * group + r;
-  };
-
-  u32x4 Q[NM][KS];
 #pragma unroll
-  for (int n = 0; n < NM; ++n) {
-    const int r = row0 + 16 * n + col;
-    const int64_t b = prefix ? r / group : b0;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_ld + (int64_t)(hk * group + (prefix ? r % group : r)) * D + 8 * grp;
+    for (int n = 0; n < NM; ++n)
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      Q[n][s] = r < R ? *reinterpret_cast<const u32x4*>(q + 32 * s) : u32x4{0u, 0u, 0u, 0u};
+      for (int s = 0; s < KS; ++s) Q[n][s] = load_q<D>(a, w, w.row0 + 16 * n + col, s, grp);
   }
 
-  const auto* kb = static_cast<const uint16_t*>(prefix ? a.k_prefix : a.k_pages) + (int64_t)hk * D;
-  const auto* vb = static_cast<const uint16_t*>(prefix ? a.v_prefix : a.v_pages) + (int64_t)hk * D;
-  const int64_t ld = prefix ? a.prefix_ld : (int64_t)a.Hkv * D;
+  const auto* kb = static_cast<const uint16_t*>(w.prefix ? a.k_prefix : a.k_pages) + (int64_t)w.hk * D;
+  const auto* vb = static_cast<const uint16_t*>(w.prefix ? a.v_prefix : a.v_pages) + (int64_t)w.hk * D;
+  const int64_t ld = w.prefix ? a.prefix_ld : (int64_t)a.Hkv * D;
   // Row of token t0 + (lane % 32) of the tile at t, or -1.
   auto row_of = [&](int64_t t) -> int {
     const int64_t tok = t + (lane & 31);
     if (tok >= t1) return -1;
-    if (prefix) return (int)tok;
+    if (w.prefix) return (int)tok;
     const uint32_t ps = (uint32_t)a.page_size, pg = (uint32_t)tok / ps;
-    const int id = a.page_table[b0 * a.max_pages + pg];
+    const int id = a.page_table[w.b0 * a.max_pages + pg];
     return id < 0 || id >= a.pages ? -1 : (int)((int64_t)id * ps + ((uint32_t)tok - pg * ps));
   };
 
@@ -217,17 +264,22 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, con
   for (; t < t1; t += kStep) {
     const int have = rows;
     // scores, then the next tile's rows and keys
-    f32x4 S[2][NM];
+    f32x4 S[NM][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int n = 0; n < NM; ++n)
 #pragma unroll
-      for (int n = 0; n < NM; ++n) {
-        S[h][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int h = 0; h < 2; ++h) S[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int n = 0; n < NM; ++n)
         if (n < live) {
+          u32x4 q;
+          if constexpr (QL) q = *reinterpret_cast<const u32x4*>(ql + (16 * n + col) * QROW + 64 * s + 16 * grp);
+          else q = Q[n][s];
 #pragma unroll
-          for (int s = 0; s < KS; ++s) S[h][n] = mma<F16>(K[h][s], Q[n][s], S[h][n]);
+          for (int h = 0; h < 2; ++h) S[n][h] = mma<F16>(K[h][s], q, S[n][h]);
         }
-      }
     const int64_t tn = t + kStep;
     if (tn < t1) {
       rows = row_of(tn);
@@ -242,48 +294,18 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, con
     const uint32_t mine = ((uint32_t)in >> (4 * grp) & 15u) | ((uint32_t)in >> (16 + 4 * grp) & 15u) << 4;
     u32x4 hi[NM], lo[NM];
 #pragma unroll
-    for (int n = 0; n < NM; ++n) {
-      if (n >= live) continue;
-      float s[8], top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j] = (mine >> j) & 1u ? S[j >> 2][n][j & 3] * sc : -INFINITY;
-        top = fmaxf(top, s[j]);
-      }
-      const float mn = fmaxf(m[n], max_groups(top));
-      const float base = mn == -INFINITY ? 0.f : mn;  // no token yet: every exponent below is -infinity
-      if (__any(mn != m[n])) {
-        const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-        l[n] *= keep;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) O[d][n] *= keep;
-        m[n] = mn;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j] = __builtin_amdgcn_exp2f(s[j] - base + kLift<F16>);
-        l[n] += s[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float rx, ry, r0, r1;
-        hi[n][j] = round2<F16>(s[2 * j], s[2 * j + 1], &rx, &ry);
-        lo[n][j] = round2<F16>(rx, ry, &r0, &r1);
-      }
-    }
+    for (int n = 0; n < NM; ++n)
+      if (n < live) weigh<F16, DT>(S[n], mine, sc, m[n], l[n], &O[0][n], NM, hi[n], lo[n]);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vr + 32 * d));
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vr + 16 * VROW + 32 * d));
-      const uint2 xw = __builtin_bit_cast(uint2, x), yw = __builtin_bit_cast(uint2, y);
-      const u32x4 vt4 = {xw.x, xw.y, yw.x, yw.y};
+      const u32x4 v = transposed(vr + 32 * d, 16 * VROW);
 #pragma unroll
       for (int n = 0; n < NM; ++n)
-        if (n < live) {
-          O[d][n] = mma<F16>(vt4, hi[n], O[d][n]);
-          O[d][n] = mma<F16>(vt4, lo[n], O[d][n]);
-        }
+        if (n < live) O[d][n] = mma<F16>(v, hi[n], O[d][n]);
+#pragma unroll
+      for (int n = 0; n < NM; ++n)
+        if (n < live) O[d][n] = mma<F16>(v, lo[n], O[d][n]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -302,25 +324,163 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_main(const q1_attn a, con
     for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = O[d][n];
   }
   __syncthreads();
-  const int64_t base = (int64_t)split * a.B * a.Hq;
   for (int i = threadIdx.x; i < 16 * live * (D / 4); i += 64 * kWaves) {
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    if (row0 + r >= R) continue;
+    if (w.row0 + r >= w.R) continue;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sml[w * 16 * NM + r].x);
+    for (int v = 0; v < kWaves; ++v) top = fmaxf(top, sml[v * 16 * NM + r].x);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float2 ml = sml[w * 16 * NM + r];
+    for (int v = 0; v < kWaves; ++v) {
+      const float2 ml = sml[v * 16 * NM + r];
       const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-      o += f * *reinterpret_cast<const f32x4*>(so + (w * 16 * NM + r) * OROW + c);
+      o += f * *reinterpret_cast<const f32x4*>(so + (v * 16 * NM + r) * OROW + c);
       sum += f * ml.y;
     }
-    const int64_t at = base + out_row(row0 + r);
+    const int64_t at = base + w.seq(w.row0 + r) * a.Hq + w.head(w.row0 + r);
     *reinterpret_cast<f32x4*>(part_o + at * D + c) = o;
     if (c == 0) part_ml[at] = float2{top, sum};
+  }
+}
+
+// A prefix item by rows: wave w has rows row0 + 16 NM w .. of the item's.
+template <bool F16, int D, int NM>
+__device__ __forceinline__ void item_by_rows(const q1_attn& a, const Rows& w, int64_t t0, int64_t t1, int64_t base,
+                                             float* part_o, float2* part_ml, unsigned char* lds) {
+  constexpr int KS = D / 32, DT = D / 16, KROW = 2 * D + 16, VROW = 2 * D + 32, BUF = kTile * (KROW + VROW);
+  constexpr int CH = D / 8, N = kTile * CH / (64 * kWaves);  // 16-byte pieces a row, loads of a tile per thread
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
+  const int row0 = w.row0 + 16 * NM * __builtin_amdgcn_readfirstlane(tid >> 6);
+  u32x4 Q[NM][KS];
+#pragma unroll
+  for (int n = 0; n < NM; ++n)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) Q[n][s] = load_q<D>(a, w, row0 + 16 * n + col, s, grp);
+  const auto* kb = static_cast<const uint16_t*>(a.k_prefix) + (int64_t)w.hk * D;
+  const auto* vb = static_cast<const uint16_t*>(a.v_prefix) + (int64_t)w.hk * D;
+  u32x4 K[N], V[N];
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t tok = t + (i * 64 * kWaves + tid) / CH;
+      const int64_t at = tok * a.prefix_ld + 8 * (tid % CH);
+      K[i] = tok < t1 ? *reinterpret_cast<const u32x4*>(kb + at) : u32x4{0u, 0u, 0u, 0u};
+      V[i] = tok < t1 ? *reinterpret_cast<const u32x4*>(vb + at) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  auto put = [&](unsigned char* buf) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = (i * 64 * kWaves + tid) / CH, c = tid % CH;
+      *reinterpret_cast<u32x4*>(buf + r * KROW + 16 * c) = K[i];
+      *reinterpret_cast<u32x4*>(buf + kTile * KROW + r * VROW + 16 * c) = V[i];
+    }
+  };
+  f32x4 O[NM][DT];
+  float m[NM], l[NM];
+#pragma unroll
+  for (int n = 0; n < NM; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const float sc = a.scale * kLog2e;
+  load(t0);
+  put(lds);
+  load(t0 + kTile);
+  __syncthreads();
+  int at = 0;
+  for (int64_t t = t0; t < t1; t += kTile, at ^= BUF) {
+    // the next tile to the other buffer, the one after it into registers
+    put(lds + (at ^ BUF));
+    load(t + 2 * kTile);
+    const unsigned char* buf = lds + at;
+    f32x4 S[NM][2];
+#pragma unroll
+    for (int n = 0; n < NM; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) S[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(buf + (16 * h + col) * KROW + 64 * s + 16 * grp);
+#pragma unroll
+        for (int n = 0; n < NM; ++n) S[n][h] = mma<F16>(k, Q[n][s], S[n][h]);
+      }
+    const uint32_t in = t1 - t >= kTile ? ~0u : (1u << (int)(t1 - t)) - 1u;
+    const uint32_t mine = (in >> (4 * grp) & 15u) | (in >> (16 + 4 * grp) & 15u) << 4;
+    u32x4 hi[NM], lo[NM];
+#pragma unroll
+    for (int n = 0; n < NM; ++n) weigh<F16, DT>(S[n], mine, sc, m[n], l[n], &O[n][0], 1, hi[n], lo[n]);
+    const unsigned char* vr = buf + kTile * KROW + (4 * grp + col / 4) * VROW + 8 * (col & 3);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const u32x4 v = transposed(vr + 32 * d, 16 * VROW);
+#pragma unroll
+      for (int n = 0; n < NM; ++n) O[n][d] = mma<F16>(v, hi[n], O[n][d]);
+#pragma unroll
+      for (int n = 0; n < NM; ++n) O[n][d] = mma<F16>(v, lo[n], O[n][d]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int n = 0; n < NM; ++n) {
+    const int r = row0 + 16 * n + col;
+    const float sum = sum_groups(l[n]);
+    if (r >= w.R) continue;
+    const int64_t out = base + w.seq(r) * a.Hq + w.head(r);
+    if (grp == 0) part_ml[out] = float2{m[n], sum};
+#pragma unroll
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(part_o + out * D + 16 * d + 4 * grp) = O[n][d];
+  }
+}
+
+// NM: blocks of 16 rows of an item (by rows: of each wave of a prefix item).
+template <bool F16, int D, int NM, bool BYROWS>
+__global__ __launch_bounds__(64 * kWaves, BYROWS || NM * D > 256 ? 1 : 2) void q1_attn_main(const q1_attn a, const AttnPlan p, float* part_o, float2* part_ml) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  Rows w;
+  w.group = a.Hq / a.Hkv;
+  w.prefix = blockIdx.x < (unsigned)p.prefix_wgs;
+  w.b0 = 0;
+  int64_t t0, t1;
+  int split;
+  if (w.prefix) {
+    // blocks of rows over the same tokens are 8 workgroups apart: the same XCD's L2
+    const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+    const int pair = (y / p.prefix_rb) * 8 + x;
+    if (pair >= a.Hkv * p.prefix_splits) return;
+    w.hk = pair % a.Hkv;
+    split = pair / a.Hkv;
+    w.R = (int)a.B * w.group;
+    w.row0 = (y % p.prefix_rb) * (BYROWS ? 16 * NM * kWaves : 16 * NM);
+    t0 = (int64_t)split * p.prefix_tokens;
+    t1 = t0 + p.prefix_tokens < a.P ? t0 + p.prefix_tokens : a.P;
+  } else {
+    int64_t i = blockIdx.x - p.prefix_wgs;
+    w.hk = (int)(i % a.Hkv);
+    i /= a.Hkv;
+    w.row0 = (int)(i % p.suffix_rb) * (BYROWS ? 16 : 16 * NM);
+    i /= p.suffix_rb;
+    split = (int)(i % p.suffix_splits);
+    w.b0 = i / p.suffix_splits;
+    w.R = w.group;
+    const int64_t n = suffix_len(a, w.b0);
+    t0 = (int64_t)split * p.suffix_tokens;
+    t1 = t0 + p.suffix_tokens < n ? t0 + p.suffix_tokens : n;
+    split += p.prefix_splits;
+    if (t0 >= t1) return;
+  }
+  const int64_t base = (int64_t)split * a.B * a.Hq;
+  if constexpr (BYROWS) {
+    if (w.prefix) item_by_rows<F16, D, NM>(a, w, t0, t1, base, part_o, part_ml, lds);
+    else item_by_tokens<F16, D, 1>(a, w, t0, t1, base, part_o, part_ml, lds);
+  } else {
+    item_by_tokens<F16, D, NM>(a, w, t0, t1, base, part_o, part_ml, lds);
   }
 }
 
@@ -355,54 +515,61 @@ __global__ __launch_bounds__(64) void q1_attn_join(const q1_attn a, const AttnPl
   if (lane == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? (top - lift) * 0.69314718055994530942f + logf(sum) : -INFINITY;
 }
 
-template <bool F16, int D, int NM>
+template <bool F16, int D, int NM, bool BYROWS>
 hipError_t launch(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
-  constexpr int vt = kWaves * kTile * (2 * D + 32), jo = kWaves * 16 * NM * ((D + 4) * 4 + 8);
-  constexpr int bytes = vt > jo ? vt : jo;
-  static bool set = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_attn_main<F16, D, NM>),
-                                        hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
-  (void)set;
+  constexpr int tokens = kTokenLds<D, BYROWS ? 1 : NM>(), rows = BYROWS ? kRowLds<D>() : 0;
+  constexpr int bytes = tokens > rows ? tokens : rows;
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_attn_main<F16, D, NM, BYROWS>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (attr != hipSuccess) return attr;
   if (p.wgs > 0)
-    hipLaunchKernelGGL((q1_attn_main<F16, D, NM>), dim3((unsigned)p.wgs), dim3(64 * kWaves), bytes, s, a, p, po, pml);
+    hipLaunchKernelGGL((q1_attn_main<F16, D, NM, BYROWS>), dim3((unsigned)p.wgs), dim3(64 * kWaves), bytes, s, a, p, po, pml);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((q1_attn_join<D>), dim3((unsigned)(a.B * a.Hq)), dim3(64), 0, s, a, p, po, pml, kLift<F16>);
   return hipGetLastError();
 }
 
+template <bool F16, int D>
+hipError_t launch_d(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
+  if (p.by_rows) return p.nm == 1 ? launch<F16, D, 1, true>(a, p, po, pml, s) : launch<F16, D, 2, true>(a, p, po, pml, s);
+  return p.nm == 1 ? launch<F16, D, 1, false>(a, p, po, pml, s) : launch<F16, D, 2, false>(a, p, po, pml, s);
+}
+
 template <bool F16>
 hipError_t launch_t(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
-  if (a.D == 64) return p.nm == 1 ? launch<F16, 64, 1>(a, p, po, pml, s) : p.nm == 2 ? launch<F16, 64, 2>(a, p, po, pml, s) : launch<F16, 64, 4>(a, p, po, pml, s);
-  if (a.D == 128) return p.nm == 1 ? launch<F16, 128, 1>(a, p, po, pml, s) : p.nm == 2 ? launch<F16, 128, 2>(a, p, po, pml, s) : launch<F16, 128, 4>(a, p, po, pml, s);
-  return p.nm == 1 ? launch<F16, 256, 1>(a, p, po, pml, s) : launch<F16, 256, 2>(a, p, po, pml, s);
+  return a.D == 64 ? launch_d<F16, 64>(a, p, po, pml, s) : a.D == 128 ? launch_d<F16, 128>(a, p, po, pml, s) : launch_d<F16, 256>(a, p, po, pml, s);
 }
+
+int64_t up_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
 }  // namespace
 
+// Few rows (up to 32 of them share a key/value head): items by tokens, all rows in
+// an item.  More: prefix items by rows, 64 or 128 a block, suffix items by tokens.
 AttnPlan plan_prefix_attn(const q1_attn& a) {
   AttnPlan p = {};
   const int64_t group = a.Hq / a.Hkv, R = a.P > 0 ? a.B * group : group;
-  const int64_t tiles = (R + 15) / 16;
-  p.nm = tiles <= 1 ? 1 : tiles <= 2 || a.D == 256 ? 2 : 4;
-  p.prefix_rb = (int)((a.B * group + 16 * p.nm - 1) / (16 * p.nm));
-  p.suffix_rb = (int)((group + 16 * p.nm - 1) / (16 * p.nm));
-  const int64_t most = a.max_pages * a.page_size;
-  const int64_t pit = (a.P + kStep - 1) / kStep, sit = (most + kStep - 1) / kStep;
-  // iterations of kStep tokens, over all items
+  p.by_rows = a.P > 0 && R > 32;
+  p.nm = p.by_rows ? (R > 64 ? 2 : 1) : (R > 16 ? 2 : 1);
+  p.prefix_rb = (int)up_div(a.B * group, 16 * p.nm * (p.by_rows ? kWaves : 1));
+  p.suffix_rb = (int)up_div(group, p.by_rows ? 16 : 16 * p.nm);
+  // units of work: kStep tokens by tokens, kTile by rows (about as long)
+  const int64_t most = a.max_pages * a.page_size, punit = p.by_rows ? kTile : kStep;
+  const int64_t pit = up_div(a.P, punit), sit = up_div(most, kStep);
   const int64_t total = pit * a.Hkv * p.prefix_rb + sit * a.B * a.Hkv * p.suffix_rb;
-  const int64_t cus = device_cus();
-  int64_t per = (total + cus - 1) / cus;  // iterations per item: about a workgroup per compute unit
+  const int64_t slots = (int64_t)device_cus() * (p.by_rows || p.nm * a.D > 256 ? 1 : 2);  // workgroups at a time
+  int64_t per = up_div(total, slots);
   if (per < 1) per = 1;
   // at most 64 parts of each kind to add per row
   int64_t pper = per, sper = per;
-  if ((pit + pper - 1) / pper > 64) pper = (pit + 63) / 64;
-  if ((sit + sper - 1) / sper > 64) sper = (sit + 63) / 64;
-  p.prefix_splits = (int)((pit + pper - 1) / pper);
-  p.prefix_tokens = pper * kStep;
-  p.suffix_splits = (int)((sit + sper - 1) / sper);
+  if (up_div(pit, pper) > 64) pper = up_div(pit, 64);
+  if (up_div(sit, sper) > 64) sper = up_div(sit, 64);
+  p.prefix_splits = (int)up_div(pit, pper);
+  p.prefix_tokens = pper * punit;
+  p.suffix_splits = (int)up_div(sit, sper);
   p.suffix_tokens = sper * kStep;
-  const int64_t pairs = (a.Hkv * (int64_t)p.prefix_splits + 7) / 8 * 8;
-  p.prefix_wgs = pairs * p.prefix_rb;
+  p.prefix_wgs = up_div(a.Hkv * (int64_t)p.prefix_splits, 8) * 8 * p.prefix_rb;
   p.wgs = p.prefix_wgs + (int64_t)p.suffix_splits * a.B * a.Hkv * p.suffix_rb;
   const size_t rows = (size_t)(p.prefix_splits + p.suffix_splits) * a.B * a.Hq;
   p.ml_off = (rows * a.D * 4 + 255) / 256 * 256;
