@@ -21,8 +21,12 @@
 //                 and come back transposed (ds_read_tr16).
 // Weights enter the second product as two 16-bit parts (high and remainder), so
 // that their rounding (2^-17) stays below the output's; their sum, the maximum
-// and the output are fp32.  Values and keys of tokens past the length are never
-// loaded: zeros stand for them and their scores are -infinity.
+// and the output are fp32.  A token that does not count (past the length, no such
+// page) has the score -infinity, whatever its key, and zeros for its values.
+//
+// Loops have no branch around loads or products (a branch makes the compiler wait
+// for every load in flight where the paths join): loads past the end are dropped
+// by a buffer's range or go to a row that does count.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -97,7 +101,7 @@ __device__ __forceinline__ float sum_groups(float v) {
 }
 
 __device__ __forceinline__ int64_t suffix_len(const q1_attn& a, int64_t b) {
-  if (a.max_pages == 0) return 0;
+  if (a.max_pages == 0 || a.pages == 0) return 0;
   const int64_t n = a.suffix_lens[b], most = a.max_pages * a.page_size;
   return n < 0 ? 0 : n > most ? most : n;
 }
@@ -182,8 +186,14 @@ constexpr int kRowLds() {
   return 2 * kTile * ((2 * D + 16) + (2 * D + 32));
 }
 
+// Rows [0, n) of a strided operand: loads past them give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t n, int64_t ld_bytes, int width_bytes) {
+  const int bytes = n > 0 ? (int)((n < kTile ? n : kTile) - 1) * (int)ld_bytes + width_bytes : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+}
+
 // An item by tokens.
-template <bool F16, int D, int NM>
+template <bool F16, int D, int NM, bool PREFIX>
 __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, int64_t t0, int64_t t1, int64_t base,
                                                float* part_o, float2* part_ml, unsigned char* lds) {
   constexpr int KS = D / 32, DT = D / 16, VROW = 2 * D + 32;  // LDS bytes of a value row: rows start 8 banks apart
@@ -193,7 +203,6 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so the loop they are in must be a scalar one
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int live = (w.R - w.row0 + 15) / 16 < NM ? (w.R - w.row0 + 15) / 16 : NM;
   unsigned char* const ql = lds + kWaves * kTile * VROW;
   u32x4 Q[QL ? 1 : NM][QL ? 1 : KS];
   if constexpr (QL) {
@@ -209,35 +218,50 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
       for (int s = 0; s < KS; ++s) Q[n][s] = load_q<D>(a, w, w.row0 + 16 * n + col, s, grp);
   }
 
-  const auto* kb = static_cast<const uint16_t*>(w.prefix ? a.k_prefix : a.k_pages) + (int64_t)w.hk * D;
-  const auto* vb = static_cast<const uint16_t*>(w.prefix ? a.v_prefix : a.v_pages) + (int64_t)w.hk * D;
-  const int64_t ld = w.prefix ? a.prefix_ld : (int64_t)a.Hkv * D;
-  // Row of token t0 + (lane % 32) of the tile at t, or -1.
+  const auto* kb = static_cast<const uint16_t*>(PREFIX ? a.k_prefix : a.k_pages) + (int64_t)w.hk * D;
+  const auto* vb = static_cast<const uint16_t*>(PREFIX ? a.v_prefix : a.v_pages) + (int64_t)w.hk * D;
+  const int64_t ld = PREFIX ? a.prefix_ld : (int64_t)a.Hkv * D;
+  // Suffix: the page row of token t + (lane % 32), -1 if it does not count.
   auto row_of = [&](int64_t t) -> int {
-    const int64_t tok = t + (lane & 31);
-    if (tok >= t1) return -1;
-    if (w.prefix) return (int)tok;
-    const uint32_t ps = (uint32_t)a.page_size, pg = (uint32_t)tok / ps;
+    const int64_t tok = t + (lane & 31), last = t1 - 1;
+    const uint32_t ps = (uint32_t)a.page_size, at = (uint32_t)(tok < last ? tok : last), pg = at / ps;
     const int id = a.page_table[w.b0 * a.max_pages + pg];
-    return id < 0 || id >= a.pages ? -1 : (int)((int64_t)id * ps + ((uint32_t)tok - pg * ps));
+    return tok > last || id < 0 || id >= a.pages ? -1 : (int)((int64_t)id * ps + (at - pg * ps));
   };
 
   u32x4 K[2][KS], V[VN];
-  int rows = -1;
-  auto load_k = [&]() {
+  int rows = 0;
+  auto load_k = [&](int64_t t) {
+    if constexpr (PREFIX) {
+      const auto r = rows_of(kb + t * ld, t1 - t, ld * 2, 2 * D);
+      const int at = col * (int)ld * 2 + 16 * grp;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = __shfl(rows, 16 * h + col);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-        K[h][s] = r >= 0 ? *reinterpret_cast<const u32x4*>(kb + r * ld + 32 * s + 8 * grp) : u32x4{0u, 0u, 0u, 0u};
+        for (int s = 0; s < KS; ++s)
+          K[h][s] = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * h * (int)ld * 2 + 64 * s, 0, 0);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = __shfl(rows, 16 * h + col);
+        const u32x4* k = reinterpret_cast<const u32x4*>(kb + (r < 0 ? 0 : r) * ld) + grp;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) K[h][s] = k[4 * s];
+      }
     }
   };
-  auto load_v = [&]() {
+  auto load_v = [&](int64_t t) {
+    if constexpr (PREFIX) {
+      const auto r = rows_of(vb + t * ld, t1 - t, ld * 2, 2 * D);
+      const int at = (lane / VCH) * (int)ld * 2 + 16 * (lane % VCH);
 #pragma unroll
-    for (int i = 0; i < VN; ++i) {
-      const int r = __shfl(rows, i * VPI + lane / VCH);
-      V[i] = r >= 0 ? *reinterpret_cast<const u32x4*>(vb + r * ld + 8 * (lane % VCH)) : u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < VN; ++i) V[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + i * VPI * (int)ld * 2, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VN; ++i) {
+        const int r = __shfl(rows, i * VPI + lane / VCH);
+        V[i] = reinterpret_cast<const u32x4*>(vb + (r < 0 ? 0 : r) * ld)[lane % VCH];
+      }
     }
   };
 
@@ -257,13 +281,19 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
 
   int64_t t = t0 + wave * kTile;
   if (t < t1) {
-    rows = row_of(t);
-    load_k();
-    load_v();
+    if constexpr (!PREFIX) rows = row_of(t);
+    load_k(t);
+    load_v(t);
   }
   for (; t < t1; t += kStep) {
+    // which tokens of the tile count
+    uint32_t in;
+    if constexpr (PREFIX) in = t1 - t >= kTile ? ~0u : (1u << (int)(t1 - t)) - 1u;
+    else in = (uint32_t)__ballot(rows >= 0);
     const int have = rows;
-    // scores, then the next tile's rows and keys
+    const int64_t tn = t + kStep;
+    if constexpr (!PREFIX) rows = row_of(tn);
+    // scores, then the next tile's keys
     f32x4 S[NM][2];
 #pragma unroll
     for (int n = 0; n < NM; ++n)
@@ -272,40 +302,39 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int n = 0; n < NM; ++n)
-        if (n < live) {
-          u32x4 q;
-          if constexpr (QL) q = *reinterpret_cast<const u32x4*>(ql + (16 * n + col) * QROW + 64 * s + 16 * grp);
-          else q = Q[n][s];
+      for (int n = 0; n < NM; ++n) {
+        u32x4 q;
+        if constexpr (QL) q = *reinterpret_cast<const u32x4*>(ql + (16 * n + col) * QROW + 64 * s + 16 * grp);
+        else q = Q[n][s];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) S[n][h] = mma<F16>(K[h][s], q, S[n][h]);
-        }
-    const int64_t tn = t + kStep;
-    if (tn < t1) {
-      rows = row_of(tn);
-      load_k();
+        for (int h = 0; h < 2; ++h) S[n][h] = mma<F16>(K[h][s], q, S[n][h]);
+      }
+    load_k(tn);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      if constexpr (!PREFIX) {  // values of tokens that do not count (anything) are zeros
+        const int r = __shfl(have, i * VPI + lane / VCH);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) V[i][e] = r < 0 ? 0u : V[i][e];
+      }
+      *reinterpret_cast<u32x4*>(vw + i * VPI * VROW) = V[i];
     }
-#pragma unroll
-    for (int i = 0; i < VN; ++i) *reinterpret_cast<u32x4*>(vw + i * VPI * VROW) = V[i];
-    if (tn < t1) load_v();
-
-    // which of this lane's 8 tokens count
-    const uint64_t in = __ballot(have >= 0);
-    const uint32_t mine = ((uint32_t)in >> (4 * grp) & 15u) | ((uint32_t)in >> (16 + 4 * grp) & 15u) << 4;
+    load_v(tn);
+    const uint32_t mine = (in >> (4 * grp) & 15u) | (in >> (16 + 4 * grp) & 15u) << 4;
     u32x4 hi[NM], lo[NM];
 #pragma unroll
     for (int n = 0; n < NM; ++n)
-      if (n < live) weigh<F16, DT>(S[n], mine, sc, m[n], l[n], &O[0][n], NM, hi[n], lo[n]);
+      weigh<F16, DT>(S[n], mine, sc, m[n], l[n], &O[0][n], NM, hi[n], lo[n]);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const u32x4 v = transposed(vr + 32 * d, 16 * VROW);
 #pragma unroll
       for (int n = 0; n < NM; ++n)
-        if (n < live) O[d][n] = mma<F16>(v, hi[n], O[d][n]);
+        O[d][n] = mma<F16>(v, hi[n], O[d][n]);
 #pragma unroll
       for (int n = 0; n < NM; ++n)
-        if (n < live) O[d][n] = mma<F16>(v, lo[n], O[d][n]);
+        O[d][n] = mma<F16>(v, lo[n], O[d][n]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -324,7 +353,7 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
     for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = O[d][n];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * live * (D / 4); i += 64 * kWaves) {
+  for (int i = threadIdx.x; i < 16 * NM * (D / 4); i += 64 * kWaves) {
     const int r = i / (D / 4), c = 4 * (i % (D / 4));
     if (w.row0 + r >= w.R) continue;
     float top = -INFINITY;
@@ -361,13 +390,13 @@ __device__ __forceinline__ void item_by_rows(const q1_attn& a, const Rows& w, in
   const auto* kb = static_cast<const uint16_t*>(a.k_prefix) + (int64_t)w.hk * D;
   const auto* vb = static_cast<const uint16_t*>(a.v_prefix) + (int64_t)w.hk * D;
   u32x4 K[N], V[N];
+  const int ld = (int)a.prefix_ld * 2, at0 = (tid / CH) * ld + 16 * (tid % CH);
   auto load = [&](int64_t t) {
+    const auto rk = rows_of(kb + t * a.prefix_ld, t1 - t, ld, 2 * D), rv = rows_of(vb + t * a.prefix_ld, t1 - t, ld, 2 * D);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t tok = t + (i * 64 * kWaves + tid) / CH;
-      const int64_t at = tok * a.prefix_ld + 8 * (tid % CH);
-      K[i] = tok < t1 ? *reinterpret_cast<const u32x4*>(kb + at) : u32x4{0u, 0u, 0u, 0u};
-      V[i] = tok < t1 ? *reinterpret_cast<const u32x4*>(vb + at) : u32x4{0u, 0u, 0u, 0u};
+      K[i] = __builtin_amdgcn_raw_buffer_load_b128(rk, at0 + i * (64 * kWaves / CH) * ld, 0, 0);
+      V[i] = __builtin_amdgcn_raw_buffer_load_b128(rv, at0 + i * (64 * kWaves / CH) * ld, 0, 0);
     }
   };
   auto put = [&](unsigned char* buf) {
@@ -478,9 +507,11 @@ __global__ __launch_bounds__(64 * kWaves, BYROWS || NM * D > 256 ? 1 : 2) void q
   const int64_t base = (int64_t)split * a.B * a.Hq;
   if constexpr (BYROWS) {
     if (w.prefix) item_by_rows<F16, D, NM>(a, w, t0, t1, base, part_o, part_ml, lds);
-    else item_by_tokens<F16, D, 1>(a, w, t0, t1, base, part_o, part_ml, lds);
+    else item_by_tokens<F16, D, 1, false>(a, w, t0, t1, base, part_o, part_ml, lds);
+  } else if (w.prefix) {
+    item_by_tokens<F16, D, NM, true>(a, w, t0, t1, base, part_o, part_ml, lds);
   } else {
-    item_by_tokens<F16, D, NM>(a, w, t0, t1, base, part_o, part_ml, lds);
+    item_by_tokens<F16, D, NM, false>(a, w, t0, t1, base, part_o, part_ml, lds);
   }
 }
 

@@ -97,6 +97,7 @@ q1_status check_attn(const q1_attn* a) {
   if ((a->P > 0 && a->prefix_ld % 8 != 0) || a->q_ld % 8 != 0)
     return fail(Q1_ERR_INVALID_ARG, "q_ld and prefix_ld must be multiples of 8 elements");
   const int64_t lim = (int64_t)1 << 46;
+  if (a->P > 0 && a->prefix_ld >= (int64_t)1 << 23) return fail(Q1_ERR_UNSUPPORTED, "prefix_ld must be below 2^23 elements");
   if (a->B > kMaxGrid / 4096 || a->q_ld > lim / (a->B + 1) || (a->P > 0 && a->P >= (int64_t)1 << 31) ||
       (a->P > 0 && a->prefix_ld > lim / a->P))
     return fail(Q1_ERR_UNSUPPORTED, "call too large");
