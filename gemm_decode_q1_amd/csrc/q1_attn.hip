@@ -51,6 +51,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int kWaves = 4;
 constexpr int kTile = 32;               // tokens of a wave's tile
 constexpr int kStep = kWaves * kTile;   // tokens of a workgroup's iteration
+constexpr int kOnce = 2;                // cache hint of a buffer load: not read again
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <bool F16>
@@ -239,7 +240,7 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-          K[h][s] = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * h * (int)ld * 2 + 64 * s, 0, 0);
+          K[h][s] = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * h * (int)ld * 2 + 64 * s, 0, kOnce);
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -255,7 +256,7 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
       const auto r = rows_of(vb + t * ld, t1 - t, ld * 2, 2 * D);
       const int at = (lane / VCH) * (int)ld * 2 + 16 * (lane % VCH);
 #pragma unroll
-      for (int i = 0; i < VN; ++i) V[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + i * VPI * (int)ld * 2, 0, 0);
+      for (int i = 0; i < VN; ++i) V[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + i * VPI * (int)ld * 2, 0, kOnce);
     } else {
 #pragma unroll
       for (int i = 0; i < VN; ++i) {
@@ -374,19 +375,17 @@ __device__ __forceinline__ void item_by_tokens(const q1_attn& a, const Rows& w, 
   }
 }
 
-// A prefix item by rows: wave w has rows row0 + 16 NM w .. of the item's.
-template <bool F16, int D, int NM>
+// A prefix item by rows: wave w has rows row0 + 16 w .. +15.
+template <bool F16, int D>
 __device__ __forceinline__ void item_by_rows(const q1_attn& a, const Rows& w, int64_t t0, int64_t t1, int64_t base,
                                              float* part_o, float2* part_ml, unsigned char* lds) {
   constexpr int KS = D / 32, DT = D / 16, KROW = 2 * D + 16, VROW = 2 * D + 32, BUF = kTile * (KROW + VROW);
   constexpr int CH = D / 8, N = kTile * CH / (64 * kWaves);  // 16-byte pieces a row, loads of a tile per thread
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
-  const int row0 = w.row0 + 16 * NM * __builtin_amdgcn_readfirstlane(tid >> 6);
-  u32x4 Q[NM][KS];
+  const int r = w.row0 + 16 * __builtin_amdgcn_readfirstlane(tid >> 6) + col;
+  u32x4 Q[KS];
 #pragma unroll
-  for (int n = 0; n < NM; ++n)
-#pragma unroll
-    for (int s = 0; s < KS; ++s) Q[n][s] = load_q<D>(a, w, row0 + 16 * n + col, s, grp);
+  for (int s = 0; s < KS; ++s) Q[s] = load_q<D>(a, w, r, s, grp);
   const auto* kb = static_cast<const uint16_t*>(a.k_prefix) + (int64_t)w.hk * D;
   const auto* vb = static_cast<const uint16_t*>(a.v_prefix) + (int64_t)w.hk * D;
   u32x4 K[N], V[N];
@@ -402,20 +401,15 @@ __device__ __forceinline__ void item_by_rows(const q1_attn& a, const Rows& w, in
   auto put = [&](unsigned char* buf) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = (i * 64 * kWaves + tid) / CH, c = tid % CH;
-      *reinterpret_cast<u32x4*>(buf + r * KROW + 16 * c) = K[i];
-      *reinterpret_cast<u32x4*>(buf + kTile * KROW + r * VROW + 16 * c) = V[i];
+      const int row = (i * 64 * kWaves + tid) / CH, c = tid % CH;
+      *reinterpret_cast<u32x4*>(buf + row * KROW + 16 * c) = K[i];
+      *reinterpret_cast<u32x4*>(buf + kTile * KROW + row * VROW + 16 * c) = V[i];
     }
   };
-  f32x4 O[NM][DT];
-  float m[NM], l[NM];
+  f32x4 O[DT];
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int n = 0; n < NM; ++n) {
-    m[n] = -INFINITY;
-    l[n] = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) O[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int d = 0; d < DT; ++d) O[d] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float sc = a.scale * kLog2e;
   load(t0);
   put(lds);
@@ -427,50 +421,36 @@ __device__ __forceinline__ void item_by_rows(const q1_attn& a, const Rows& w, in
     put(lds + (at ^ BUF));
     load(t + 2 * kTile);
     const unsigned char* buf = lds + at;
-    f32x4 S[NM][2];
-#pragma unroll
-    for (int n = 0; n < NM; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) S[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 S[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 k = *reinterpret_cast<const u32x4*>(buf + (16 * h + col) * KROW + 64 * s + 16 * grp);
-#pragma unroll
-        for (int n = 0; n < NM; ++n) S[n][h] = mma<F16>(k, Q[n][s], S[n][h]);
-      }
+      for (int h = 0; h < 2; ++h)
+        S[h] = mma<F16>(*reinterpret_cast<const u32x4*>(buf + (16 * h + col) * KROW + 64 * s + 16 * grp), Q[s], S[h]);
     const uint32_t in = t1 - t >= kTile ? ~0u : (1u << (int)(t1 - t)) - 1u;
     const uint32_t mine = (in >> (4 * grp) & 15u) | (in >> (16 + 4 * grp) & 15u) << 4;
-    u32x4 hi[NM], lo[NM];
-#pragma unroll
-    for (int n = 0; n < NM; ++n) weigh<F16, DT>(S[n], mine, sc, m[n], l[n], &O[n][0], 1, hi[n], lo[n]);
+    u32x4 hi, lo;
+    weigh<F16, DT>(S, mine, sc, m, l, O, 1, hi, lo);
     const unsigned char* vr = buf + kTile * KROW + (4 * grp + col / 4) * VROW + 8 * (col & 3);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const u32x4 v = transposed(vr + 32 * d, 16 * VROW);
-#pragma unroll
-      for (int n = 0; n < NM; ++n) O[n][d] = mma<F16>(v, hi[n], O[n][d]);
-#pragma unroll
-      for (int n = 0; n < NM; ++n) O[n][d] = mma<F16>(v, lo[n], O[n][d]);
+      O[d] = mma<F16>(v, hi, O[d]);
+      O[d] = mma<F16>(v, lo, O[d]);
     }
     __syncthreads();
   }
+  const float sum = sum_groups(l);
+  if (r >= w.R) return;
+  const int64_t out = base + w.seq(r) * a.Hq + w.head(r);
+  if (grp == 0) part_ml[out] = float2{m, sum};
 #pragma unroll
-  for (int n = 0; n < NM; ++n) {
-    const int r = row0 + 16 * n + col;
-    const float sum = sum_groups(l[n]);
-    if (r >= w.R) continue;
-    const int64_t out = base + w.seq(r) * a.Hq + w.head(r);
-    if (grp == 0) part_ml[out] = float2{m[n], sum};
-#pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(part_o + out * D + 16 * d + 4 * grp) = O[n][d];
-  }
+  for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(part_o + out * D + 16 * d + 4 * grp) = O[d];
 }
 
-// NM: blocks of 16 rows of an item (by rows: of each wave of a prefix item).
+// NM: blocks of 16 rows of an item by tokens.
 template <bool F16, int D, int NM, bool BYROWS>
-__global__ __launch_bounds__(64 * kWaves, BYROWS || NM * D > 256 ? 1 : 2) void q1_attn_main(const q1_attn a, const AttnPlan p, float* part_o, float2* part_ml) {
+__global__ __launch_bounds__(64 * kWaves, NM * D > 256 ? 1 : 2) void q1_attn_main(const q1_attn a, const AttnPlan p, float* part_o, float2* part_ml) {
   extern __shared__ __align__(16) unsigned char lds[];
   Rows w;
   w.group = a.Hq / a.Hkv;
@@ -483,17 +463,17 @@ __global__ __launch_bounds__(64 * kWaves, BYROWS || NM * D > 256 ? 1 : 2) void q
     const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
     const int pair = (y / p.prefix_rb) * 8 + x;
     if (pair >= a.Hkv * p.prefix_splits) return;
-    w.hk = pair % a.Hkv;
-    split = pair / a.Hkv;
+    w.hk = pair / p.prefix_splits;  // (an XCD reads a range of tokens for all heads: whole rows)
+    split = pair % p.prefix_splits;
     w.R = (int)a.B * w.group;
-    w.row0 = (y % p.prefix_rb) * (BYROWS ? 16 * NM * kWaves : 16 * NM);
+    w.row0 = (y % p.prefix_rb) * (BYROWS ? 16 * kWaves : 16 * NM);
     t0 = (int64_t)split * p.prefix_tokens;
     t1 = t0 + p.prefix_tokens < a.P ? t0 + p.prefix_tokens : a.P;
   } else {
     int64_t i = blockIdx.x - p.prefix_wgs;
     w.hk = (int)(i % a.Hkv);
     i /= a.Hkv;
-    w.row0 = (int)(i % p.suffix_rb) * (BYROWS ? 16 : 16 * NM);
+    w.row0 = (int)(i % p.suffix_rb) * 16 * NM;
     i /= p.suffix_rb;
     split = (int)(i % p.suffix_splits);
     w.b0 = i / p.suffix_splits;
@@ -506,8 +486,8 @@ __global__ __launch_bounds__(64 * kWaves, BYROWS || NM * D > 256 ? 1 : 2) void q
   }
   const int64_t base = (int64_t)split * a.B * a.Hq;
   if constexpr (BYROWS) {
-    if (w.prefix) item_by_rows<F16, D, NM>(a, w, t0, t1, base, part_o, part_ml, lds);
-    else item_by_tokens<F16, D, 1, false>(a, w, t0, t1, base, part_o, part_ml, lds);
+    if (w.prefix) item_by_rows<F16, D>(a, w, t0, t1, base, part_o, part_ml, lds);
+    else item_by_tokens<F16, D, NM, false>(a, w, t0, t1, base, part_o, part_ml, lds);
   } else if (w.prefix) {
     item_by_tokens<F16, D, NM, true>(a, w, t0, t1, base, part_o, part_ml, lds);
   } else {
@@ -548,7 +528,7 @@ __global__ __launch_bounds__(64) void q1_attn_join(const q1_attn a, const AttnPl
 
 template <bool F16, int D, int NM, bool BYROWS>
 hipError_t launch(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
-  constexpr int tokens = kTokenLds<D, BYROWS ? 1 : NM>(), rows = BYROWS ? kRowLds<D>() : 0;
+  constexpr int tokens = kTokenLds<D, NM>(), rows = BYROWS ? kRowLds<D>() : 0;
   constexpr int bytes = tokens > rows ? tokens : rows;
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_attn_main<F16, D, NM, BYROWS>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -563,7 +543,7 @@ hipError_t launch(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, h
 
 template <bool F16, int D>
 hipError_t launch_d(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, hipStream_t s) {
-  if (p.by_rows) return p.nm == 1 ? launch<F16, D, 1, true>(a, p, po, pml, s) : launch<F16, D, 2, true>(a, p, po, pml, s);
+  if (p.by_rows) return launch<F16, D, 1, true>(a, p, po, pml, s);
   return p.nm == 1 ? launch<F16, D, 1, false>(a, p, po, pml, s) : launch<F16, D, 2, false>(a, p, po, pml, s);
 }
 
@@ -577,31 +557,34 @@ int64_t up_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 }  // namespace
 
 // Few rows (up to 32 of them share a key/value head): items by tokens, all rows in
-// an item.  More: prefix items by rows, 64 or 128 a block, suffix items by tokens.
+// an item.  More: prefix items by rows, 64 a block (128 a block, two blocks a wave:
+// 62 against 45 us at 192 rows of D = 256 over 8201 tokens, where it leaves one
+// workgroup a CU, 41 against 38 us at 384 rows of D = 128 over 4000), suffix items
+// by tokens.
 AttnPlan plan_prefix_attn(const q1_attn& a) {
   AttnPlan p = {};
   const int64_t group = a.Hq / a.Hkv, R = a.P > 0 ? a.B * group : group;
   p.by_rows = a.P > 0 && R > 32;
-  p.nm = p.by_rows ? (R > 64 ? 2 : 1) : (R > 16 ? 2 : 1);
+  p.nm = !p.by_rows && R > 16 ? 2 : 1;
   p.prefix_rb = (int)up_div(a.B * group, 16 * p.nm * (p.by_rows ? kWaves : 1));
-  p.suffix_rb = (int)up_div(group, p.by_rows ? 16 : 16 * p.nm);
+  p.suffix_rb = (int)up_div(group, 16 * p.nm);
   // units of work: kStep tokens by tokens, kTile by rows (about as long)
   const int64_t most = a.max_pages * a.page_size, punit = p.by_rows ? kTile : kStep;
   const int64_t pit = up_div(a.P, punit), sit = up_div(most, kStep);
   const int64_t total = pit * a.Hkv * p.prefix_rb + sit * a.B * a.Hkv * p.suffix_rb;
-  const int64_t slots = (int64_t)device_cus() * (p.by_rows || p.nm * a.D > 256 ? 1 : 2);  // workgroups at a time
-  int64_t per = up_div(total, slots);
-  if (per < 1) per = 1;
-  // at most 64 parts of each kind to add per row
-  int64_t pper = per, sper = per;
-  if (up_div(pit, pper) > 64) pper = up_div(pit, 64);
-  if (up_div(sit, sper) > 64) sper = up_div(sit, 64);
-  p.prefix_splits = (int)up_div(pit, pper);
-  p.prefix_tokens = pper * punit;
-  p.suffix_splits = (int)up_div(sit, sper);
-  p.suffix_tokens = sper * kStep;
-  p.prefix_wgs = up_div(a.Hkv * (int64_t)p.prefix_splits, 8) * 8 * p.prefix_rb;
-  p.wgs = p.prefix_wgs + (int64_t)p.suffix_splits * a.B * a.Hkv * p.suffix_rb;
+  const int64_t slots = (int64_t)device_cus() * (p.nm * a.D > 256 ? 1 : 2);  // workgroups at a time
+  // units per item: the fewest with which all items run at a time (a second round of
+  // workgroups would start when the first ends), at most 64 parts of a kind per row
+  for (int64_t per = up_div(total, slots) > 1 ? up_div(total, slots) : 1;; per += up_div(per, 16)) {
+    const int64_t pper = up_div(pit, 64) > per ? up_div(pit, 64) : per, sper = up_div(sit, 64) > per ? up_div(sit, 64) : per;
+    p.prefix_splits = (int)up_div(pit, pper);
+    p.prefix_tokens = pper * punit;
+    p.suffix_splits = (int)up_div(sit, sper);
+    p.suffix_tokens = sper * kStep;
+    p.prefix_wgs = up_div(a.Hkv * (int64_t)p.prefix_splits, 8) * 8 * p.prefix_rb;
+    p.wgs = p.prefix_wgs + (int64_t)p.suffix_splits * a.B * a.Hkv * p.suffix_rb;
+    if (p.wgs <= slots || per >= 2 * up_div(total, slots)) break;
+  }
   const size_t rows = (size_t)(p.prefix_splits + p.suffix_splits) * a.B * a.Hq;
   p.ml_off = (rows * a.D * 4 + 255) / 256 * 256;
   p.ws_bytes = p.ml_off + (rows * 8 + 255) / 256 * 256;

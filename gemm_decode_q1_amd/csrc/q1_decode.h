@@ -48,7 +48,7 @@ hipError_t launch_delta_chunk(const DeltaArgs& a, bool f16, int Dk, unsigned cha
 
 // How a call is cut into work items (see q1_attn.hip).
 struct AttnPlan {
-  int32_t nm;                            // blocks of 16 query rows per item (by rows: per wave)
+  int32_t nm;                            // blocks of 16 query rows per item by tokens
   int32_t by_rows;                       // 1: waves of a prefix item share its tokens
   int32_t prefix_rb, suffix_rb;          // items along the rows
   int32_t prefix_splits, suffix_splits;  // items along the tokens
