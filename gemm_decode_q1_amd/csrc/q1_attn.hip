@@ -495,35 +495,58 @@ __global__ __launch_bounds__(64 * kWaves, NM * D > 256 ? 1 : 2) void q1_attn_mai
   }
 }
 
-// One wave per (sequence, query head): adds its parts.
+// One workgroup per (sequence, query head) adds its parts (at most 128): every wave
+// finds the parts' factors, two per lane, and sums every fourth part.
 template <int D>
-__global__ __launch_bounds__(64) void q1_attn_join(const q1_attn a, const AttnPlan p, const float* part_o,
-                                                   const float2* part_ml, float lift) {
+__global__ __launch_bounds__(64 * kWaves) void q1_attn_join(const q1_attn a, const AttnPlan p, const float* part_o,
+                                                            const float2* part_ml, float lift) {
   constexpr int E = D / 64;
+  __shared__ float so[kWaves][D];
   const int64_t row = blockIdx.x, rows = a.B * a.Hq;
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n = suffix_len(a, row / a.Hq);
   const int parts = p.prefix_splits + (int)((n + p.suffix_tokens - 1) / p.suffix_tokens);
-  float top = -INFINITY;
-  for (int s = lane; s < parts; s += 64) top = fmaxf(top, part_ml[s * rows + row].x);
+  const float2 none = {-INFINITY, 0.f};
+  const float2 ml0 = lane < parts ? part_ml[lane * rows + row] : none;
+  const float2 ml1 = lane + 64 < parts ? part_ml[(lane + 64) * rows + row] : none;
+  float top = fmaxf(ml0.x, ml1.x);
   for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-  float o[E], sum = 0.f;
+  const float base = top == -INFINITY ? 0.f : top;
+  const float f0 = __builtin_amdgcn_exp2f(ml0.x - base), f1 = __builtin_amdgcn_exp2f(ml1.x - base);
+  float sum = f0 * ml0.y + f1 * ml1.y;
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      const float2 ml = part_ml[s * rows + row];
-      const float f = __builtin_amdgcn_exp2f(ml.x - top);
-      sum += f * ml.y;
+  for (int s0 = wave; s0 < parts; s0 += 4 * kWaves) {  // four parts' loads at a time
+    float x[4][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(f, part_o[(s * rows + row) * D + e * 64 + lane], o[e]);
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u * kWaves < parts ? s0 + u * kWaves : parts - 1;
+      const float* po = part_o + (s * rows + row) * D + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[u][e] = po[64 * e];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u * kWaves;
+      const float f = s < parts ? __shfl(s < 64 ? f0 : f1, s & 63) : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(f, x[u][e], o[e]);
     }
   }
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) store_out(a.out, a.out_dtype, row * D + e * 64 + lane, o[e] * inv);
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? (top - lift) * 0.69314718055994530942f + logf(sum) : -INFINITY;
+  for (int e = 0; e < E; ++e) so[wave][64 * e + lane] = o[e];
+  __syncthreads();
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  if (threadIdx.x < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) t += so[w][threadIdx.x];
+    store_out(a.out, a.out_dtype, row * D + threadIdx.x, t * inv);
+  }
+  if (threadIdx.x == 0 && a.lse != nullptr)
+    a.lse[row] = sum > 0.f ? (top - lift) * 0.69314718055994530942f + logf(sum) : -INFINITY;
 }
 
 template <bool F16, int D, int NM, bool BYROWS>
@@ -537,7 +560,7 @@ hipError_t launch(const q1_attn& a, const AttnPlan& p, float* po, float2* pml, h
     hipLaunchKernelGGL((q1_attn_main<F16, D, NM, BYROWS>), dim3((unsigned)p.wgs), dim3(64 * kWaves), bytes, s, a, p, po, pml);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((q1_attn_join<D>), dim3((unsigned)(a.B * a.Hq)), dim3(64), 0, s, a, p, po, pml, kLift<F16>);
+  hipLaunchKernelGGL((q1_attn_join<D>), dim3((unsigned)(a.B * a.Hq)), dim3(64 * kWaves), 0, s, a, p, po, pml, kLift<F16>);
   return hipGetLastError();
 }
 
