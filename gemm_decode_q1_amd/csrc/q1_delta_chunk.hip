@@ -417,6 +417,33 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       for (int i = 0; i < 2; ++i) outf[i] = *reinterpret_cast<const f32x4*>(&cw->out[32 * hf + 16 * i + 4 * grp]);
       keep = cw->keep;
     };
+    // K S0 of this wave's tokens: with its own half of the state (from registers), with the other (from LDS)
+    f32x4 ks[2];
+    auto scores = [&](int o, int b) {
+#pragma unroll
+      for (int s = 0; s < HS; ++s) {
+        const int kk = (o ? 1 - hf : hf) * HS + s;
+        u32x4 sv[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) sv[p] = o ? Ss[sl][kk][p][lane] : Sp[s][p];
+        u32x4 kop[2][KP];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int p = 0; p < KP; ++p)
+            kop[i][p] = *reinterpret_cast<const u32x4*>(&kt[b][p][(32 * hf + 16 * i + col) * KROW + 64 * kk + 16 * grp]);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][0], sv[p], ks[i]);
+        if constexpr (F16) {
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][KP - 1], sv[p], ks[i]);
+        }
+      }
+    };
     load_in(w);
     load_t(w, 0);
     load_t(w, 1);  // (of use to hf = 1 only)
@@ -424,35 +451,12 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     put_state();
     __syncthreads();
     int buf = 0;
+    ks[0] = ks[1] = zero;
+    scores(0, 0);
     for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
       const ChunkWs* wn = t0 + C < hi ? w + 1 : w;
-      // K S0: this half's state from registers, the other's from LDS
-      f32x4 ks[2] = {zero, zero};
-#pragma unroll
-      for (int o = 0; o < 2; ++o)
-#pragma unroll
-        for (int s = 0; s < HS; ++s) {
-          const int kk = (o ? 1 - hf : hf) * HS + s;
-          u32x4 sv[3];
-#pragma unroll
-          for (int p = 0; p < 3; ++p) sv[p] = o ? Ss[sl][kk][p][lane] : Sp[s][p];
-          u32x4 kop[2][KP];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int p = 0; p < KP; ++p)
-              kop[i][p] = *reinterpret_cast<const u32x4*>(&kt[buf][p][(32 * hf + 16 * i + col) * KROW + 64 * kk + 16 * grp]);
-#pragma unroll
-          for (int p = 2; p >= 0; --p)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][0], sv[p], ks[i]);
-          if constexpr (F16) {
-#pragma unroll
-            for (int p = 1; p >= 0; --p)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) ks[i] = mma(kop[i][KP - 1], sv[p], ks[i]);
-          }
-        }
+      // K S0: the rest, with the other half's state from LDS
+      scores(1, buf);
       f32x4 rr[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -535,6 +539,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       for (int p = 0; p < 3; ++p) W[p] = Ws[sl][1 - hf][p][lane];
       update(1 - hf, W);
       put_state();
+      ks[0] = ks[1] = zero;
+      scores(0, buf ^ 1);  // (the next keys are there since the barrier before)
       __syncthreads();
       w = wn;
     }
