@@ -39,7 +39,7 @@ hipError_t launch_delta_recurrent(const DeltaArgs& a, bool f16, int Dk, hipStrea
 
 // Prompts in chunks of kDeltaChunk tokens (q1_delta_chunk.hip).
 constexpr int kDeltaChunk = 64;
-constexpr size_t kDeltaChunkBytes = (6 * 3 + 6 * 2 + 1) * 1024;  // workspace per chunk and value head
+constexpr size_t kDeltaChunkBytes = (10 + 10 + 1) * 1024;  // workspace per chunk and value head
 // Chunks the workspace has room for, whatever the sequences' lengths.
 inline int64_t delta_chunk_slots(int64_t tokens, int64_t nseq) { return tokens / kDeltaChunk + nseq + 1; }
 hipError_t launch_delta_chunk(const DeltaArgs& a, bool f16, int Dk, unsigned char* ws, hipStream_t s);

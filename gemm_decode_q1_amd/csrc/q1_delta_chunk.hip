@@ -50,18 +50,21 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int C = kDeltaChunk;
 
 // Workspace of one (value head, chunk), a head's chunks one after another (the run
-// walks through them; a chunk's heads together cost it a new page every chunk): T and P as operands -- for 16 rows it and
-// 32 columns k, lane l has row 16 it + l%16 and columns 32 k + 4(l/16) .. +3 and
-// 16 further; T in three parts, P in two -- then the factors.  Pairs (it, k) above
-// the diagonal are left out.
+// walks through them; a chunk's heads together cost it a new page every chunk): T
+// and P in 10 tiles (it, jt <= it) of 64 lanes x 16 bytes -- T: row 16 it + l%16,
+// columns 16 jt + 4(l/16) .. +3 in fp32; P: the same elements as four high and four
+// low parts -- then the factors.  The preparation is bound by writing this: T as
+// the three bf16 parts that the run takes it in, and pairs of tiles with zeros,
+// were 31 KB instead of 21.
 struct ChunkWs {
-  u32x4 T[6][3][64];
-  u32x4 P[6][2][64];
+  f32x4 T[10][64];
+  u32x4 P[10][64];
   float in[C], out[C], read[C];  // r e^G, r e^{G63-G}, scale s e^G
   float keep, pad[63];           // e^{G63}
 };
 static_assert(sizeof(ChunkWs) == kDeltaChunkBytes, "workspace of a chunk");
 
+// As operands, two tiles side by side: 16 rows it and 32 columns k.
 constexpr int pair_of(int it, int k) { return it < 2 ? it : 2 * it - 2 + k; }
 
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
@@ -118,15 +121,25 @@ __device__ __forceinline__ int64_t xcd_unit(int64_t units) {
   return (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
 }
 
+// v plus the value that the DPP control brings from another lane, where the row mask has this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  const u32x2 o = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)b[0], CTRL, ROWS, 0xf, false),
+                   (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b[1], CTRL, ROWS, 0xf, false)};
+  return v + __builtin_bit_cast(double, o);
+}
+
 constexpr int AS = 68;  // LDS row of A in floats
 
-// One wave per (chunk, value head).
+// One workgroup of 4 waves per (chunk, value head); wave `it` has rows 16 it .. +15
+// of A, P and T.
 template <bool F16, int DK>
-__global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* ws, int64_t units) {
+__global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, ChunkWs* ws, int64_t units) {
   constexpr int KS = DK / 32;
   __shared__ __align__(16) float A[C * AS];
   __shared__ __align__(16) double Gs[C];
-  __shared__ __align__(16) float rks[C], rqs[C], bs[C];
+  __shared__ __align__(16) float rks[C], bs[C];
   const int64_t unit = xcd_unit(units);
   if (unit >= units) return;
   const int64_t slot = unit / a.Hv;
@@ -145,77 +158,84 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
   const int64_t t0 = lo + c * C;
   if (c < 0 || t0 >= hi) return;
   const int n = hi - t0 < C ? (int)(hi - t0) : C;
-  const int lane = threadIdx.x, col = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
+  // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
+  const int it = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   ChunkWs* w = ws + (int64_t)h * (units / a.Hv) + slot;
 
-  u32x4 K[4][KS], Q[4][KS];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int r = 16 * t + col;
-    const uint16_t* kp = a.k + (t0 + r) * a.k_ld + hk * DK + 8 * grp;
-    const uint16_t* qp = a.q + (t0 + r) * a.q_ld + hk * DK + 8 * grp;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      K[t][s] = r < n ? *reinterpret_cast<const u32x4*>(kp + 32 * s) : u32x4{0u, 0u, 0u, 0u};
-      Q[t][s] = r < n ? *reinterpret_cast<const u32x4*>(qp + 32 * s) : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-  // lane = token: decay sums (in units of log2), write strengths
+  // lane = token: log decay, write strength; rows past the end are zeros
   const bool in = lane < n;
   float gv = in ? a.g[(t0 + lane) * a.Hv + h] : 0.f;
-  gv = gv < -1000.f ? -1000.f : gv;  // exp is 0 there and below; a sum with -infinity in it would not be a number
-  double G = (double)gv * 1.4426950408889634074;
-  for (int off = 1; off < 64; off <<= 1) {
-    const double up = __shfl_up(G, off);
-    if (lane >= off) G += up;
-  }
-  const double G63 = __shfl(G, 63);
-  Gs[lane] = G;
   const float beta = in ? a.beta[(t0 + lane) * a.Hv + h] : 0.f;
-  bs[lane] = beta;
+  const auto kr = rows_of(a.k + t0 * a.k_ld + hk * DK, n, a.k_ld * 2, 2 * DK);
+  const auto qr = rows_of(a.q + t0 * a.q_ld + hk * DK, n, a.q_ld * 2, 2 * DK);
+  u32x4 K[4][KS], Q[KS];  // tiles above this wave's are of no use to it
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    Q[s] = __builtin_amdgcn_raw_buffer_load_b128(qr, (16 * it + col) * (int)a.q_ld * 2 + 16 * grp + 64 * s, 0, 0);
+    K[3][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, (16 * it + col) * (int)a.k_ld * 2 + 16 * grp + 64 * s, 0, 0);
+  }
+  // (K[3] is the wave's own tile, the others are 0, 1, 2)
+#pragma unroll
+  for (int t = 0; t < 3; ++t)
+    if (t < it)
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        K[t][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, (16 * t + col) * (int)a.k_ld * 2 + 16 * grp + 64 * s, 0, 0);
+
+  gv = gv < -1000.f ? -1000.f : gv;  // exp is 0 there and below; a sum with -infinity in it would not be a number
+  double G = (double)gv * 1.4426950408889634074;  // decay sums in units of log2
+  G = scan_step<0x111, 0xf>(G);  // inclusive over the lanes: within rows of 16, then row to row
+  G = scan_step<0x112, 0xf>(G);
+  G = scan_step<0x114, 0xf>(G);
+  G = scan_step<0x118, 0xf>(G);
+  G = scan_step<0x142, 0xa>(G);
+  G = scan_step<0x143, 0xc>(G);
+  const u32x2 last = __builtin_bit_cast(u32x2, G);
+  const double G63 = __builtin_bit_cast(
+      double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)last[0], 63), (uint32_t)__builtin_amdgcn_readlane((int)last[1], 63)});
+  float rq = 1.f;  // of row 16 it + col
+  if (it == 0) {
+    Gs[lane] = G;
+    bs[lane] = beta;
+  }
   if (a.l2norm) {
+    f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qq = kk;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qq = kk;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        kk = mma_in<F16>(K[t][s], K[t][s], kk);
-        qq = mma_in<F16>(Q[t][s], Q[t][s], qq);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col == 4 * grp + i) {
-          rks[16 * t + col] = 1.0f / sqrtf(kk[i] + 1e-6f);
-          rqs[16 * t + col] = 1.0f / sqrtf(qq[i] + 1e-6f);
-        }
+    for (int s = 0; s < KS; ++s) {
+      kk = mma_in<F16>(K[3][s], K[3][s], kk);
+      qq = mma_in<F16>(Q[s], Q[s], qq);
     }
-  } else {
-    rks[lane] = 1.f;
-    rqs[lane] = 1.f;
+    // the diagonal: lane (col, grp) with col / 4 == grp has it, in place col % 4
+    const int e = col & 3;
+    const float dk = e == 0 ? kk[0] : e == 1 ? kk[1] : e == 2 ? kk[2] : kk[3];
+    const float dq = e == 0 ? qq[0] : e == 1 ? qq[1] : e == 2 ? qq[2] : qq[3];
+    const int from = col + 16 * (col >> 2);
+    if (grp == col >> 2) rks[16 * it + col] = 1.0f / sqrtf(dk + 1e-6f);
+    rq = 1.0f / sqrtf(__shfl(dq, from) + 1e-6f);
+  } else if (grp == 0) {
+    rks[16 * it + col] = 1.f;
   }
   __syncthreads();
-  {
-    const float rk = rks[lane], eG = __builtin_amdgcn_exp2f((float)G);
-    w->in[lane] = rk * eG;
-    w->out[lane] = rk * __builtin_amdgcn_exp2f((float)(G63 - G));
-    w->read[lane] = a.scale * rqs[lane] * eG;
-    if (lane == 0) w->keep = __builtin_amdgcn_exp2f((float)G63);
+  const int i = 16 * it + col;
+  const double Gi = Gs[i];
+  if (grp == 0) {
+    const float eG = __builtin_amdgcn_exp2f((float)Gi);
+    w->in[i] = rks[i] * eG;
+    w->out[i] = rks[i] * __builtin_amdgcn_exp2f((float)(G63 - Gi));
+    w->read[i] = a.scale * rq * eG;
+    if (i == 0) w->keep = __builtin_amdgcn_exp2f((float)G63);
   }
 
   // A (rows i = l % 16, columns j = 4 (l / 16) .. +3 of a tile) to LDS, P to the workspace
-#pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int i = 16 * it + col;
-    const double Gi = Gs[i];
-    const float bi = bs[i] * rks[i], qi = a.scale * rqs[i];
-    u32x2 ph[2], pl[2];
-#pragma unroll
-    for (int jt = 0; jt <= it; ++jt) {
+  {
+    const float bi = bs[i] * rks[i], qi = a.scale * rq;
+    auto tile = [&](int jt, const u32x4* Kj) {
       f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        kk = mma_in<F16>(K[jt][s], K[it][s], kk);
-        qk = mma_in<F16>(K[jt][s], Q[it][s], qk);
+        kk = mma_in<F16>(Kj[s], K[3][s], kk);
+        qk = mma_in<F16>(Kj[s], Q[s], qk);
       }
       const int j0 = 16 * jt + 4 * grp;
       const f32x4 rj = *reinterpret_cast<const f32x4*>(&rks[j0]);
@@ -228,44 +248,43 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
         qk[e] = i >= j0 + e ? qi * qk[e] * d : 0.f;
       }
       *reinterpret_cast<f32x4*>(&A[i * AS + j0]) = kk;
-      ph[jt & 1] = part(qk);
-      pl[jt & 1] = part(qk);
-      if (jt == it && !(jt & 1)) ph[1] = pl[1] = u32x2{0u, 0u};
-      if (jt == it || (jt & 1)) {
-        w->P[pair_of(it, jt >> 1)][0][lane] = u32x4{ph[0][0], ph[0][1], ph[1][0], ph[1][1]};
-        w->P[pair_of(it, jt >> 1)][1][lane] = u32x4{pl[0][0], pl[0][1], pl[1][0], pl[1][1]};
-      }
-    }
+      const u32x2 ph = part(qk), pl = part(qk);
+      w->P[it * (it + 1) / 2 + jt][lane] = u32x4{ph[0], ph[1], pl[0], pl[1]};
+    };
+    tile(it, K[3]);
+#pragma unroll
+    for (int jt = 0; jt < 3; ++jt)
+      if (jt < it) tile(jt, K[jt]);
   }
   __syncthreads();
 
-  // Inverse of I + A in place.  The four diagonal blocks by substitution, a block
-  // per 16 lanes, a column per lane ...
-  {
+  // Inverse of I + A in place.  The four diagonal blocks by substitution, all by one
+  // wave (a block per 16 lanes, a column per lane) ...
+  if (it == 0) {
     float x[16];
-    const float* Ab = &A[(16 * grp) * AS + 16 * grp];
+    float* Ab = &A[(16 * grp) * AS + 16 * grp];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int r = 0; r < 16; ++r) {
       float s0v = 0.f, s1v = 0.f;
 #pragma unroll
-      for (int k = 0; k < i; k += 4) {
-        const f32x4 r = *reinterpret_cast<const f32x4*>(Ab + i * AS + k);
+      for (int k = 0; k < r; k += 4) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(Ab + r * AS + k);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (k + e < i) {
-            if (e & 1) s1v = __builtin_fmaf(r[e], x[k + e], s1v);
-            else s0v = __builtin_fmaf(r[e], x[k + e], s0v);
+          if (k + e < r) {
+            if (e & 1) s1v = __builtin_fmaf(y[e], x[k + e], s1v);
+            else s0v = __builtin_fmaf(y[e], x[k + e], s0v);
           }
       }
-      x[i] = (i == col ? 1.f : 0.f) - (s0v + s1v);
+      x[r] = (r == col ? 1.f : 0.f) - (s0v + s1v);
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) A[(16 * grp + i) * AS + 16 * grp + col] = x[i];
+    for (int r = 0; r < 16; ++r) Ab[r * AS + col] = x[r];
   }
   __syncthreads();
   // ... then, with I, J the blocks of the lower and upper half: T_IJ = -T_II' A_I'J' T_J'J,
-  // first for halves of 16 rows, then of 32.
+  // first for halves of 16 rows (waves 1 and 3), then of 32 (a wave each block).
   auto row4 = [&](int I, int J) { return *reinterpret_cast<const f32x4*>(&A[(16 * I + col) * AS + 16 * J + 4 * grp]); };
   auto col4 = [&](int I, int J) {
     f32x4 r;
@@ -274,48 +293,30 @@ __global__ __launch_bounds__(64) void q1_chunk_prep(const DeltaArgs a, ChunkWs* 
     return r;
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  {
-    const f32x4 y0 = mma4(row4(1, 0), col4(0, 0), zero), y1 = mma4(row4(3, 2), col4(2, 2), zero);
-    const f32x4 x0 = mma4(y0, row4(1, 1), zero), x1 = mma4(y1, row4(3, 3), zero);
-    __syncthreads();
-    *reinterpret_cast<f32x4*>(&A[(16 + col) * AS + 4 * grp]) = -x0;
-    *reinterpret_cast<f32x4*>(&A[(48 + col) * AS + 32 + 4 * grp]) = -x1;
+  if (it & 1) {
+    const f32x4 y = mma4(row4(it, it - 1), col4(it - 1, it - 1), zero);
+    const f32x4 x = mma4(y, row4(it, it), zero);
+    *reinterpret_cast<f32x4*>(&A[(16 * it + col) * AS + 16 * (it - 1) + 4 * grp]) = -x;
   }
   __syncthreads();
   {
-    f32x4 y[2][2];  // rows 2, 3 x columns 0, 1 of A times the upper half's inverse
-#pragma unroll
-    for (int I = 0; I < 2; ++I)
-#pragma unroll
-      for (int J = 0; J < 2; ++J) {
-        y[I][J] = mma4(row4(2 + I, 1), col4(1, J), zero);
-        if (J == 0) y[I][J] = mma4(row4(2 + I, 0), col4(0, 0), y[I][J]);
-      }
-    f32x4 x[2][2];
-#pragma unroll
-    for (int J = 0; J < 2; ++J) {
-      x[0][J] = mma4(y[0][J], row4(2, 2), zero);
-      x[1][J] = mma4(y[1][J], row4(3, 3), mma4(y[0][J], row4(3, 2), zero));
-    }
+    const int I = it >> 1, J = it & 1;
+    auto half = [&](int r) {  // rows 2 + r of A times the upper half's inverse, columns J
+      f32x4 y = mma4(row4(2 + r, 1), col4(1, J), zero);
+      if (J == 0) y = mma4(row4(2 + r, 0), col4(0, 0), y);
+      return y;
+    };
+    const f32x4 y0 = half(0);
+    f32x4 x;
+    if (I == 0) x = mma4(y0, row4(2, 2), zero);
+    else x = mma4(half(1), row4(3, 3), mma4(y0, row4(3, 2), zero));
     __syncthreads();
-#pragma unroll
-    for (int I = 0; I < 2; ++I)
-#pragma unroll
-      for (int J = 0; J < 2; ++J) *reinterpret_cast<f32x4*>(&A[(32 + 16 * I + col) * AS + 16 * J + 4 * grp]) = -x[I][J];
+    *reinterpret_cast<f32x4*>(&A[(32 + 16 * I + col) * AS + 16 * J + 4 * grp]) = -x;
   }
   __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 4; ++it)
-#pragma unroll
-    for (int k = 0; 2 * k <= it; ++k) {
-      f32x4 x = row4(it, 2 * k) * *reinterpret_cast<const f32x4*>(&bs[32 * k + 4 * grp]);
-      f32x4 y = 2 * k + 1 <= it ? row4(it, 2 * k + 1) * *reinterpret_cast<const f32x4*>(&bs[32 * k + 16 + 4 * grp]) : zero;
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const u32x2 xp = part(x), yp = part(y);
-        w->T[pair_of(it, k)][p][lane] = u32x4{xp[0], xp[1], yp[0], yp[1]};
-      }
-    }
+  for (int jt = 0; jt < 4; ++jt)
+    if (jt <= it) w->T[it * (it + 1) / 2 + jt][lane] = row4(it, jt) * *reinterpret_cast<const f32x4*>(&bs[16 * jt + 4 * grp]);
 }
 
 // One workgroup of 8 waves per (sequence, value head, 32 columns of the state).
@@ -330,9 +331,10 @@ constexpr int kVRow = 64 + 16;  // LDS bytes of a row of 32 values
 template <bool F16, int DK, bool OUT32>
 __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t slots, int64_t units) {
   constexpr int KS = DK / 32, HS = KS / 2, KP = F16 ? 2 : 1, ST = DK / 32;  // k steps (a half), parts of k and q, state tiles
-  constexpr int KROW = 2 * DK + 32, CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
+  constexpr int KROW = 2 * DK + (F16 && DK == 128 ? 16 : 32), CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
   __shared__ __align__(16) unsigned char kt[2][KP][C * KROW], qt[C * KROW], vt[C * kVRow];
   __shared__ __align__(16) u32x4 Ss[2][KS][3][64], Rs[2][3][64], Ws[2][2][3][64];
+  __shared__ __align__(16) u32x4 Ts[6][3][64];
   __shared__ __align__(16) f32x4 Vs[2][4][64];
   const int64_t unit = xcd_unit(units);
   if (unit >= units) return;
@@ -397,21 +399,14 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         }
       }
     };
-    u32x4 T[2][2][3];  // rows 32 hf + 16 r, columns 32 hf (own), 0 (the other half; hf = 1)
     f32x4 in[2], outf[2];
     float keep;
     auto load_in = [&](const ChunkWs* cw) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) in[i] = *reinterpret_cast<const f32x4*>(&cw->in[32 * hf + 16 * i + 4 * grp]);
     };
-    // own pairs: (0,0) (1,0) or (2,1) (3,1); the others: none or (2,0) (3,0)
+    // pairs of T with the own columns: (0,0) (1,0) or (2,1) (3,1); with the others: none or (2,0) (3,0)
     const int t_own = hf ? 3 : 0, t_oth = 2, t_step = hf ? 2 : 1;
-    auto load_t = [&](const ChunkWs* cw, int o) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int p = 0; p < 3; ++p) T[i][o][p] = cw->T[(o ? t_oth : t_own) + i * t_step][p][lane];
-    };
     auto load_out = [&](const ChunkWs* cw) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) outf[i] = *reinterpret_cast<const f32x4*>(&cw->out[32 * hf + 16 * i + 4 * grp]);
@@ -445,8 +440,6 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       }
     };
     load_in(w);
-    load_t(w, 0);
-    load_t(w, 1);  // (of use to hf = 1 only)
     load_out(w);
     put_state();
     __syncthreads();
@@ -477,22 +470,25 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       // V' = T R: the six products of parts down to 2^-24
       f32x4 vn[2] = {zero, zero};
       auto times = [&](int o, const u32x4* r) {
+        u32x4 T[2][3];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int p = 0; p < 3; ++p) T[i][p] = Ts[(o ? t_oth : t_own) + i * t_step][p][lane];
 #pragma unroll
         for (int x = 2; x >= 0; --x)
 #pragma unroll
           for (int p = 0; p <= x; ++p)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) vn[i] = mma(T[i][o][p], r[x - p], vn[i]);
+            for (int i = 0; i < 2; ++i) vn[i] = mma(T[i][p], r[x - p], vn[i]);
       };
       times(0, R);
-      load_t(wn, 0);
       __syncthreads();
       if (hf == 1) {
         u32x4 r0[3];
 #pragma unroll
         for (int p = 0; p < 3; ++p) r0[p] = Rs[sl][p][lane];
         times(1, r0);
-        load_t(wn, 1);
       }
       u32x4 W[3];
       {
@@ -552,7 +548,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
   } else {
     // ---- output, and the next chunk's keys ----
     const int tid = threadIdx.x & 255;
-    u32x4 Kn[NL], Qn[NL], Vn, P[2][2][2], Pn[2][2][2];  // (n: the next chunk's)
+    u32x4 Kn[NL], Qn[NL], Vn, P[2][4], Pn[2][4];  // (n: the next chunk's)
+    f32x4 Tn[3];
     float read[2], readn[2];
     const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
     const int q_off = (tid / CH) * (int)a.q_ld * 2 + 16 * (tid % CH), q_step = (256 / CH) * (int)a.q_ld * 2;
@@ -596,17 +593,21 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         }
       }
     };
-    // pairs (2 hf + i, k): 0 1 without k = 1, or 2 3, 4 5
-    const int p_off = (hf ? 2 : 0) * 2048 + 16 * lane, p_step = hf ? 4096 : 2048, p_k = hf ? 2048 : kNone;
+    // tiles (2 hf + i, j) of P; those above the diagonal are past the range: zeros
+    int p_off[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int it = 2 * hf + i;
+        p_off[i][j] = j <= it ? (it * (it + 1) / 2 + j) * 1024 + 16 * lane : kNone;
+      }
     auto load_p = [&](const ChunkWs* cw) {
-      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<u32x4*>(&cw->P[0][0][0]), (short)0, (int)sizeof(cw->P), 0x00020000);
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<u32x4*>(&cw->P[0][0]), (short)0, (int)sizeof(cw->P), 0x00020000);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            Pn[i][k][p] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off + i * p_step + k * p_k + 1024 * p, 0, 0);
+        for (int j = 0; j < 4; ++j) Pn[i][j] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off[i][j], 0, 0);
         readn[i] = cw->read[32 * hf + 16 * i + col];
       }
     };
@@ -614,10 +615,28 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int p = 0; p < 2; ++p) P[i][k][p] = Pn[i][k][p];
+        for (int j = 0; j < 4; ++j) P[i][j] = Pn[i][j];
         read[i] = readn[i];
+      }
+    };
+    // T: wave x of the four takes tiles x, x + 4, x + 8 (of 10) from the workspace to LDS, in three parts
+    const int tw = wave & 3;
+    auto load_t = [&](const ChunkWs* cw) {
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<f32x4*>(&cw->T[0][0]), (short)0, (int)sizeof(cw->T), 0x00020000);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        Tn[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (tw + 4 * i) * 1024 + 16 * lane, 0, 0));
+    };
+    auto put_t = [&]() {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int t = tw + 4 * i, it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jt = t - it * (it + 1) / 2;
+        if (t < 10) {
+          f32x4 x = Tn[i];
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            reinterpret_cast<u32x2*>(&Ts[it < 2 ? it : 2 * it - 2 + (jt >> 1)][p][lane])[jt & 1] = part(x);
+        }
       }
     };
     const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
@@ -630,12 +649,18 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         f32x4 x = Vs[sl][2 * k][lane], y = Vs[sl][2 * k + 1][lane];
         const u32x2 x0 = part(x), x1 = part(x), y0 = part(y), y1 = part(y);
         const u32x4 v0 = {x0[0], x0[1], y0[0], y0[1]}, v1 = {x1[0], x1[1], y1[0], y1[1]};
+        u32x4 ph[2], pl[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) o[i] = mma(v1, P[i][k][0], o[i]);
+        for (int i = 0; i < 2; ++i) {
+          ph[i] = u32x4{P[i][2 * k][0], P[i][2 * k][1], P[i][2 * k + 1][0], P[i][2 * k + 1][1]};
+          pl[i] = u32x4{P[i][2 * k][2], P[i][2 * k][3], P[i][2 * k + 1][2], P[i][2 * k + 1][3]};
+        }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) o[i] = mma(v0, P[i][k][1], o[i]);
+        for (int i = 0; i < 2; ++i) o[i] = mma(v1, ph[i], o[i]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) o[i] = mma(v0, P[i][k][0], o[i]);
+        for (int i = 0; i < 2; ++i) o[i] = mma(v0, pl[i], o[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = mma(v0, ph[i], o[i]);
       }
       const auto ores = rows_of(ob + t * o_ld, n, o_ld, a.Dv * esz);
 #pragma unroll
@@ -652,9 +677,17 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     load_k(lo);
     load_q(lo);
     load_p(w);
+    load_t(w);
     take_p();
     put_kv(0);
     put_q();
+    // the upper halves of pairs (0,0) and (2,1) stay zero
+    if (tw == 0)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        reinterpret_cast<u32x2*>(&Ts[pair_of(0, 0)][p][lane])[1] = reinterpret_cast<u32x2*>(&Ts[pair_of(2, 1)][p][lane])[1] = u32x2{0u, 0u};
+    put_t();
+    load_t(lo + C < hi ? w + 1 : w);
     load_k(lo + C);
     load_q(lo + C);
     __syncthreads();
@@ -702,8 +735,10 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       __syncthreads();
       put_q();
       load_q(t0 + 2 * C);
+      put_t();
       if (t0 + C < hi) ++w;
       load_p(w);
+      load_t(t0 + 2 * C < hi ? w + 1 : w);
       __syncthreads();
     }
     const int64_t last = lo + (hi - lo - 1) / C * C;
@@ -714,7 +749,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 template <bool F16, int DK>
 hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
   const int64_t slots = delta_chunk_slots(a.tokens, a.nseq), prep = slots * a.Hv;
-  hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(64), 0, s, a, ws, prep);
+  hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(256), 0, s, a, ws, prep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
