@@ -36,6 +36,7 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2048;            // of (top - x) / T in [0, 27.75): beyond, weights are zero
 constexpr float kBinsPerUnit = 73.8f;
 constexpr int kMost = 4096;            // candidates of one cut
+constexpr int kFewK = kMost / 2;       // up to it, top-k takes all it keeps as candidates
 typedef unsigned long long u64;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -89,12 +90,12 @@ __device__ __forceinline__ u64 composite(float x, int i) { return (u64)key_of(x)
 
 __device__ __forceinline__ float exp_of(float x, float top, float T) { return x == top ? 1.0f : expf((x - top) / T); }
 
-// floor(e 2^40) for 0 <= e <= 1: the scaling is exact and the conversion cuts off;
-// weights from 2^32 on (few) are shifted out of the bits of e.
+// floor(e 2^40) for 0 <= e <= 1, as the 17 bits down to 2^-16 and the 24 below: the
+// scalings and the fraction are exact, the conversions cut off.
 __device__ __forceinline__ u64 weight_of(float e) {
-  u64 w = (uint32_t)(e * 1099511627776.0f);
-  if (e >= 0.00390625f) w = (u64)((__float_as_uint(e) & 0x7fffffu) | 0x800000u) << 17 >> (127u - (__float_as_uint(e) >> 23));
-  return w;
+  const float f = e * 65536.0f;
+  const uint32_t hi = (uint32_t)f, lo = (uint32_t)(__builtin_amdgcn_fractf(f) * 16777216.0f);
+  return (u64)(hi >> 8) << 32 | (hi << 24 | lo);
 }
 
 __device__ __forceinline__ u64 bound_of(float p, u64 total) {
@@ -105,7 +106,7 @@ __device__ __forceinline__ u64 bound_of(float p, u64 total) {
 struct Row {
   float T, p, mp;
   int64_t k;
-  bool greedy, use_k, use_p;
+  bool greedy, use_k, use_p, few;
 };
 
 __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
@@ -119,24 +120,31 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
   r.mp = r.mp > 0.f ? fminf(r.mp, 1.f) : 0.f;
   r.use_k = !r.greedy && r.k > 0 && r.k < a.V;
   r.use_p = !r.greedy && r.p < 1.f;
+  r.few = r.use_k && r.k <= kFewK;
   return r;
 }
 
 // (x - top) / T of one logit, not below -64 (where weights are zero long since).
-// The quotient has to be the correctly rounded one.  With inv the correctly
-// rounded reciprocal, two corrections by the exact remainder give it (Markstein);
-// outside 2^+-40 for T the division itself is used.  NaN comes out as -64.
+// The quotient has to be the correctly rounded one.  inv, the correctly rounded
+// reciprocal, and what it lacks (rest) give it within a unit in the last place, and
+// then one correction by the exact remainder rounds it correctly (Markstein); outside
+// 2^+-40 for T the division itself is used.  NaN comes out as -64.
 struct Scale {
-  float top, T, inv, least;
+  float top, T, inv, rest, least, bins;
   bool plain;
   __device__ Scale(float top_, float T_)
-      : top(top_), T(T_), inv(1.0f / T_), least(-64.0f * T_), plain(!(T_ > 9e-13f && T_ < 1e12f) || top_ == INFINITY) {}
+      : top(top_), T(T_), inv(1.0f / T_), rest(__builtin_fmaf(-inv, T_, 1.0f) * inv), least(-64.0f * T_),
+        bins(kBinsPerUnit * inv), plain(!(T_ > 9e-13f && T_ < 1e12f) || top_ == INFINITY) {}
   __device__ __forceinline__ float exponent(float x) const {
     const float d = fmaxf(x - top, least);
     if (plain) return x == top ? 0.f : fmaxf(d / T, -64.f);
-    float q = d * inv;
-    q = __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
+    const float q = __builtin_fmaf(d, inv, d * rest);
     return __builtin_fmaf(__builtin_fmaf(-q, T, d), inv, q);
+  }
+  // A bin that falls with the logit, where no weight is wanted: kBins for those past all bins and NaN.
+  __device__ __forceinline__ int rank_bin(float x) const {
+    const float f = plain ? -exponent(x) * kBinsPerUnit : (top - x) * bins;
+    return (int)fminf(f, (float)kBins);
   }
   // Below it, every logit's bin is past `bin`.
   __device__ __forceinline__ float past(int bin) const {
@@ -149,8 +157,9 @@ __device__ __forceinline__ int bin_of(float t) { return (int)(-t * kBinsPerUnit)
 // Chunk c of a row: [c len, (c + 1) len), len = V over all chunks, rounded up.
 __device__ __forceinline__ int chunk_len(int64_t V, int chunks) { return (int)((V + chunks - 1) / chunks); }
 
-// f(index, logit as it is) for every element of [lo, hi), by one wave: 16-byte loads, four
-// in flight, between the first and the last aligned element.
+// f(index, logit as it is, whether there is one) for every element of [lo, hi), by one
+// wave whose lanes call f together: 16-byte loads, four in flight, between the first and
+// the last aligned element.
 template <int DT, class F>
 __device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
   constexpr int E = 16 / kSize<DT>;
@@ -159,25 +168,27 @@ __device__ __forceinline__ void each(const void* row, int lo, int hi, F f) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (int64_t)lo * kSize<DT>;
   int head = (int)((16 - at % 16) % 16) / kSize<DT>;
   if (head > hi - lo) head = hi - lo;
-  auto raw = [&](int i) { return value_of<DT>(DT == F32 ? static_cast<const uint32_t*>(row)[i] : static_cast<const uint16_t*>(row)[i]); };
-  if (lane < head) f(lo + lane, raw(lo + lane));
   const int a0 = lo + head, nv = (hi - a0) / E;
   const u32x4* v = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(row) + (int64_t)a0 * kSize<DT>);
-  for (int i = lane; i < nv; i += 256) {
+  auto all = [&](const u32x4& x, int i, bool ok) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      f(a0 + i * E + e, value_of<DT>(DT == F32 ? x[e] : (x[e >> 1] >> (16 * (e & 1))) & 0xffffu), ok);
+  };
+  int i = lane;
+  for (; i - lane + 256 <= nv; i += 256) {
     u32x4 x[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i + 64 * u < nv) x[u] = v[i + 64 * u];
+    for (int u = 0; u < 4; ++u) x[u] = v[i + 64 * u];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (i + 64 * u < nv) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          f(a0 + (i + 64 * u) * E + e, value_of<DT>(DT == F32 ? x[u][e] : (x[u][e >> 1] >> (16 * (e & 1))) & 0xffffu));
-      }
+    for (int u = 0; u < 4; ++u) all(x[u], i + 64 * u, true);
   }
-  const int tail = a0 + nv * E + lane;
-  if (tail < hi) f(tail, raw(tail));
+  for (; i - lane < nv; i += 64) all(v[i < nv ? i : nv - 1], i, i < nv);
+  // before and past the aligned part: at most 2 (E - 1) elements
+  const int past = a0 + nv * E, n = head + hi - past;
+  const int j = lane < head ? lo + lane : past + lane - head;
+  const int c = lane < n ? j : lo;
+  f(j, value_of<DT>(DT == F32 ? static_cast<const uint32_t*>(row)[c] : static_cast<const uint16_t*>(row)[c]), lane < n);
 }
 
 // One step of a scan over a wave's lanes: v plus (or the larger of v and) the value
@@ -261,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void q1_sample_top(const SampleArgs a, co
   const int s = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
   const int len = chunk_len(a.V, S * kWaves), lo = (s * kWaves + wave) * len, end = lo + len;
   float top = -INFINITY;
-  each<DT>(row_ptr<DT>(a, b), lo, end < a.V ? end : (int)a.V, [&](int, float x) { top = fmaxf(top, x); });
+  each<DT>(row_ptr<DT>(a, b), lo, end < a.V ? end : (int)a.V, [&](int, float x, bool ok) { top = fmaxf(top, ok ? x : -INFINITY); });
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) part[wave] = top;
   for (int i = s * kThreads + threadIdx.x; i < kBins; i += S * kThreads) {
@@ -292,8 +303,8 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a
   const void* row = row_ptr<DT>(a, b);
   if (r.greedy) {
     int first = 0x7fffffff;
-    each<DT>(row, lo, hi, [&](int i, float x) {
-      if (x == top && i < first) first = i;
+    each<DT>(row, lo, hi, [&](int i, float x, bool ok) {
+      if (ok && x == top && i < first) first = i;
     });
     if (first != 0x7fffffff) atomicMin(&ws.cut[b].first, (uint32_t)first);
     return;
@@ -301,9 +312,9 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a
   const Scale sc(top, r.T);
   if (!r.use_k && !r.use_p) {
     u64 sum = 0;
-    each<DT>(row, lo, hi, [&](int, float x) {
+    each<DT>(row, lo, hi, [&](int, float x, bool ok) {
       const float e = expf(sc.exponent(x));
-      if (!(e < r.mp)) sum += weight_of(e);
+      if (ok && !(e < r.mp)) sum += weight_of(e);
     });
     sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + c] = sum;
@@ -314,16 +325,16 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a
     h.count[i] = 0;
   }
   __syncthreads();
-  if (!r.use_p) {
-    each<DT>(row, lo, hi, [&](int, float x) {
-      const int bin = bin_of(sc.exponent(x));
-      if (bin < kBins) atomicAdd(&h.count[bin], 1u);
+  if (r.few || !r.use_p) {
+    each<DT>(row, lo, hi, [&](int, float x, bool ok) {
+      const int bin = sc.rank_bin(x);
+      if (ok && bin < kBins) atomicAdd(&h.count[bin], 1u);
     });
   } else {
-    each<DT>(row, lo, hi, [&](int, float x) {
+    each<DT>(row, lo, hi, [&](int, float x, bool ok) {
       const float t = sc.exponent(x);
       const u64 w = weight_of(expf(t));
-      if (w == 0) return;
+      if (!ok || w == 0) return;
       const int bin = bin_of(t);
       atomicAdd(&h.weight[bin], w);
       if (r.use_k) atomicAdd(&h.count[bin], 1u);
@@ -354,6 +365,22 @@ __device__ __forceinline__ Cut find_cut(const Bins& h, const Row& r, u64* s, Cut
     out->bin_k = out->lo_p = out->hi_p = -1;
     out->n_k = out->n_p = 0;
     out->above_k = out->above_p = out->want_k = 0;
+  }
+  if (r.few) {  // the bins down to that of the cut, all of them candidates
+    nb = block_scan((u64)n0 + n1, s + kWaves, &all);
+    const u64 want = (u64)r.k < all ? (u64)r.k : all;
+    if (nb < want && want <= nb + n0 + n1) {
+      const bool second = nb + n0 < want;
+      out->bin_k = 2 * t + second;
+      out->n_k = (uint32_t)(nb + n0 + (second ? n1 : 0));
+    }
+    __syncthreads();
+    Cut c = {};
+    c.bin_k = out->bin_k;
+    c.n_k = out->n_k;
+    c.lo_p = c.hi_p = -1;
+    c.want_k = want;
+    return c;
   }
   if (r.use_p) wb = block_scan(w0 + w1, s, &total);
   if (r.use_k) nb = block_scan((u64)n0 + n1, s + kWaves, &all);
@@ -413,8 +440,10 @@ template <int DT>
 __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a, const Ws ws, int S) {
   __shared__ u64 s[2 * kWaves + 1];
   __shared__ Cut found;
+  __shared__ uint2 queue[kWaves][128];
   const int64_t b = blockIdx.x / S;
-  const int sl = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
+  const int sl = (int)(blockIdx.x - b * S), lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float top = row_top(ws, b, S);
   const Bins bins = {reinterpret_cast<const ulonglong2*>(ws.hist[b].weight)[threadIdx.x],
                      reinterpret_cast<const uint2*>(ws.hist[b].count)[threadIdx.x]};
@@ -435,24 +464,20 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
   }
   if (c.n_k > kMost || c.n_p > kMost) return;
   // below the first bin of the deciding cut, everything is kept
-  const int sure = r.use_p ? c.lo_p : c.bin_k >= 0 ? c.bin_k : kBins;
+  const int sure = r.few ? 0 : r.use_p ? c.lo_p : c.bin_k >= 0 ? c.bin_k : kBins;
   const int last = c.bin_k > c.hi_p ? c.bin_k : c.hi_p;  // past it nothing is (none in use: -1, and sure has all)
   const Scale sc(top, r.T);
   const int len = chunk_len(a.V, S * kWaves), ch = sl * kWaves + wave, lo = ch * len;
   const int hi = lo + len < a.V ? lo + len : (int)a.V;
   u64 sum = 0;
-  const float past = sc.past(sure > last ? sure : last);
-  each<DT>(row_ptr<DT>(a, b), lo, hi, [&](int i, float x) {
-    if (!(x >= past)) return;
-    const float t = sc.exponent(x);
-    const int bin = bin_of(t);
-    if (bin >= sure && bin > last) return;
-    const float e = expf(t);
+  auto take = [&](int i, float x) {
+    const float t = sc.exponent(x), e = expf(t);
+    const int bin = r.few || !r.use_p ? sc.rank_bin(x) : bin_of(t);
     const u64 w = weight_of(e);
     const bool low = e < r.mp;
     if (bin < sure && !low) sum += w;
     const ulonglong2 entry = {composite(clean(x), i), w | (low ? 1ull << 63 : 0)};
-    if (bin == c.bin_k) {
+    if (r.few ? bin <= c.bin_k : bin == c.bin_k) {
       const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
       if (at < kMost) ws.cand[(b * 2) * kMost + at] = entry;
     }
@@ -460,109 +485,146 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
       const uint32_t at = atomicAdd(&ws.cut[b].got_p, 1u);
       if (at < kMost) ws.cand[(b * 2 + 1) * kMost + at] = entry;
     }
+  };
+  // Elements that may matter are collected, so that a wave works on 64 of them at a time.
+  const float past = sc.past(sure > last ? sure : last);
+  uint2* q = queue[wave];
+  uint32_t in = 0, done = 0;
+  each<DT>(row_ptr<DT>(a, b), lo, hi, [&](int i, float x, bool ok) {
+    const u64 some = __ballot(ok && x >= past);
+    if (some == 0) return;
+    const uint32_t at = in + __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
+    if (ok && x >= past) q[at & 127] = uint2{(uint32_t)i, __float_as_uint(x)};
+    in += (uint32_t)__builtin_popcountll(some);
+    if (in - done >= 64) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const uint2 m = q[(done + lane) & 127];
+      take((int)m.x, __uint_as_float(m.y));
+      done += 64;
+    }
   });
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (done + lane < in) {
+    const uint2 m = q[(done + lane) & 127];
+    take((int)m.x, __uint_as_float(m.y));
+  }
   sum = wave_sum(sum);
   if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + ch] = sum;
 }
 
-constexpr int kFew = 256;  // candidates that are ranked by comparing all pairs
-
 struct DrawShared {
-  u64 comp[kMost], weight[kMost];
   u64 bins[kThreads];
-
-  u64 s[4][kWaves];  // one for each scan between barriers
-  u64 pick, over;
-  uint32_t left;
+  u64 chunk[kThreads];  // weight in each chunk
+  u64 s[3][kWaves];  // one for each sum or scan between barriers
+  u64 over, cut;
+  uint32_t pick, left;
 };
 
-// Of the n candidates in LDS (weights with the min-p bit), largest composite
-// first: the one at which the running sum of ones or weights reaches `want`; 0 if
-// the sum stays below.  Up to kFew: each against each, four waves' shares a
-// candidate.  More: digits of 10 bits, from the highest bit in which those left differ.
-__device__ u64 select_candidate(DrawShared& d, int n, bool weighted, u64 want) {
-  const int t = threadIdx.x;
-  constexpr u64 kWeight = ~(1ull << 63);
-  if (n <= kFew) {
-    const int i = t & (kFew - 1), share = t / kFew;
-    if (t < kFew) d.bins[t] = 0;
-    if (t == 0) d.pick = 0;
-    __syncthreads();
-    if (i < n) {
-      const u64 mine = d.comp[i];
-      u64 sum = 0;
-      for (int j = share; j < n; j += kThreads / kFew)
-        if (d.comp[j] > mine) sum += weighted ? d.weight[j] & kWeight : 1ull;
-      if (sum != 0) atomicAdd(&d.bins[i], sum);
-    }
-    __syncthreads();
-    if (t < n) {
-      const u64 w = weighted ? d.weight[t] & kWeight : 1ull;
-      if (d.bins[t] < want && want <= d.bins[t] + w) d.pick = d.comp[t];
-    }
-    __syncthreads();
-    return d.pick;
-  }
-  u64 mask = 0, prefix = 0, before = 0;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 step_most(u64 v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  const u64 o = (u64)hi << 32 | lo;
+  return o > v ? o : v;
+}
+
+__device__ __forceinline__ u64 wave_most(u64 v) {
+  v = step_most<0x111, 0xf>(v);
+  v = step_most<0x112, 0xf>(v);
+  v = step_most<0x114, 0xf>(v);
+  v = step_most<0x118, 0xf>(v);
+  v = step_most<0x142, 0xa>(v);
+  return last_lane(step_most<0x143, 0xc>(v));
+}
+
+// The candidates of a cut are worked on by W waves, four a thread, in registers: by one
+// wave up to kFew (every instruction costs the workgroup's 16 waves 16 cycles, and they
+// would wait for each other: a row with all filters took 12 us so, and 3 with one
+// wave), by all of them beyond.
+constexpr int kFew = 256;
+constexpr int kEach = 4;
+static_assert(kEach * 64 == kFew && kEach * kThreads == kMost, "four a thread");
+
+template <int W>
+__device__ __forceinline__ void group_sync() {
+  if (W == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  else __syncthreads();
+}
+
+template <int W>
+__device__ __forceinline__ u64 group_most(u64 v, u64* s) {
+  v = wave_most(v);
+  if (W == 1) return v;
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return wave_most(lane < W ? s[lane] : 0);
+}
+
+template <int W>
+__device__ __forceinline__ u64 group_scan(u64 v, u64* s, u64* total) {
+  if (W != 1) return block_scan(v, s, total);
+  const u64 x = wave_scan(v);
+  *total = last_lane(x);
+  return x - v;
+}
+
+// Of the group's candidates (0: none), largest first, the one at which the running sum
+// of their amounts reaches `want`; 0 if the sum stays below.  The interval of those left
+// is cut into pieces of equal width (256 for one wave, 1024), the piece that the cut
+// falls in is the next interval.
+template <int W>
+__device__ __forceinline__ u64 select_candidate(DrawShared& d, const u64 (&c)[kEach], const u64 (&amount)[kEach], u64 want) {
+  constexpr int kPieces = W == 1 ? 256 : kThreads, kOwn = kPieces / (64 * W), kBits = W == 1 ? 8 : 10;
+  const int t = threadIdx.x & (64 * W - 1);
+  u64 lo = 1, hi = ~0ull, before = 0;
   for (;;) {
-    u64 ones = 0, zeros = 0;  // bits seen set and seen clear among those left
-    for (int i = t; i < n; i += kThreads)
-      if ((d.comp[i] & mask) == prefix) {
-        ones |= d.comp[i];
-        zeros |= ~d.comp[i];
+    u64 most = 0, least = 0;  // least: of the complements
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (c[k] - lo <= hi - lo) {
+        if (c[k] > most) most = c[k];
+        if (~c[k] > least) least = ~c[k];
       }
-    for (int off = 32; off > 0; off >>= 1) {
-      ones |= __shfl_xor(ones, off);
-      zeros |= __shfl_xor(zeros, off);
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) d.bins[kOwn * t + k] = 0;
+    hi = group_most<W>(most, d.s[0]);
+    lo = ~group_most<W>(least, d.s[1]);
+    group_sync<W>();
+    if (hi == lo || hi == 0) return hi;  // one left, or none
+    const int bits = 64 - __builtin_clzll(hi - lo), shift = bits > kBits ? bits - kBits : 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (c[k] - lo <= hi - lo) atomicAdd(&d.bins[(hi - c[k]) >> shift], amount[k]);
+    group_sync<W>();
+    u64 own[kOwn], sum = 0, all;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      own[k] = d.bins[kOwn * t + k];
+      sum += own[k];
     }
-    __syncthreads();
-    if ((t & 63) == 0) {
-      d.bins[t >> 6] = ones;
-      d.bins[kWaves + (t >> 6)] = zeros;
+    u64 at = before + group_scan<W>(sum, d.s[2], &all);
+    if (before + all < want) return 0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      if (at < want && want <= at + own[k]) {
+        d.pick = (uint32_t)(kOwn * t + k);
+        d.over = at;
+      }
+      at += own[k];
     }
-    __syncthreads();
-    ones = zeros = 0;
-    for (int i = 0; i < kWaves; ++i) {
-      ones |= d.bins[i];
-      zeros |= d.bins[kWaves + i];
-    }
-    const u64 differ = ones & zeros;
-    if (differ == 0) return ones;  // one left
-    const int high = 63 - __builtin_clzll(differ), shift = high > 9 ? high - 9 : 0;
-    __syncthreads();
-    d.bins[t] = 0;
-    __syncthreads();
-    for (int i = t; i < n; i += kThreads)
-      if ((d.comp[i] & mask) == prefix)
-        atomicAdd(&d.bins[(kThreads - 1) - ((d.comp[i] >> shift) & (kThreads - 1))],
-                  weighted ? d.weight[i] & ~(1ull << 63) : 1ull);
-    __syncthreads();
-    const u64 mine = d.bins[t];
-    u64 all;
-    const u64 at = before + block_scan(mine, d.s[0], &all);
-    if (t == 0) d.pick = ~0ull;
-    __syncthreads();
-    if (at < want && want <= at + mine) {
-      d.pick = (u64)(kThreads - 1 - t);
-      d.over = at;
-    }
-    __syncthreads();
-    if (d.pick == ~0ull) return prefix;  // the sum stays below: all are kept
-    // (a 1024-wide window may start above the highest differing bit: those bits agree)
-    mask = ~0ull << shift;
-    prefix = (ones & ~((2ull << high) - 1)) | ((d.pick << shift) & ((2ull << high) - 1));
+    group_sync<W>();
+    const u64 width = (1ull << shift) - 1;
+    hi -= (u64)d.pick << shift;
+    if (hi - lo > width) lo = hi - width;
     before = d.over;
-    __syncthreads();
   }
 }
 
-__device__ void load_candidates(DrawShared& d, const ulonglong2* from, int n) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    d.comp[i] = from[i].x;
-    d.weight[i] = from[i].y;
-  }
-  __syncthreads();
+// floor(u total), below total.
+__device__ __forceinline__ u64 drawn(float u, u64 total) {
+  const u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
+  return at >= total ? total - 1 : at;
 }
 
 // A row's token by radix selects over the row itself (see the top of the file).
@@ -681,8 +743,7 @@ __device__ void draw_from_row(const SampleArgs& a, int64_t b, const void* row, c
     total += sw[j];
   }
   const float u = a.u[b];
-  u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
-  if (at >= total) at = total - 1;
+  const u64 at = drawn(u, total);
   if (at >= start && at < start + mine) {
     u64 c = start;
     rank = rank0;
@@ -697,11 +758,103 @@ __device__ void draw_from_row(const SampleArgs& a, int64_t b, const void* row, c
   }
 }
 
+// The row's cuts among its candidates (own_k, own_p: the first of each list, for W = 1).
+// Where they are all that may be kept (few), the draw among them too, in index order;
+// else the lowest kept composite goes to d.cut, and the kept candidates' weights are
+// added to their chunks'.
+template <int W>
+__device__ __forceinline__ void cut_candidates(DrawShared& d, const SampleArgs& a, int64_t b, const Row& r, const Cut& c,
+                                               const ulonglong2* list, const ulonglong2 (&own_k)[kEach],
+                                               const ulonglong2 (&own_p)[kEach], float u, int len) {
+  const int t = threadIdx.x & (64 * W - 1);
+  u64 comp[kEach] = {}, weight[kEach] = {}, amount[kEach];  // weight: 0 if below min-p
+  u64 cut = 0, total = c.total;                   // total: of what top-k keeps
+  for (int step = 0; step < (r.few ? 3 : 2); ++step) {
+    u64 want;
+    if (step == 0) {
+      if (c.bin_k < 0) continue;
+      const uint32_t n = c.got_k;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const uint32_t i = (uint32_t)(t + 64 * W * k);
+        const ulonglong2 e = i >= n ? ulonglong2{0, 0} : W == 1 ? own_k[k] : list[i];
+        comp[k] = e.x;
+        weight[k] = e.y;
+        amount[k] = 1;
+      }
+      want = c.want_k;
+      if (r.few && want >= n) continue;  // all of them
+    } else if (step == 1) {
+      if (!r.use_p) continue;
+      if (c.bin_k >= 0) {
+        u64 mine = 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          if (comp[k] >= cut) mine += weight[k] & ~(1ull << 63);
+        group_sync<W>();
+        group_scan<W>(mine, d.s[2], &total);
+        total += c.above_k;
+      }
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        if (!r.few) {
+          const uint32_t i = (uint32_t)(t + 64 * W * k);
+          const ulonglong2 e = i >= c.got_p ? ulonglong2{0, 0} : W == 1 ? own_p[k] : list[kMost + i];
+          comp[k] = e.x;
+          weight[k] = e.y;
+        }
+        amount[k] = weight[k] & ~(1ull << 63);
+      }
+      want = bound_of(r.p, total) - c.above_p;
+    } else {
+      u64 mine = 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        amount[k] = comp[k] >= cut && !(weight[k] >> 63) ? weight[k] : 0;
+        comp[k] &= 0xffffffffull;  // the complement of the index
+        mine += amount[k];
+      }
+      group_sync<W>();
+      group_scan<W>(mine, d.s[2], &total);
+      want = drawn(u, total) + 1;
+    }
+    group_sync<W>();
+    const u64 found = select_candidate<W>(d, comp, amount, want);
+    if (step < 2) {
+      cut = found;
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (comp[k] == found)
+        put_token(a, b, (int64_t)~(uint32_t)found, logf((float)((double)amount[k] / (double)total)));
+  }
+  if (r.few) return;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (comp[k] != 0 && comp[k] >= cut && !(weight[k] >> 63))
+      atomicAdd(&d.chunk[~(uint32_t)comp[k] / (uint32_t)len], weight[k]);
+  if (t == 0) d.cut = cut;
+}
+
 template <int DT>
 __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, const Ws ws, int S) {
   __shared__ DrawShared d;
   const int64_t b = blockIdx.x;
   const int t = threadIdx.x, chunks = S * kWaves;
+  // what does not depend on the row's filters, all loaded at once
+  const ulonglong2* const list = ws.cand + b * 2 * kMost;
+  const Cut c = ws.cut[b];
+  ulonglong2 own_k[kEach] = {}, own_p[kEach] = {};
+  if (t < 64 && (a.top_k != nullptr || a.top_p != nullptr)) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      own_k[k] = list[t + 64 * k];
+      own_p[k] = list[kMost + t + 64 * k];
+    }
+  }
+  const u64 chunk_sum = t < chunks ? ws.sums[b * chunks + t] : 0;
+  const float u = a.u[b];
   const Row r = row_of(a, b);
   const float top = row_top(ws, b, S);
   if (top == -INFINITY) {
@@ -709,51 +862,33 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
     return;
   }
   if (r.greedy) {
-    if (t == 0) put_token(a, b, ws.cut[b].first, 0.f);
+    if (t == 0) put_token(a, b, c.first, 0.f);
     return;
   }
   const void* row = row_ptr<DT>(a, b);
+  const int len = chunk_len(a.V, chunks);
   u64 cut = 0;  // the lowest kept composite
-  int n = 0;    // candidates in LDS
+  d.chunk[t] = chunk_sum;
+  __syncthreads();
   if (r.use_k || r.use_p) {
-    const Cut c = ws.cut[b];
     if (c.n_k > kMost || c.n_p > kMost) {
-      draw_from_row<DT>(a, b, row, r, top, d.comp);
+      draw_from_row<DT>(a, b, row, r, top, d.bins);
       return;
     }
-    u64 kept = c.total;
-    if (c.bin_k >= 0) {
-      n = (int)c.n_k;
-      load_candidates(d, ws.cand + (b * 2) * kMost, n);
-      cut = select_candidate(d, n, false, c.want_k);
-      if (r.use_p) {
-        u64 mine = 0;
-        for (int i = t; i < n; i += kThreads)
-          if (d.comp[i] >= cut) mine += d.weight[i] & ~(1ull << 63);
-        block_scan(mine, d.s[1], &kept);
-        kept += c.above_k;
-      }
+    const uint32_t n_k = c.bin_k >= 0 ? c.got_k : 0, n_p = r.use_p && !r.few ? c.got_p : 0;
+    if (n_k <= kFew && n_p <= kFew) {
+      if (t < 64) cut_candidates<1>(d, a, b, r, c, list, own_k, own_p, u, len);
+    } else {
+      cut_candidates<kWaves>(d, a, b, r, c, list, own_k, own_p, u, len);
     }
-    if (r.use_p) {
-      n = (int)c.got_p;
-      load_candidates(d, ws.cand + (b * 2 + 1) * kMost, n);
-      cut = select_candidate(d, n, true, bound_of(r.p, kept) - c.above_p);
-    }
+    if (r.few) return;
+    __syncthreads();
+    cut = d.cut;
   }
-  // weights by chunk: what is sure, and the kept candidates
-  const int len = chunk_len(a.V, chunks);
-  __syncthreads();
-  d.bins[t] = t < chunks ? ws.sums[b * chunks + t] : 0;
-  __syncthreads();
-  for (int i = t; i < n; i += kThreads)
-    if (d.comp[i] >= cut && !(d.weight[i] >> 63)) atomicAdd(&d.bins[~(uint32_t)d.comp[i] / (uint32_t)len], d.weight[i]);
-  __syncthreads();
+  const u64 weight_here = d.chunk[t];
   u64 total;
-  const u64 mine = d.bins[t], start = block_scan(mine, d.s[2], &total);
-  const float u = a.u[b];
-  u64 at = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
-  if (at >= total) at = total - 1;
-  if (at >= start && at < start + mine) {
+  const u64 start = block_scan(weight_here, d.s[0], &total), at = drawn(u, total);
+  if (at >= start && at < start + weight_here) {
     d.left = (uint32_t)t;
     d.over = at - start;
   }
@@ -772,15 +907,15 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
   u64 sum = 0;
   for (int i = i0; i < i1; ++i) sum += weight(i);
   u64 all;
-  u64 c = block_scan(sum, d.s[3], &all);
-  if (want >= c && want < c + sum)
+  u64 run = block_scan(sum, d.s[1], &all);
+  if (want >= run && want < run + sum)
     for (int i = i0; i < i1; ++i) {
       const u64 w = weight(i);
-      if (want < c + w) {
+      if (want < run + w) {
         put_token(a, b, i, logf((float)((double)w / (double)total)));
         break;
       }
-      c += w;
+      run += w;
     }
 }
 

@@ -207,3 +207,21 @@ def test_binding_refusals(what):
         x = x.t().contiguous().t()
     with pytest.raises(ValueError):
         Q.q1_sample(x, u, top_k=k, top_p=p)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_many_candidates(dt):
+    """Cuts with few and with many candidates: top-k from one to more than half of
+    the row, and top-p where the logits lie so near that a cut has hundreds beside it."""
+    V = 30011
+    k = [1, 2, 64, 255, 256, 257, 1000, 2047, 2048, 2049, 4096, 20000]
+    B = len(k)
+    u = np.linspace(0.02, 0.98, B).astype(np.float32).tolist()
+    x = logits_of(11, B, V, dt)
+    check(x, u, k=k, what="top-k")
+    check(x, u, k=k, p=[0.9] * B, what="top-k and top-p")
+    check(x, u, T=[1.3] * B, k=k, p=[0.5] * B, m=[0.01] * B, what="all")
+    near = 0.05 * logits_of(12, B, V, dt)
+    check(near, u, p=np.linspace(0.01, 0.99, B).astype(np.float32).tolist(), what="near, top-p")
+    check(near, u, k=k, what="near, top-k")
+    check(near, u, k=k, p=[0.7] * B, what="near, both")
