@@ -52,11 +52,16 @@ def _stream_of(index: int) -> int:
 
 
 _scratch = {}
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
-    """Device workspace of these calls (no initial contents needed), one per
-    (device, stream), grown on demand."""
+    """Device workspace of these calls (no initial contents needed): one per
+    (device, stream), grown on demand.  A call under graph capture gets one of its
+    own, from the graph's memory: a shared one would be freed as it grows, and be
+    used by replays on other streams."""
+    if _capturing():
+        return _empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     t = _scratch.get((index, stream))
     if t is None or t.numel() < nbytes:
         t = _empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", index))
