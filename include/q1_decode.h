@@ -35,7 +35,7 @@ typedef struct q1_delta {
   const void* q;           /* token t, key head j, element i: q[t*q_ld + j*Dk + i]; 16-byte aligned */
   const void* k;           /* as q, with k_ld */
   const void* v;           /* v[t*v_ld + h*Dv + i]; 16-byte aligned */
-  int64_t q_ld, k_ld, v_ld; /* elements between tokens; multiples of 8 */
+  int64_t q_ld, k_ld, v_ld; /* elements between tokens; multiples of 8, below 2^23 */
   const float* g;          /* [tokens, Hv] log decay */
   const float* beta;       /* [tokens, Hv] write strength */
   float* state;            /* [slots, Hv, Dk, Dv], read and written; 16-byte aligned */
@@ -93,8 +93,8 @@ typedef struct q1_attn {
   const int32_t* suffix_lens;  /* device [B]; NULL iff max_pages == 0 */
   void* out;                   /* [B, Hq, D] in out_dtype; 16-byte aligned */
   float* lse;                  /* [B, Hq], or NULL */
-  int64_t q_ld, prefix_ld;     /* prefix_ld % 8 == 0 */
-  int64_t B, P, pages, max_pages, page_size;
+  int64_t q_ld, prefix_ld;     /* prefix_ld % 8 == 0, below 2^23 */
+  int64_t B, P, pages, max_pages, page_size; /* P, pages * page_size and max_pages * page_size below 2^31 */
   int32_t Hq, Hkv;             /* Hq % Hkv == 0 */
   int32_t D;                   /* 64, 128 or 256 */
   int32_t dtype;               /* of q, keys and values: Q1_BF16 or Q1_F16 */

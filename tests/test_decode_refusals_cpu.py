@@ -129,3 +129,17 @@ def test_sample_empty_and_workspace():
         assert sample() == -3
         assert sample(ws=FAKE, n=need - 1) == -3
         assert sample(ws=FAKE + 32, n=need) == -1
+
+
+@pytest.mark.parametrize("kw", [dict(q_ld=1 << 23), dict(k_ld=1 << 23), dict(v_ld=1 << 24)])
+def test_delta_stride_limit(kw):
+    L, d = B.load_library(), delta(**kw)
+    assert L.q1_delta_step(ctypes.byref(d), 3, 1, None) == -2 and "2^23" in said()
+    assert L.q1_delta_prefill(ctypes.byref(d), 70, 3, FAKE, None, 0, None) == -2 and "2^23" in said()
+
+
+@pytest.mark.parametrize("kw,msg", [(dict(prefix_ld=1 << 23), "2^23"), (dict(pages=1 << 27), "too large"),
+                                    (dict(P=1 << 31), "too large")])
+def test_attn_limits(kw, msg):
+    L, a = B.load_library(), attn(**kw)
+    assert L.q1_prefix_attn(ctypes.byref(a), None, 0, None) == -2 and msg in said()

@@ -279,3 +279,30 @@ def test_binding_refusals(what):
         slots = torch.zeros(3, dtype=torch.int32).cuda()
     with pytest.raises(ValueError):
         Q.q1_delta_step(q, k, v, g, beta, state, slots, l2norm=True)
+
+
+def test_offsets_past_32_bits():
+    """States at the end of a pool of over 4 GiB, and tokens so far apart that their
+    offsets pass 32 bits: the same results as for small operands."""
+    Hk, Hv, D, T, ld = 1, 2, 128, 9000, 1 << 18
+    q, k, v, g, beta, state = draw(9, (T,), Hk, Hv, D, D, "bf16", True, 3)
+    slots = 40000
+    pool = torch.empty(slots, Hv, D, D, device="cuda")
+    pool[-3:] = state
+    cu = torch.tensor([0, 5, T], dtype=torch.int32).cuda()
+    at = torch.tensor([2, 0], dtype=torch.int32).cuda()
+    wide = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, 4 * D), (ld, 1))
+    wide[:, :D], wide[:, D:2 * D], wide[:, 2 * D:] = q.reshape(T, -1), k.reshape(T, -1), v.reshape(T, -1)
+    far = lambda a, h: wide[:, a:a + h * D].unflatten(1, (h, D))  # noqa: E731
+    for step in (False, True):
+        if step:
+            n = 2
+            args = [x.reshape(2, T // 2, *x.shape[1:]) if x.is_contiguous() else x.unflatten(0, (2, T // 2))
+                    for x in (q, k, v, g, beta)]
+            wargs = [x.unflatten(0, (2, T // 2)) for x in (far(0, Hk), far(D, Hk), far(2 * D, Hv))]
+            want = Q.q1_delta_step(*args, state, at[:n], l2norm=True)
+            got = Q.q1_delta_step(*wargs, *args[3:], pool, at[:n] + (slots - 3), l2norm=True)
+        else:
+            want = Q.q1_delta_prefill(q, k, v, g, beta, state, cu, at, l2norm=True)
+            got = Q.q1_delta_prefill(far(0, Hk), far(D, Hk), far(2 * D, Hv), g, beta, pool, cu, at + (slots - 3), l2norm=True)
+        assert torch.equal(got, want) and torch.equal(pool[-3:], state)

@@ -192,3 +192,24 @@ def test_binding_refusals(what):
         vp = None
     with pytest.raises(ValueError):
         Q.q1_prefix_attn(q, kp, vp, kc, vc, table, L)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_offsets_past_32_bits(dt):
+    """A cache of over 4 GiB whose last pages are used, and prefix rows so far apart that
+    their offsets pass 32 bits."""
+    B, Hq, Hkv, D, page, pages, P = 2, 8, 4, 128, 64, 70000, 9000
+    lens = [130, 65]
+    q, kp, vp, kc, vc, table, n = draw(77, B, Hq, Hkv, D, P, lens, page, dt)
+    far = pages - kc.shape[0]
+    big = [torch.empty(pages, page, Hkv, D, dtype=DT[dt], device="cuda") for _ in range(2)]
+    for b, small in zip(big, (kc, vc)):
+        b[far:] = small
+    ld = 1 << 18
+    wide = [torch.empty(P * ld, dtype=DT[dt], device="cuda").as_strided((P, Hkv, D), (ld, D, 1)) for _ in range(2)]
+    for w, small in zip(wide, (kp, vp)):
+        w.copy_(small)
+    want = Q.q1_prefix_attn(q, kp, vp, kc, vc, table, n, out_dtype=torch.float32)
+    got = Q.q1_prefix_attn(q, wide[0], wide[1], big[0], big[1], table + far, n, out_dtype=torch.float32)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(got[0], got[1], q, kp, vp, kc, vc, table, lens, page, "f32", D ** -0.5, "far")

@@ -225,3 +225,15 @@ def test_many_candidates(dt):
     check(near, u, p=np.linspace(0.01, 0.99, B).astype(np.float32).tolist(), what="near, top-p")
     check(near, u, k=k, what="near, top-k")
     check(near, u, k=k, p=[0.7] * B, what="near, both")
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that their offsets pass 32 bits."""
+    B, V, ld = 5, 2000, 1 << 30
+    x = logits_of(13, B, V, "bf16")
+    wide = torch.empty((B - 1) * ld + V, dtype=torch.bfloat16, device="cuda").as_strided((B, V), (ld, 1))
+    wide.copy_(x)
+    u = dev([0.1, 0.3, 0.5, 0.7, 0.9])
+    for filters in (dict(), dict(top_p=dev([0.8] * B)), dict(top_k=dev([30] * B, torch.int32))):
+        a, b = Q.q1_sample(wide, u, **filters), Q.q1_sample(x, u, **filters)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
