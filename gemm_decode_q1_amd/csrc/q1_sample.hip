@@ -2,15 +2,18 @@
 // random number.
 //
 // A row is cut into contiguous chunks, one per wave; four launches:
-//   q1_sample_top     largest logit of each workgroup's chunks (and a cleared histogram)
-//   q1_sample_hist    e = exp((x - top)/T), weight w = floor(e 2^40); rows with top-k:
-//                     counts in 2048 bins of (top - x)/T, with top-p: weights in them;
-//                     other rows: each chunk's sum of kept weights
+//   q1_sample_top     largest logit of each workgroup's chunks, and of each small group
+//                     of threads; a cleared histogram
+//   q1_sample_hist    e = exp((x - top)/T), weight w = floor(e 2^40).  Rows with a top-k
+//                     that is small beside the row (Row::few): all that it may keep, as
+//                     candidates, from a bound that the groups' largest logits give.
+//                     Others with top-k: counts in 2048 bins of (top - x)/T, with top-p:
+//                     weights in them.  Rows with neither: each chunk's kept weight
 //   q1_sample_cut     the bins in which the top-k and the top-p cut fall, from the
 //                     histogram; each chunk's sum of the weights above them, and the
 //                     elements in them as candidates
-//   q1_sample_draw    one workgroup per row: the exact cut among the candidates, the
-//                     draw, the chunk it falls into, the token in that chunk
+//   q1_sample_draw    one workgroup per row: the exact cut among the candidates and the
+//                     draw; where it falls into a chunk, the token in that chunk
 // so a row is read two or three times (once from HBM, then from the caches), never
 // sorted, and any number of workgroups share it.  Weights are whole multiples of
 // 2^-40, so sums are exact: no result depends on the order of the additions.
@@ -21,6 +24,14 @@
 //
 // Where a cut's bins hold more than kMost candidates (rows that are flat, or full
 // of equal logits) the draw falls back to a radix select over the row itself.
+//
+// What bounds it: for many rows the first launch reads the logits at the rate of a
+// plain read (192 rows of 152064 in fp32, 117 MB: 19 us, 6.1 TB/s); the second and
+// third are bound by arithmetic, some 40 vector instructions an element for the
+// exponential, the exact quotient, the weight and its bin (31 and 24 us), which is why
+// elements that cannot matter are left out by one comparison before it; the draw is
+// one workgroup's chain of selects (16 us).  For one row all four are latency: 3 + 6 +
+// 2 + 9 us, near what four launches cost the caller (17 us).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -36,7 +47,6 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2048;            // of (top - x) / T in [0, 27.75): beyond, weights are zero
 constexpr float kBinsPerUnit = 73.8f;
 constexpr int kMost = 4096;            // candidates of one cut
-constexpr int kFewK = kMost / 2;       // up to it, top-k takes all it keeps as candidates
 typedef unsigned long long u64;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -58,6 +68,7 @@ struct Cut {
 
 struct Ws {
   float* top;      // [B][S]
+  float* most;     // [B][groups(S)]: largest logit of each group of threads
   Hist* hist;      // [B]
   Cut* cut;        // [B]
   u64* sums;       // [B][S * kWaves]
@@ -109,7 +120,16 @@ struct Row {
   bool greedy, use_k, use_p, few;
 };
 
-__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
+// Threads of a row's workgroups that have one largest logit together (1, 4 or 16), so that
+// there are at most 4096 of these: every workgroup of the row goes through them.
+__device__ __host__ __forceinline__ int group_lanes(int S) { return S <= 4 ? 1 : S <= 16 ? 4 : 16; }
+__device__ __host__ __forceinline__ int groups(int S) { return S * kThreads / group_lanes(S); }
+
+// few: all that top-k may keep are candidates (see q1_sample_hist).  The k-th largest of
+// the groups' largest logits is near the k-th of all as long as k is a small part of the
+// groups (at a quarter, about 1.15 k elements are above it, at all of them no bound is
+// left).  Rows of up to kMost elements fit as they are.
+__device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b, int S) {
   Row r;
   r.T = a.temperature ? a.temperature[b] : 1.0f;
   r.greedy = !(r.T > 0.f);
@@ -120,7 +140,7 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b) {
   r.mp = r.mp > 0.f ? fminf(r.mp, 1.f) : 0.f;
   r.use_k = !r.greedy && r.k > 0 && r.k < a.V;
   r.use_p = !r.greedy && r.p < 1.f;
-  r.few = r.use_k && r.k <= kFewK;
+  r.few = r.use_k && (r.k <= groups(S) / 4 || a.V <= kMost);
   return r;
 }
 
@@ -206,6 +226,12 @@ __device__ __forceinline__ float step_max(float v) {
   return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(none, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false)));
 }
 
+// The value of another lane of the four (or of the row of 16) by a DPP control.
+template <int CTRL>
+__device__ __forceinline__ float with_lane(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+
 // Inclusive sum over the lanes of a wave: rows of 16 by shifts of 1, 2, 4, 8, then
 // the last lane of a row to the next one, and of the lower half to the upper.
 __device__ __forceinline__ u64 wave_scan(u64 v) {
@@ -273,6 +299,13 @@ __global__ __launch_bounds__(kThreads) void q1_sample_top(const SampleArgs a, co
   const int len = chunk_len(a.V, S * kWaves), lo = (s * kWaves + wave) * len, end = lo + len;
   float top = -INFINITY;
   each<DT>(row_ptr<DT>(a, b), lo, end < a.V ? end : (int)a.V, [&](int, float x, bool ok) { top = fmaxf(top, ok ? x : -INFINITY); });
+  if (a.top_k != nullptr) {
+    const int L = group_lanes(S);
+    float m = top;
+    if (L > 1) m = fmaxf(with_lane<0xb1>(m), fmaxf(m, fmaxf(with_lane<0x4e>(m), with_lane<0x1b>(m))));
+    if (L > 4) m = fmaxf(fmaxf(m, with_lane<0x124>(m)), fmaxf(with_lane<0x128>(m), with_lane<0x12c>(m)));
+    if ((threadIdx.x & (L - 1)) == 0) ws.most[b * groups(S) + (s * kThreads + threadIdx.x) / L] = m;
+  }
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) part[wave] = top;
   for (int i = s * kThreads + threadIdx.x; i < kBins; i += S * kThreads) {
@@ -290,13 +323,49 @@ __global__ __launch_bounds__(kThreads) void q1_sample_top(const SampleArgs a, co
   }
 }
 
+// take(index, logit) for the elements of [lo, hi) not below `past`, by one wave: they are
+// collected in `queue`, so that the wave works on 64 of them at a time.
+template <int DT, class F>
+__device__ __forceinline__ void each_from(const void* row, int lo, int hi, float past, uint2 (&queue)[128], F take) {
+  const int lane = threadIdx.x & 63;
+  uint32_t in = 0, done = 0;
+  each<DT>(row, lo, hi, [&](int i, float x, bool ok) {
+    const u64 some = __ballot(ok && x >= past);
+    if (some == 0) return;
+    const uint32_t at = in + __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
+    if (ok && x >= past) queue[at & 127] = uint2{(uint32_t)i, __float_as_uint(x)};
+    in += (uint32_t)__builtin_popcountll(some);
+    if (in - done >= 64) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const uint2 m = queue[(done + lane) & 127];
+      take((int)m.x, __uint_as_float(m.y));
+      done += 64;
+    }
+  });
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (done + lane < in) {
+    const uint2 m = queue[(done + lane) & 127];
+    take((int)m.x, __uint_as_float(m.y));
+  }
+}
+
 template <int DT>
 __global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a, const Ws ws, int S) {
   __shared__ Hist h;
+  __shared__ uint2 queue[kWaves][128];
+  __shared__ u64 scan[kWaves];
+  __shared__ int last;
   const int64_t b = blockIdx.x / S;
-  const int s = (int)(blockIdx.x - b * S), wave = threadIdx.x >> 6;
+  const int s = (int)(blockIdx.x - b * S), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = groups(S);
+  float most[4];  // at most 4096 groups: four a thread, loaded before anything is waited for
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i * kThreads + threadIdx.x;
+    most[i] = a.top_k != nullptr && at < n ? ws.most[b * n + at] : -INFINITY;
+  }
   const float top = row_top(ws, b, S);
-  const Row r = row_of(a, b);
+  const Row r = row_of(a, b, S);
   if (top == -INFINITY) return;
   const int len = chunk_len(a.V, S * kWaves), c = s * kWaves + wave, lo = c * len;
   const int hi = lo + len < a.V ? lo + len : (int)a.V;
@@ -320,12 +389,38 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_hist(const SampleArgs a
     if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + c] = sum;
     return;
   }
+  if (r.few) {
+    // the bin of the k-th largest of the groups' largest logits: k elements at least are
+    // in it and those before it, and all of these are candidates
+    h.count[threadIdx.x] = h.count[threadIdx.x + kThreads] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int bin = sc.rank_bin(most[i]);
+      if (i * kThreads < n && bin < kBins) atomicAdd(&h.count[bin], 1u);
+    }
+    if (threadIdx.x == 0) last = kBins - 1;  // if there are fewer: every element with a weight
+    __syncthreads();
+    const uint32_t n0 = h.count[2 * threadIdx.x], n1 = h.count[2 * threadIdx.x + 1];
+    u64 all;
+    const u64 before = block_scan((u64)n0 + n1, scan, &all), k = (u64)r.k;
+    if (before < k && k <= before + n0 + n1) last = 2 * threadIdx.x + (before + n0 < k);
+    __syncthreads();
+    const int bins = last;
+    each_from<DT>(row, lo, hi, sc.past(bins), queue[wave], [&](int i, float x) {
+      if (sc.rank_bin(x) > bins) return;
+      const float e = expf(sc.exponent(x));
+      const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
+      if (at < kMost) ws.cand[(b * 2) * kMost + at] = ulonglong2{composite(clean(x), i), weight_of(e) | (e < r.mp ? 1ull << 63 : 0)};
+    });
+    return;
+  }
   for (int i = threadIdx.x; i < kBins; i += kThreads) {
     h.weight[i] = 0;
     h.count[i] = 0;
   }
   __syncthreads();
-  if (r.few || !r.use_p) {
+  if (!r.use_p) {
     each<DT>(row, lo, hi, [&](int, float x, bool ok) {
       const int bin = sc.rank_bin(x);
       if (ok && bin < kBins) atomicAdd(&h.count[bin], 1u);
@@ -365,22 +460,6 @@ __device__ __forceinline__ Cut find_cut(const Bins& h, const Row& r, u64* s, Cut
     out->bin_k = out->lo_p = out->hi_p = -1;
     out->n_k = out->n_p = 0;
     out->above_k = out->above_p = out->want_k = 0;
-  }
-  if (r.few) {  // the bins down to that of the cut, all of them candidates
-    nb = block_scan((u64)n0 + n1, s + kWaves, &all);
-    const u64 want = (u64)r.k < all ? (u64)r.k : all;
-    if (nb < want && want <= nb + n0 + n1) {
-      const bool second = nb + n0 < want;
-      out->bin_k = 2 * t + second;
-      out->n_k = (uint32_t)(nb + n0 + (second ? n1 : 0));
-    }
-    __syncthreads();
-    Cut c = {};
-    c.bin_k = out->bin_k;
-    c.n_k = out->n_k;
-    c.lo_p = c.hi_p = -1;
-    c.want_k = want;
-    return c;
   }
   if (r.use_p) wb = block_scan(w0 + w1, s, &total);
   if (r.use_k) nb = block_scan((u64)n0 + n1, s + kWaves, &all);
@@ -442,13 +521,13 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
   __shared__ Cut found;
   __shared__ uint2 queue[kWaves][128];
   const int64_t b = blockIdx.x / S;
-  const int sl = (int)(blockIdx.x - b * S), lane = threadIdx.x & 63;
+  const int sl = (int)(blockIdx.x - b * S);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float top = row_top(ws, b, S);
   const Bins bins = {reinterpret_cast<const ulonglong2*>(ws.hist[b].weight)[threadIdx.x],
                      reinterpret_cast<const uint2*>(ws.hist[b].count)[threadIdx.x]};
-  const Row r = row_of(a, b);
-  if ((!r.use_k && !r.use_p) || top == -INFINITY) return;
+  const Row r = row_of(a, b, S);
+  if ((!r.use_k && !r.use_p) || r.few || top == -INFINITY) return;
   const Cut c = find_cut(bins, r, s, &found);
   if (sl == 0 && threadIdx.x == 0) {
     Cut* o = &ws.cut[b];
@@ -464,7 +543,7 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
   }
   if (c.n_k > kMost || c.n_p > kMost) return;
   // below the first bin of the deciding cut, everything is kept
-  const int sure = r.few ? 0 : r.use_p ? c.lo_p : c.bin_k >= 0 ? c.bin_k : kBins;
+  const int sure = r.use_p ? c.lo_p : c.bin_k >= 0 ? c.bin_k : kBins;
   const int last = c.bin_k > c.hi_p ? c.bin_k : c.hi_p;  // past it nothing is (none in use: -1, and sure has all)
   const Scale sc(top, r.T);
   const int len = chunk_len(a.V, S * kWaves), ch = sl * kWaves + wave, lo = ch * len;
@@ -472,12 +551,12 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
   u64 sum = 0;
   auto take = [&](int i, float x) {
     const float t = sc.exponent(x), e = expf(t);
-    const int bin = r.few || !r.use_p ? sc.rank_bin(x) : bin_of(t);
+    const int bin = r.use_p ? bin_of(t) : sc.rank_bin(x);
     const u64 w = weight_of(e);
     const bool low = e < r.mp;
     if (bin < sure && !low) sum += w;
     const ulonglong2 entry = {composite(clean(x), i), w | (low ? 1ull << 63 : 0)};
-    if (r.few ? bin <= c.bin_k : bin == c.bin_k) {
+    if (bin == c.bin_k) {
       const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
       if (at < kMost) ws.cand[(b * 2) * kMost + at] = entry;
     }
@@ -486,28 +565,7 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
       if (at < kMost) ws.cand[(b * 2 + 1) * kMost + at] = entry;
     }
   };
-  // Elements that may matter are collected, so that a wave works on 64 of them at a time.
-  const float past = sc.past(sure > last ? sure : last);
-  uint2* q = queue[wave];
-  uint32_t in = 0, done = 0;
-  each<DT>(row_ptr<DT>(a, b), lo, hi, [&](int i, float x, bool ok) {
-    const u64 some = __ballot(ok && x >= past);
-    if (some == 0) return;
-    const uint32_t at = in + __builtin_amdgcn_mbcnt_hi((uint32_t)(some >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)some, 0));
-    if (ok && x >= past) q[at & 127] = uint2{(uint32_t)i, __float_as_uint(x)};
-    in += (uint32_t)__builtin_popcountll(some);
-    if (in - done >= 64) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const uint2 m = q[(done + lane) & 127];
-      take((int)m.x, __uint_as_float(m.y));
-      done += 64;
-    }
-  });
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  if (done + lane < in) {
-    const uint2 m = q[(done + lane) & 127];
-    take((int)m.x, __uint_as_float(m.y));
-  }
+  each_from<DT>(row_ptr<DT>(a, b), lo, hi, sc.past(sure > last ? sure : last), queue[wave], take);
   sum = wave_sum(sum);
   if ((threadIdx.x & 63) == 0) ws.sums[b * S * kWaves + ch] = sum;
 }
@@ -772,7 +830,7 @@ __device__ __forceinline__ void cut_candidates(DrawShared& d, const SampleArgs& 
   for (int step = 0; step < (r.few ? 3 : 2); ++step) {
     u64 want;
     if (step == 0) {
-      if (c.bin_k < 0) continue;
+      if (!r.few && c.bin_k < 0) continue;
       const uint32_t n = c.got_k;
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
@@ -782,18 +840,18 @@ __device__ __forceinline__ void cut_candidates(DrawShared& d, const SampleArgs& 
         weight[k] = e.y;
         amount[k] = 1;
       }
-      want = c.want_k;
+      want = r.few ? (u64)r.k : c.want_k;
       if (r.few && want >= n) continue;  // all of them
     } else if (step == 1) {
       if (!r.use_p) continue;
-      if (c.bin_k >= 0) {
+      if (r.few || c.bin_k >= 0) {
         u64 mine = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k)
           if (comp[k] >= cut) mine += weight[k] & ~(1ull << 63);
         group_sync<W>();
         group_scan<W>(mine, d.s[2], &total);
-        total += c.above_k;
+        if (!r.few) total += c.above_k;
       }
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
@@ -805,7 +863,7 @@ __device__ __forceinline__ void cut_candidates(DrawShared& d, const SampleArgs& 
         }
         amount[k] = weight[k] & ~(1ull << 63);
       }
-      want = bound_of(r.p, total) - c.above_p;
+      want = bound_of(r.p, total) - (r.few ? 0 : c.above_p);
     } else {
       u64 mine = 0;
 #pragma unroll
@@ -855,7 +913,7 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
   }
   const u64 chunk_sum = t < chunks ? ws.sums[b * chunks + t] : 0;
   const float u = a.u[b];
-  const Row r = row_of(a, b);
+  const Row r = row_of(a, b, S);
   const float top = row_top(ws, b, S);
   if (top == -INFINITY) {
     if (t == 0) put_token(a, b, -1, -INFINITY);
@@ -871,11 +929,11 @@ __global__ __launch_bounds__(kThreads) void q1_sample_draw(const SampleArgs a, c
   d.chunk[t] = chunk_sum;
   __syncthreads();
   if (r.use_k || r.use_p) {
-    if (c.n_k > kMost || c.n_p > kMost) {
+    if (r.few ? c.got_k > kMost : c.n_k > kMost || c.n_p > kMost) {
       draw_from_row<DT>(a, b, row, r, top, d.bins);
       return;
     }
-    const uint32_t n_k = c.bin_k >= 0 ? c.got_k : 0, n_p = r.use_p && !r.few ? c.got_p : 0;
+    const uint32_t n_k = r.few || c.bin_k >= 0 ? c.got_k : 0, n_p = r.use_p && !r.few ? c.got_p : 0;
     if (n_k <= kFew && n_p <= kFew) {
       if (t < 64) cut_candidates<1>(d, a, b, r, c, list, own_k, own_p, u, len);
     } else {
@@ -945,7 +1003,7 @@ int sample_split(int64_t B, int64_t V) {
 size_t sample_ws_bytes(int64_t B, int64_t V) {
   const size_t S = (size_t)sample_split(B, V), b = (size_t)B;
   return up(b * sizeof(Hist)) + up(b * 2 * kMost * sizeof(ulonglong2)) + up(b * sizeof(Cut)) +
-         up(b * S * kWaves * sizeof(u64)) + up(b * S * sizeof(float));
+         up(b * S * kWaves * sizeof(u64)) + up(b * S * sizeof(float)) + up(b * (size_t)groups((int)S) * sizeof(float));
 }
 
 hipError_t launch_sample(const SampleArgs& a, unsigned char* ws, hipStream_t s) {
@@ -961,6 +1019,8 @@ hipError_t launch_sample(const SampleArgs& a, unsigned char* ws, hipStream_t s) 
   w.sums = reinterpret_cast<u64*>(ws);
   ws += up(b * (size_t)S * kWaves * sizeof(u64));
   w.top = reinterpret_cast<float*>(ws);
+  ws += up(b * (size_t)S * sizeof(float));
+  w.most = reinterpret_cast<float*>(ws);
   if (a.dtype == F32) return launch_t<F32>(a, w, S, s);
   if (a.dtype == BF16) return launch_t<BF16>(a, w, S, s);
   return launch_t<F16>(a, w, S, s);
