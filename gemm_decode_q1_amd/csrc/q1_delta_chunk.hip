@@ -325,6 +325,15 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
 // hf DK/2 .. of the state.  What a wave makes itself it uses from its registers;
 // LDS only carries the other half.  Loads are those of the next chunk, into the
 // registers that a product has just read.
+//
+// A chunk has three parts between barriers: K S0 and R with the half of V' that needs
+// no other wave; the other half, W and half of the new state; the rest of it and its
+// parts.  Bound by this chain: 2.4 us a chunk (bf16, 128x128), of which the matrix
+// cores are busy 0.6 and the vector units 0.75; the output waves' work is dealt so
+// that none of the three waits for it (with the output made in the first part and
+// Q S0 in the second, 8192 tokens of 48 heads took 378 us instead of 362).  Three bf16
+// parts keep the state in fp32.  Four waves with 16 columns and no division of labour
+// took 932 us for 16384 tokens when eight with 32 took 863.
 constexpr int kRunThreads = 512;
 constexpr int kVRow = 64 + 16;  // LDS bytes of a row of 32 values
 
@@ -548,9 +557,9 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
   } else {
     // ---- output, and the next chunk's keys ----
     const int tid = threadIdx.x & 255;
-    u32x4 Kn[NL], Qn[NL], Vn, P[2][4], Pn[2][4];  // (n: the next chunk's)
+    u32x4 Kn[NL], Qn[NL], Vn, P[2][4];  // (n: the next chunk's)
     f32x4 Tn[3];
-    float read[2], readn[2];
+    float read[2];
     const int k_off = (tid / CH) * (int)a.k_ld * 2 + 16 * (tid % CH), k_step = (256 / CH) * (int)a.k_ld * 2;
     const int q_off = (tid / CH) * (int)a.q_ld * 2 + 16 * (tid % CH), q_step = (256 / CH) * (int)a.q_ld * 2;
     const int vc = (c0 & ~31) + 8 * (tid & 3);
@@ -607,16 +616,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Pn[i][j] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off[i][j], 0, 0);
-        readn[i] = cw->read[32 * hf + 16 * i + col];
-      }
-    };
-    auto take_p = [&]() {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) P[i][j] = Pn[i][j];
-        read[i] = readn[i];
+        for (int j = 0; j < 4; ++j) P[i][j] = __builtin_amdgcn_raw_buffer_load_b128(r, p_off[i][j], 0, 0);
+        read[i] = cw->read[32 * hf + 16 * i + col];
       }
     };
     // T: wave x of the four takes tiles x, x + 4, x + 8 (of 10) from the workspace to LDS, in three parts
@@ -627,23 +628,33 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       for (int i = 0; i < 3; ++i)
         Tn[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (tw + 4 * i) * 1024 + 16 * lane, 0, 0));
     };
+    u32x2 Tp[3][3];
+    auto split_t = [&]() {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        f32x4 x = Tn[i];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) Tp[i][p] = part(x);
+      }
+    };
     auto put_t = [&]() {
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int t = tw + 4 * i, it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, jt = t - it * (it + 1) / 2;
         if (t < 10) {
-          f32x4 x = Tn[i];
 #pragma unroll
           for (int p = 0; p < 3; ++p)
-            reinterpret_cast<u32x2*>(&Ts[it < 2 ? it : 2 * it - 2 + (jt >> 1)][p][lane])[jt & 1] = part(x);
+            reinterpret_cast<u32x2*>(&Ts[it < 2 ? it : 2 * it - 2 + (jt >> 1)][p][lane])[jt & 1] = Tp[i][p];
         }
       }
     };
     const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
     f32x4 qs[2] = {zero, zero};
-    // O^T = scale s e^G (Q S0)^T + V'^T P^T of the chunk at t; a lane has token 32 hf + 16 i + col
-    auto finish = [&](int64_t t, int n) {
-      f32x4 o[2] = {read[0] * qs[0], read[1] * qs[1]};
+    // O^T = scale s e^G (Q S0)^T + V'^T P^T; a lane has token 32 hf + 16 i + col
+    f32x4 o[2] = {zero, zero};
+    auto finish = [&]() {
+      o[0] = read[0] * qs[0];
+      o[1] = read[1] * qs[1];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         f32x4 x = Vs[sl][2 * k][lane], y = Vs[sl][2 * k + 1][lane];
@@ -662,6 +673,8 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
         for (int i = 0; i < 2; ++i) o[i] = mma(v0, ph[i], o[i]);
       }
+    };
+    auto store = [&](int64_t t, int n) {
       const auto ores = rows_of(ob + t * o_ld, n, o_ld, a.Dv * esz);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -678,7 +691,6 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
     load_q(lo);
     load_p(w);
     load_t(w);
-    take_p();
     put_kv(0);
     put_q();
     // the upper halves of pairs (0,0) and (2,1) stay zero
@@ -686,19 +698,17 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
       for (int p = 0; p < 3; ++p)
         reinterpret_cast<u32x2*>(&Ts[pair_of(0, 0)][p][lane])[1] = reinterpret_cast<u32x2*>(&Ts[pair_of(2, 1)][p][lane])[1] = u32x2{0u, 0u};
+    split_t();
     put_t();
     load_t(lo + C < hi ? w + 1 : w);
     load_k(lo + C);
     load_q(lo + C);
     __syncthreads();
-    int buf = 0, done = 0;  // rows of the chunk before that wait for finish(): none at first
+    int buf = 0, done = 0;  // rows of the chunk before that wait for store(): none at first
     for (int64_t t0 = lo; t0 < hi; t0 += C, buf ^= 1) {
-      // while the state waves make R: the output of the chunk before
-      finish(t0 - done, done);
-      take_p();
+      // while the state waves make R: the chunk before goes out, (Q S0)^T
+      store(t0 - done, done);
       done = C;
-      __syncthreads();
-      // while they make V' and the new state: (Q S0)^T and the next keys
       qs[0] = qs[1] = zero;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
@@ -730,19 +740,25 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
           for (int i = 0; i < 2; ++i) qs[i] = mma(s0, Q[i], qs[i]);
         }
       }
+      __syncthreads();
+      // while they make V' and half of the new state: the next keys, values and queries
+      split_t();
       put_kv(buf ^ 1);
       load_k(t0 + 2 * C);
-      __syncthreads();
       put_q();
       load_q(t0 + 2 * C);
+      __syncthreads();
+      // while they make the rest of it: the output, and the next T
+      const ChunkWs* wn = t0 + C < hi ? w + 1 : w;
+      finish();
+      load_p(wn);
       put_t();
-      if (t0 + C < hi) ++w;
-      load_p(w);
-      load_t(t0 + 2 * C < hi ? w + 1 : w);
+      load_t(t0 + 2 * C < hi ? wn + 1 : wn);
+      w = wn;
       __syncthreads();
     }
     const int64_t last = lo + (hi - lo - 1) / C * C;
-    finish(last, (int)(hi - last));
+    store(last, (int)(hi - last));
   }
 }
 
