@@ -135,15 +135,15 @@ constexpr int AS = 68;  // LDS row of A in floats
 // One workgroup of 4 waves per (chunk, value head); wave `it` has rows 16 it .. +15
 // of A, P and T.
 template <bool F16, int DK>
-__global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, ChunkWs* ws, int64_t units) {
+__global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, ChunkWs* ws, int64_t slots, int64_t units) {
   constexpr int KS = DK / 32;
-  __shared__ __align__(16) float A[C * AS];
+  __shared__ __align__(16) float A[C * AS], Kt[C * AS];  // (A's rows first hold the queries)
   __shared__ __align__(16) double Gs[C];
   __shared__ __align__(16) float rks[C], bs[C];
   const int64_t unit = xcd_unit(units);
   if (unit >= units) return;
-  const int64_t slot = unit / a.Hv;
-  const int h = (int)(unit - slot * a.Hv), hk = h / (a.Hv / a.Hk);
+  const uint32_t slot = (uint32_t)unit / (uint32_t)a.Hv;  // (there are fewer units than 2^31)
+  const uint32_t h = (uint32_t)unit - slot * (uint32_t)a.Hv, hk = h / ((uint32_t)a.Hv / (uint32_t)a.Hk);
   int64_t s0 = 0, s1 = a.nseq;  // the last sequence whose first slot is not past this one
   while (s1 - s0 > 1) {
     const int64_t m = (s0 + s1) / 2;
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
   const int it = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  ChunkWs* w = ws + (int64_t)h * (units / a.Hv) + slot;
+  ChunkWs* w = ws + h * slots + slot;
 
   // lane = token: log decay, write strength; rows past the end are zeros
   const bool in = lane < n;
@@ -169,19 +169,31 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
   const float beta = in ? a.beta[(t0 + lane) * a.Hv + h] : 0.f;
   const auto kr = rows_of(a.k + t0 * a.k_ld + hk * DK, n, a.k_ld * 2, 2 * DK);
   const auto qr = rows_of(a.q + t0 * a.q_ld + hk * DK, n, a.q_ld * 2, 2 * DK);
-  u32x4 K[4][KS], Q[KS];  // tiles above this wave's are of no use to it
+  // The wave's 16 rows of k and q, through LDS: as operands (rows side by side in a load's
+  // lanes) each load took four times as long, and the four waves' took most of the launch.
+  constexpr int CH = DK / 8, RL = 64 / CH;  // 16-byte pieces of a row, rows of a load
+  u32x4 K[KS], Q[KS];
+  {
+    u32x4 kv[KS], qv[KS];
+    const int r0 = 16 * it + lane / CH, c0 = 16 * (lane % CH);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      kv[s] = __builtin_amdgcn_raw_buffer_load_b128(kr, (r0 + RL * s) * (int)a.k_ld * 2 + c0, 0, 0);
+      qv[s] = __builtin_amdgcn_raw_buffer_load_b128(qr, (r0 + RL * s) * (int)a.q_ld * 2 + c0, 0, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      *reinterpret_cast<u32x4*>(&Kt[(r0 + RL * s) * AS + c0 / 4]) = kv[s];
+      *reinterpret_cast<u32x4*>(&A[(r0 + RL * s) * AS + c0 / 4]) = qv[s];
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
-    Q[s] = __builtin_amdgcn_raw_buffer_load_b128(qr, (16 * it + col) * (int)a.q_ld * 2 + 16 * grp + 64 * s, 0, 0);
-    K[3][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, (16 * it + col) * (int)a.k_ld * 2 + 16 * grp + 64 * s, 0, 0);
+    K[s] = *reinterpret_cast<const u32x4*>(&Kt[(16 * it + col) * AS + 4 * grp + 16 * s]);
+    Q[s] = *reinterpret_cast<const u32x4*>(&A[(16 * it + col) * AS + 4 * grp + 16 * s]);
   }
-  // (K[3] is the wave's own tile, the others are 0, 1, 2)
-#pragma unroll
-  for (int t = 0; t < 3; ++t)
-    if (t < it)
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        K[t][s] = __builtin_amdgcn_raw_buffer_load_b128(kr, (16 * t + col) * (int)a.k_ld * 2 + 16 * grp + 64 * s, 0, 0);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
   gv = gv < -1000.f ? -1000.f : gv;  // exp is 0 there and below; a sum with -infinity in it would not be a number
   double G = (double)gv * 1.4426950408889634074;  // decay sums in units of log2
@@ -203,7 +215,7 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
     f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qq = kk;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      kk = mma_in<F16>(K[3][s], K[3][s], kk);
+      kk = mma_in<F16>(K[s], K[s], kk);
       qq = mma_in<F16>(Q[s], Q[s], qq);
     }
     // the diagonal: lane (col, grp) with col / 4 == grp has it, in place col % 4
@@ -230,12 +242,13 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
   // A (rows i = l % 16, columns j = 4 (l / 16) .. +3 of a tile) to LDS, P to the workspace
   {
     const float bi = bs[i] * rks[i], qi = a.scale * rq;
-    auto tile = [&](int jt, const u32x4* Kj) {
+    auto tile = [&](int jt) {
       f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        kk = mma_in<F16>(Kj[s], K[3][s], kk);
-        qk = mma_in<F16>(Kj[s], Q[s], qk);
+        const u32x4 kj = *reinterpret_cast<const u32x4*>(&Kt[(16 * jt + col) * AS + 4 * grp + 16 * s]);
+        kk = mma_in<F16>(kj, K[s], kk);
+        qk = mma_in<F16>(kj, Q[s], qk);
       }
       const int j0 = 16 * jt + 4 * grp;
       const f32x4 rj = *reinterpret_cast<const f32x4*>(&rks[j0]);
@@ -251,10 +264,7 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
       const u32x2 ph = part(qk), pl = part(qk);
       w->P[it * (it + 1) / 2 + jt][lane] = u32x4{ph[0], ph[1], pl[0], pl[1]};
     };
-    tile(it, K[3]);
-#pragma unroll
-    for (int jt = 0; jt < 3; ++jt)
-      if (jt < it) tile(jt, K[jt]);
+    for (int jt = 0; jt <= it; ++jt) tile(jt);
   }
   __syncthreads();
 
@@ -348,14 +358,14 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
   const int64_t unit = xcd_unit(units);
   if (unit >= units) return;
   const int slices = (a.Dv + 31) / 32;
-  const int64_t sh = unit / slices;
-  const int64_t seq = sh / a.Hv;
-  const int h = (int)(sh - seq * a.Hv), hk = h / (a.Hv / a.Hk);
+  const uint32_t sh = (uint32_t)unit / (uint32_t)slices;  // (there are fewer units than 2^31)
+  const uint32_t h = sh % (uint32_t)a.Hv, hk = h / ((uint32_t)a.Hv / (uint32_t)a.Hk);
+  const int64_t seq = sh / (uint32_t)a.Hv;
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sl = (wave >> 1) & 1, hf = wave & 1;
-  const int c0 = (int)(unit - sh * slices) * 32 + 16 * sl;
+  const int c0 = (int)((uint32_t)unit - sh * slices) * 32 + 16 * sl;
   const bool live = c0 < a.Dv;  // Dv may end with the first 16 columns
   int64_t lo, hi;
   clamp_range(a, seq, &lo, &hi);
@@ -765,7 +775,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 template <bool F16, int DK>
 hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
   const int64_t slots = delta_chunk_slots(a.tokens, a.nseq), prep = slots * a.Hv;
-  hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(256), 0, s, a, ws, prep);
+  hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(256), 0, s, a, ws, slots, prep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
