@@ -345,27 +345,49 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
 // parts keep the state in fp32.  Four waves with 16 columns and no division of labour
 // took 932 us for 16384 tokens when eight with 32 took 863.
 constexpr int kRunThreads = 512;
+
+// The sequence in `place` by length, the longest first, among its block of 64: the longest
+// ones have to start first, or the launch waits for them at its end (7 sequences of 39 to
+// 1969 tokens with 32 heads: 302 us in the order given, an XCD after the other, 127 so).
+__device__ __forceinline__ int64_t by_length(const DeltaArgs& a, int64_t place) {
+  const int lane = threadIdx.x & 63;
+  const int64_t base = place & ~(int64_t)63;
+  const int n = a.nseq - base < 64 ? (int)(a.nseq - base) : 64;
+  int64_t lo = 0, hi = 0;
+  if (lane < n) clamp_range(a, base + lane, &lo, &hi);
+  const int mine = (int)(hi - lo);
+  int before = 0;
+  for (int i = 0; i < n; ++i) {
+    const int other = __builtin_amdgcn_readlane(mine, i);
+    before += other > mine || (other == mine && i < lane);
+  }
+  const uint64_t found = __ballot(lane < n && before == (int)(place - base));
+  return base + __builtin_ctzll(found);
+}
+
 constexpr int kVRow = 64 + 16;  // LDS bytes of a row of 32 values
 
 template <bool F16, int DK, bool OUT32>
-__global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t slots, int64_t units) {
+__global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, const ChunkWs* ws, int64_t slots) {
   constexpr int KS = DK / 32, HS = KS / 2, KP = F16 ? 2 : 1, ST = DK / 32;  // k steps (a half), parts of k and q, state tiles
   constexpr int KROW = 2 * DK + (F16 && DK == 128 ? 16 : 32), CH = DK / 8, NL = C * CH / 256;  // LDS bytes of a key row, 16-byte pieces, loads
   __shared__ __align__(16) unsigned char kt[2][KP][C * KROW], qt[C * KROW], vt[C * kVRow];
   __shared__ __align__(16) u32x4 Ss[2][KS][3][64], Rs[2][3][64], Ws[2][2][3][64];
   __shared__ __align__(16) u32x4 Ts[6][3][64];
   __shared__ __align__(16) f32x4 Vs[2][4][64];
-  const int64_t unit = xcd_unit(units);
-  if (unit >= units) return;
-  const int slices = (a.Dv + 31) / 32;
-  const uint32_t sh = (uint32_t)unit / (uint32_t)slices;  // (there are fewer units than 2^31)
-  const uint32_t h = sh % (uint32_t)a.Hv, hk = h / ((uint32_t)a.Hv / (uint32_t)a.Hk);
-  const int64_t seq = sh / (uint32_t)a.Hv;
+  // (sequence, head) pairs go to the XCDs in turn, a pair's column slices to the same one,
+  // and where the heads divide evenly an XCD has neighbours, which share keys.  (There are
+  // fewer workgroups than 2^31.)
+  const uint32_t slices = (uint32_t)(a.Dv + 31) / 32, Hv = (uint32_t)a.Hv, at = blockIdx.x >> 3;
+  const uint32_t pair = at / slices * 8 + (blockIdx.x & 7), place = pair / Hv, j = pair - place * Hv;
+  if (place >= (uint64_t)a.nseq) return;
+  const uint32_t h = Hv % 8 == 0 ? (j & 7) * (Hv / 8) + (j >> 3) : j, hk = h / (Hv / (uint32_t)a.Hk);
+  const int64_t seq = a.nseq == 1 ? 0 : by_length(a, place);
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   // in a scalar register: matrix-core products ignore the lane mask, so what they are in must be a scalar branch
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sl = (wave >> 1) & 1, hf = wave & 1;
-  const int c0 = (int)((uint32_t)unit - sh * slices) * 32 + 16 * sl;
+  const int c0 = (int)(at % slices) * 32 + 16 * sl;
   const bool live = c0 < a.Dv;  // Dv may end with the first 16 columns
   int64_t lo, hi;
   clamp_range(a, seq, &lo, &hi);
@@ -778,12 +800,11 @@ hipError_t launch_t(const DeltaArgs& a, ChunkWs* ws, hipStream_t s) {
   hipLaunchKernelGGL((q1_chunk_prep<F16, DK>), dim3((unsigned)((prep + 7) / 8 * 8)), dim3(256), 0, s, a, ws, slots, prep);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
-  const dim3 grid((unsigned)((units + 7) / 8 * 8));
+  const dim3 grid((unsigned)((a.nseq * a.Hv + 7) / 8 * 8 * ((a.Dv + 31) / 32)));
   if (a.out_dtype == F32)
-    hipLaunchKernelGGL((q1_chunk_run<F16, DK, true>), grid, dim3(kRunThreads), 0, s, a, ws, slots, units);
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, true>), grid, dim3(kRunThreads), 0, s, a, ws, slots);
   else
-    hipLaunchKernelGGL((q1_chunk_run<F16, DK, false>), grid, dim3(kRunThreads), 0, s, a, ws, slots, units);
+    hipLaunchKernelGGL((q1_chunk_run<F16, DK, false>), grid, dim3(kRunThreads), 0, s, a, ws, slots);
   return hipGetLastError();
 }
 

@@ -306,3 +306,21 @@ def test_offsets_past_32_bits():
             want = Q.q1_delta_prefill(q, k, v, g, beta, state, cu, at, l2norm=True)
             got = Q.q1_delta_prefill(far(0, Hk), far(D, Hk), far(2 * D, Hv), g, beta, pool, cu, at + (slots - 3), l2norm=True)
         assert torch.equal(got, want) and torch.equal(pool[-3:], state)
+
+
+@pytest.mark.parametrize("nseq,Hk,Hv", [(64, 1, 3), (65, 2, 8), (150, 1, 1)])
+def test_many_sequences(nseq, Hk, Hv):
+    """Batches of many short sequences, empty ones among them: every one is done, whatever
+    the order they are started in."""
+    r = np.random.default_rng(nseq)
+    lens = r.integers(0, 90, nseq) * (r.random(nseq) < 0.8)
+    cu, D = np.cumsum([0, *lens]), 64
+    q, k, v, g, beta, state = draw(nseq, (int(cu[-1]),), Hk, Hv, D, D, "bf16", True, nseq)
+    slots = torch.from_numpy(r.permutation(nseq).astype(np.int32)).cuda()
+    before = state.clone()
+    out = Q.q1_delta_prefill(q, k, v, g, beta, state, torch.from_numpy(cu.astype(np.int32)).cuda(), slots, l2norm=True,
+                             out_dtype=torch.float32)
+    for i, s in enumerate(slots.tolist()):
+        at = slice(int(cu[i]), int(cu[i + 1]))
+        check_sequence(q[at], k[at], v[at], g[at], beta[at], before[s], True, D ** -0.5, C_PREFILL(D), out[at], state[s],
+                       "f32", f"sequence {i} of {lens[i]}")
