@@ -13,8 +13,7 @@ namespace q1 {
 
 // ---- gated delta rule -------------------------------------------------------
 
-// Sequence s of a launch: tokens [first, first + len) of the packed rows.  With
-// cu == nullptr every sequence has T tokens.
+// Rows of a sequence: T each (single tokens), or from cu[s] to cu[s + 1] (prompts).
 struct DeltaArgs {
   const uint16_t* q;
   const uint16_t* k;
@@ -29,9 +28,9 @@ struct DeltaArgs {
   int32_t Hk, Hv, Dv;
   int32_t out_dtype, l2norm;
   float scale;
-  int64_t T;        // tokens per sequence (cu == nullptr)
+  int64_t T;        // single tokens: tokens per sequence
   const int32_t* cu;
-  int64_t tokens;   // rows in all (cu != nullptr)
+  int64_t tokens;   // prompts: rows in all
   int64_t nseq;
 };
 

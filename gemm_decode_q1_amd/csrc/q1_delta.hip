@@ -11,6 +11,11 @@
 // holds all Dk rows of them: lane l has columns 4 (l % 8) .. +3 of rows
 // (l / 8) Dk/8 .. +Dk/8-1, so a load instruction reads whole 128-byte pieces
 // and the reduction over Dk is a sum over registers, then over 8 lanes.
+//
+// Bound by the state's bytes, read and written once whatever the number of tokens:
+// 61 sequences of 48 heads of 128x128 with 3 tokens each (390 MB) take 82 us, 4.75
+// TB/s, where a copy of 2 GiB reaches 4.86; 8 sequences (51 MB) 11.7 us; one (6 MB)
+// 5.2 us, which is a launch, two dependent reads and a write.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -158,8 +163,8 @@ __global__ __launch_bounds__(64 * kStepWaves) void q1_delta_recurrent_kernel(con
 hipError_t launch_delta_recurrent(const DeltaArgs& a, bool f16, int Dk, hipStream_t s) {
   const int64_t units = a.nseq * a.Hv * ((a.Dv + 31) / 32);
   // A workgroup of its own for each wave where they then still have a compute unit each (one
-  // sequence of 48 heads: 5.7 us, with four to a workgroup 6.2); more waves by four (8 such
-  // sequences: 12.5 us, one by one 12.7; 61 with 3 tokens each: 88 us, one by one 92).
+  // sequence of 48 heads: 5.2 us, with four to a workgroup 5.8); more waves by four (one by one,
+  // 8 such sequences took 2 % longer, 61 with 3 tokens each 4 %).
   const int waves = units <= device_cus() ? 1 : kStepWaves;
   const dim3 grid((unsigned)((units + waves - 1) / waves)), block(64 * waves);
 #define Q1_DR(H, D) hipLaunchKernelGGL((q1_delta_recurrent_kernel<H, D>), grid, block, 0, s, a)

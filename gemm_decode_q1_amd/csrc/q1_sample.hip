@@ -597,7 +597,7 @@ __device__ __forceinline__ u64 wave_most(u64 v) {
 
 // The candidates of a cut are worked on by W waves, four a thread, in registers: by one
 // wave up to kFew (every instruction costs the workgroup's 16 waves 16 cycles, and they
-// would wait for each other: a row with all filters took 12 us so, and 3 with one
+// would wait for each other: a row with all filters took 12 us so, and 7 with one
 // wave), by all of them beyond.
 constexpr int kFew = 256;
 constexpr int kEach = 4;
