@@ -44,6 +44,7 @@ _ATTN_PACK = struct.Struct("@9P7q5if").pack      # the fields of _Attn
 
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _empty = torch.empty
+_new = torch.empty_strided  # half the host time of torch.empty
 
 
 def _stream_of(index: int) -> int:
@@ -115,6 +116,15 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _dense_strides(shape):
+    """Strides of a contiguous tensor."""
+    strides, n = [], 1
+    for m in reversed(shape):
+        strides.append(n)
+        n *= m
+    return tuple(reversed(strides))
+
+
 def _check_delta(q, k, v, g, beta, state, slots, nseq, out, out_dtype):
     """The descriptor's fields that follow from the operands' layouts."""
     _same_device(q, k=k, v=v, g=g, beta=beta, state=state, slots=slots, out=out)
@@ -141,10 +151,11 @@ def _check_delta(q, k, v, g, beta, state, slots, nseq, out, out_dtype):
         out_dtype = v.dtype
     lds = (_row_stride(q, "q", lead), _row_stride(k, "k", lead), _row_stride(v, "v", lead))
     return (lds, (state.shape[0], Hk, Hv, Dk, Dv, _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out_dtype, -1)),
-            out_dtype, Dk ** -0.5, q.get_device())
+            out_dtype, Dk ** -0.5, q.get_device(), tuple(v.shape), _dense_strides(v.shape), v.device)
 
 
 _delta_layouts = {}
+_prefill_needs = {}
 
 
 def _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype):
@@ -159,12 +170,12 @@ def _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype):
         if len(_delta_layouts) > 4096:
             _delta_layouts.clear()
         _delta_layouts[key] = found
-    lds, ints, dtype, usual, index = found
+    lds, ints, dtype, usual, index, shape, strides, device = found
     if out is None:
-        out = _empty(v.shape, dtype=dtype, device=v.device)
+        out = _new(shape, strides, dtype=dtype, device=device)
     return _DELTA_PACK(q.data_ptr(), k.data_ptr(), v.data_ptr(), *lds, g.data_ptr(), beta.data_ptr(), state.data_ptr(),
                        0 if slots is None else slots.data_ptr(), out.data_ptr(), *ints, 1 if l2norm else 0,
-                       usual if scale is None else scale), out, index
+                       usual if scale is None else scale), out, index, ints
 
 
 def q1_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -181,7 +192,7 @@ def q1_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if q.dim() != 4:
         raise ValueError("q must be [B, T, Hk, Dk]")
     B, T = q.shape[0], q.shape[1]
-    d, out, index = _delta(q, k, v, g, beta, state, slots, B, scale, l2norm, out, out_dtype)
+    d, out, index, _ = _delta(q, k, v, g, beta, state, slots, B, scale, l2norm, out, out_dtype)
     status = load_library().q1_delta_step(d, B, T, _stream_of(index))
     if status:
         _check(status)
@@ -203,13 +214,17 @@ def q1_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     nseq, tokens = cu_seqlens.numel() - 1, q.shape[0]
     if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous int32")
-    d, out, index = _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype)
+    d, out, index, ints = _delta(q, k, v, g, beta, state, slots, nseq, scale, l2norm, out, out_dtype)
     if cu_seqlens.get_device() != index:
         raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, q on {q.device}")
     L = load_library()
     stream = _stream_of(index)
     if workspace is None:
-        need = L.q1_delta_prefill_workspace_bytes(d, tokens, nseq)
+        need = _prefill_needs.get((tokens, nseq, ints))
+        if need is None:
+            if len(_prefill_needs) > 4096:
+                _prefill_needs.clear()
+            need = _prefill_needs[tokens, nseq, ints] = L.q1_delta_prefill_workspace_bytes(d, tokens, nseq)
         workspace = _workspace(need, index, stream) if need else None
     status = L.q1_delta_prefill(d, tokens, nseq, cu_seqlens.data_ptr(), _ptr(workspace),
                                 0 if workspace is None else workspace.numel(), stream)
@@ -249,23 +264,24 @@ def q1_prefix_attn(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix: 
     found = _attn_layouts.get(key)
     if found is None:
         found = _check_attn(q, k_prefix, v_prefix, k_pages, v_pages, page_table, suffix_lens, out, out_dtype, lse)
-        if len(_attn_layouts) > 4096:
-            _attn_layouts.clear()
-        _attn_layouts[key] = found
-    longs, ints, dtype, usual, index = found
+    longs, ints, dtype, usual, index, shape, strides, device, need = found
     P, pages, max_pages = longs[3], longs[4], longs[5]
     if out is None:
-        out = _empty(q.shape, dtype=dtype, device=q.device)
+        out = _new(shape, strides, dtype=dtype, device=device)
     if lse is None:
-        lse = _empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _new(shape[:2], (shape[1], 1), dtype=torch.float32, device=device)
     a = _ATTN_PACK(q.data_ptr(), k_prefix.data_ptr() if P else 0, v_prefix.data_ptr() if P else 0,
                    k_pages.data_ptr() if pages else 0, v_pages.data_ptr() if pages else 0,
                    page_table.data_ptr() if max_pages else 0, suffix_lens.data_ptr() if max_pages else 0,
                    out.data_ptr(), lse.data_ptr(), *longs, *ints, usual if scale is None else scale)
     L = load_library()
     stream = _stream_of(index)
-    if workspace is None:
+    if need is None:  # a layout that is new: its workspace depends on nothing else
         need = L.q1_prefix_attn_workspace_bytes(a)
+        if len(_attn_layouts) > 4096:
+            _attn_layouts.clear()
+        _attn_layouts[key] = (*found[:-1], need)
+    if workspace is None:
         workspace = _workspace(need, index, stream) if need else None
     status = L.q1_prefix_attn(a, _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
     if status:
@@ -317,7 +333,7 @@ def _check_attn(q, k_prefix, v_prefix, k_pages, v_pages, page_table, suffix_lens
     _dense(lse, "lse", torch.float32, (B, Hq))
     return ((_row_stride(q, "q", 1), prefix_ld, B, P, pages, max_pages, page_size),
             (Hq, Hkv, D, _TORCH_TO_Q1.get(q.dtype, -1), _TORCH_TO_Q1.get(out_dtype, -1)), out_dtype, 1.0 / math.sqrt(D),
-            q.get_device())
+            q.get_device(), (B, Hq, D), (Hq * D, D, 1), q.device, None)
 
 
 def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
@@ -344,11 +360,11 @@ def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch
         if len(_sample_layouts) > 4096:
             _sample_layouts.clear()
         _sample_layouts[key] = found
-    B, V, ld, dtype, need, index = found
+    B, V, ld, dtype, need, index, device = found
     if tokens is None:
-        tokens = _empty(B, dtype=torch.int64, device=logits.device)
+        tokens = _new((B,), (1,), dtype=torch.int64, device=device)
     if logprob is None:
-        logprob = _empty(B, dtype=torch.float32, device=logits.device)
+        logprob = _new((B,), (1,), dtype=torch.float32, device=device)
     stream = _stream_of(index)
     if workspace is None and need:
         workspace = _workspace(need, index, stream)
@@ -364,7 +380,7 @@ _sample_layouts = {}
 
 
 def _check_sample(L, logits, u, temperature, top_k, top_p, min_p, tokens, logprob):
-    """What follows from the operands' layouts: (B, V, row stride, dtype, workspace bytes, device)."""
+    """What follows from the operands' layouts: (B, V, row stride, dtype, workspace bytes, device index, device)."""
     if logits.dim() != 2:
         raise ValueError("logits must be [B, V]")
     _same_device(logits, u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
@@ -381,4 +397,4 @@ def _check_sample(L, logits, u, temperature, top_k, top_p, min_p, tokens, logpro
         _dense(tokens, "tokens", tokens.dtype, (B,))
     _dense(logprob, "logprob", torch.float32, (B,))
     return (B, V, _row_stride(logits, "logits", 1), _TORCH_TO_Q1.get(logits.dtype, -1),
-            L.q1_sample_workspace_bytes(B, V) if V > 0 else 0, logits.get_device())
+            L.q1_sample_workspace_bytes(B, V) if V > 0 else 0, logits.get_device(), logits.device)
