@@ -312,7 +312,7 @@ def _check_attn(q, k_prefix, v_prefix, k_pages, v_pages, page_table, suffix_lens
         if k_prefix.dim() != 3 or k_prefix.shape[1:] != (Hkv, D) or v_prefix.shape != k_prefix.shape:
             raise ValueError(f"k_prefix and v_prefix must be [P, {Hkv}, {D}]")
         P, prefix_ld = k_prefix.shape[0], _row_stride(k_prefix, "k_prefix", 1)
-        if P > 1 and _row_stride(v_prefix, "v_prefix", 1) != prefix_ld:
+        if P > 0 and _row_stride(v_prefix, "v_prefix", 1) != prefix_ld and P > 1:  # (one row's stride is never used)
             raise ValueError("k_prefix and v_prefix must have the same row stride")
     pages = max_pages = page_size = 0
     if k_pages is not None:
