@@ -70,6 +70,13 @@ def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     return t
 
 
+def _given(workspace: torch.Tensor, index: int) -> torch.Tensor:
+    """A workspace of the caller's: bytes, all of them there, on the operands' device."""
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
+    return workspace
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -226,6 +233,8 @@ def q1_delta_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
                 _prefill_needs.clear()
             need = _prefill_needs[tokens, nseq, ints] = L.q1_delta_prefill_workspace_bytes(d, tokens, nseq)
         workspace = _workspace(need, index, stream) if need else None
+    else:
+        _given(workspace, index)
     status = L.q1_delta_prefill(d, tokens, nseq, cu_seqlens.data_ptr(), _ptr(workspace),
                                 0 if workspace is None else workspace.numel(), stream)
     if status:
@@ -283,6 +292,8 @@ def q1_prefix_attn(q: torch.Tensor, k_prefix: Optional[torch.Tensor], v_prefix: 
         _attn_layouts[key] = (*found[:-1], need)
     if workspace is None:
         workspace = _workspace(need, index, stream) if need else None
+    else:
+        _given(workspace, index)
     status = L.q1_prefix_attn(a, _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)
     if status:
         _check(status)
@@ -366,8 +377,10 @@ def q1_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch
     if logprob is None:
         logprob = _new((B,), (1,), dtype=torch.float32, device=device)
     stream = _stream_of(index)
-    if workspace is None and need:
-        workspace = _workspace(need, index, stream)
+    if workspace is None:
+        workspace = _workspace(need, index, stream) if need else None
+    else:
+        _given(workspace, index)
     status = L.q1_sample(logits.data_ptr(), dtype, B, V, ld, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
                          _ptr(min_p), tokens.data_ptr(), 1 if tokens.dtype == torch.int64 else 0, logprob.data_ptr(),
                          _ptr(workspace), 0 if workspace is None else workspace.numel(), stream)

@@ -37,3 +37,54 @@ def test_one_prefix_token_may_have_any_row_stride():
     assert attn_layout(k, v)
     with pytest.raises(ValueError, match="row stride"):
         attn_layout(*(torch.zeros(3, n, 64, dtype=torch.bfloat16)[:2, :2] for n in (2, 5)))
+
+
+
+class Library:
+    """Stands in for the library: takes any call, wants 4096 bytes of workspace."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_bytes"):
+            return lambda *args: 4096
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(D, "load_library", lambda: lib)
+    monkeypatch.setattr(D, "_stream_of", lambda index: 0)
+    monkeypatch.setattr(D, "_device", lambda: -1)
+    return lib
+
+
+def call(op, **kw):
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(*shape, dtype=dtype)  # noqa: E731
+    f = torch.float32
+    if op == "sample":
+        return D.q1_sample(z(2, 100, dtype=f), z(2, dtype=f), **kw)
+    if op == "attn":
+        return D.q1_prefix_attn(z(2, 4, 64), z(9, 2, 64), z(9, 2, 64), **kw)
+    return D.q1_delta_prefill(z(9, 1, 64), z(9, 1, 64), z(9, 2, 64), z(9, 2, dtype=f), z(9, 2, dtype=f),
+                              z(1, 2, 64, 64, dtype=f), torch.tensor([0, 9], dtype=torch.int32), **kw)
+
+
+OPS = ["sample", "attn", "prefill"]
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_a_given_workspace_is_checked(library, op):
+    """Its bytes are counted from its elements, and the kernels write to all of them:
+    so bytes, dense, on the operands' device."""
+    call(op, workspace=torch.zeros(4096, dtype=torch.uint8))
+    assert len(library.calls) == 1 and 4096 in library.calls[0][1]
+    for odd in (torch.zeros(4096), torch.zeros(8192, dtype=torch.uint8)[::2],
+                torch.zeros(1, dtype=torch.uint8).expand(4096)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(op, workspace=odd)
+    assert len(library.calls) == 1
+    with pytest.raises(ValueError, match="workspace"):
+        D._given(torch.zeros(4096, dtype=torch.uint8), 0)  # host memory beside operands on device 0
