@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+import threading
 from typing import Optional
 
 import torch
@@ -52,21 +53,31 @@ def _stream_of(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-_scratch = {}
+class _Scratch(threading.local):
+    """The workspaces of one thread, by (device, stream)."""
+
+    def __init__(self):
+        self.kept = {}
+
+
+_scratch = _Scratch()
 _capturing = torch.cuda.is_current_stream_capturing
 
 
 def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     """Device workspace of these calls (no initial contents needed): one per
-    (device, stream), grown on demand.  A call under graph capture gets one of its
-    own, from the graph's memory: a shared one would be freed as it grows, and be
-    used by replays on other streams."""
+    (thread, device, stream), grown on demand.  A call is several launches that hand
+    data on through it, and another thread's launches may come between them on the
+    same stream.  A call under graph capture gets one of its own, from the graph's
+    memory: a shared one would be freed as it grows, and be used by replays on other
+    streams."""
     if _capturing():
         return _empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
-    t = _scratch.get((index, stream))
+    kept = _scratch.kept
+    t = kept.get((index, stream))
     if t is None or t.numel() < nbytes:
         t = _empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=torch.device("cuda", index))
-        _scratch[index, stream] = t
+        kept[index, stream] = t
     return t
 
 

@@ -149,9 +149,11 @@ def _stream(device=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-class _Workspaces:
-    """Zero-filled device workspaces, one per (device, stream), grown on demand.
-    The library leaves the zero-required part zero after every call."""
+class _Workspaces(threading.local):
+    """Zero-filled device workspaces, one per (thread, device, stream), grown on
+    demand: a call may be several launches, between which another thread's may come
+    on the same stream.  The library leaves the zero-required part zero after every
+    call."""
 
     def __init__(self):
         self._ws = {}

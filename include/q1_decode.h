@@ -7,7 +7,9 @@
  * before any HIP call, then the workspace check, then the device check; calls
  * only enqueue work on `stream`, allocate nothing, keep nothing between calls,
  * and can be captured in a HIP graph.  Workspaces here need no initial
- * contents (the reserved block of q1.h is not used).
+ * contents (the reserved block of q1.h is not used); calls that may run at the
+ * same time, and calls of several threads on one stream, need separate ones (a
+ * call is several launches that hand data on through its workspace).
  *
  * Numbers the kernels read from device memory (lengths, offsets, page and slot
  * ids) cannot be checked by the call; each one below says what an id outside

@@ -1,9 +1,15 @@
 """What the decode binding checks of its operands' layouts, on host tensors (no GPU
 needed: the device check is taken out)."""
+import ctypes
+import gc
+import threading
+import weakref
+
 import pytest
 import torch
 
 from gemm_decode_q1_amd import decode as D
+from gemm_decode_q1_amd import q1 as B
 
 
 @pytest.fixture(autouse=True)
@@ -88,3 +94,47 @@ def test_a_given_workspace_is_checked(library, op):
     assert len(library.calls) == 1
     with pytest.raises(ValueError, match="workspace"):
         D._given(torch.zeros(4096, dtype=torch.uint8), 0)  # host memory beside operands on device 0
+
+
+def in_thread(f):
+    t = threading.Thread(target=f)
+    t.start()
+    t.join()
+
+
+def test_a_thread_has_a_workspace_of_its_own(monkeypatch):
+    """A call is several launches that hand data on through its workspace, and another thread's may come
+    between them on the same stream: threads share none.  A thread's calls share one, freed as it ends."""
+    made = []
+
+    def empty(n, dtype, device):
+        t = torch.empty(n, dtype=dtype)
+        made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(D, "_empty", empty)
+    monkeypatch.setattr(D, "_capturing", lambda: False)
+
+    def nested():
+        mine = D._workspace(100000, 0, 7)
+        assert D._workspace(4096, 0, 7) is mine and D._workspace(4096, 0, 8) is not mine
+        in_thread(lambda: others.append(D._workspace(4096, 0, 7)))
+        assert others and others[0] is not mine and others[0].data_ptr() != mine.data_ptr()
+        done.append(1)
+
+    others, done = [], []
+    in_thread(nested)
+    assert done and len(made) == 3
+    others.clear()
+    gc.collect()
+    assert all(r() is None for r in made)
+
+
+def test_packed_calls_share_no_workspace_between_threads(monkeypatch):
+    monkeypatch.setattr(B, "_stream", lambda device=None: ctypes.c_void_p(7))
+    spaces, host, got = B._Workspaces(), torch.device("cpu"), []
+    take = lambda: got.append(spaces.get(1000, host))  # noqa: E731
+    take()
+    in_thread(take)
+    take()
+    assert got[0] is got[2] and got[1] is not got[0] and got[0].data_ptr() != got[1].data_ptr()
