@@ -545,7 +545,8 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_join(const q1_attn a, con
 #pragma unroll
   for (int e = 0; e < E; ++e) so[wave][64 * e + lane] = o[e];
   __syncthreads();
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  const bool nothing = sum == 0.f;  // no token, or none above -infinity (a NaN stays one)
+  const float inv = nothing ? 0.f : 1.0f / sum;
   if (threadIdx.x < D) {
     float t = 0.f;
 #pragma unroll
@@ -553,7 +554,7 @@ __global__ __launch_bounds__(64 * kWaves) void q1_attn_join(const q1_attn a, con
     store_out(a.out, a.out_dtype, row * D + threadIdx.x, t * inv);
   }
   if (threadIdx.x == 0 && a.lse != nullptr)
-    a.lse[row] = sum > 0.f ? (top - lift) * 0.69314718055994530942f + logf(sum) : -INFINITY;
+    a.lse[row] = nothing ? -INFINITY : (top - lift) * 0.69314718055994530942f + logf(sum);
 }
 
 template <bool F16, int D, int NM, bool BYROWS>

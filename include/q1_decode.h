@@ -84,6 +84,10 @@ size_t q1_delta_prefill_workspace_bytes(const q1_delta* d, int64_t tokens, int64
  * page_size]; a token whose page id is outside [0, pages) is left out.  A row
  * with no token at all gives zeros and lse = -infinity.  Rows past a length
  * are never used, whatever they hold.  Scores, softmax and sums are fp32.
+ * A NaN or +infinite score of a token that counts makes its row's out and lse
+ * NaN.  A NaN or infinite value of such a token makes its column of the row
+ * NaN, or infinite where it is (weights enter the product in two parts, of which
+ * one may be 0 or negative: an infinite sum can become NaN).
  */
 typedef struct q1_attn {
   const void* q;               /* [B, Hq, D] with q_ld elements between sequences; 16-byte aligned, q_ld % 8 == 0 */

@@ -213,3 +213,51 @@ def test_offsets_past_32_bits(dt):
     got = Q.q1_prefix_attn(q, wide[0], wide[1], big[0], big[1], table + far, n, out_dtype=torch.float32)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check(got[0], got[1], q, kp, vp, kc, vc, table, lens, page, "f32", D ** -0.5, "far")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,P", [(3, 6, 2, 64, 700), (3, 4, 2, 256, 90), (24, 8, 2, 128, 300), (3, 8, 2, 128, 0)])
+def test_nan_and_infinity_in_what_counts(B, Hq, Hkv, D, P, dt):
+    """A NaN or an infinite score makes its rows NaN, the sum of weights too (-infinity would say that there is
+    no token); a NaN or infinite value its column, not the sum; other rows and columns keep their bits."""
+    lens, page, group = [9 + 5 * (b % 7) for b in range(B)], 16, Hq // Hkv
+    q, kp, vp, kc, vc, table, n = draw(21, B, Hq, Hkv, D, P, lens, page, dt)
+    call = lambda q, kp, vp, kc, vc: Q.q1_prefix_attn(q, *((kp, vp) if P else (None, None)), kc, vc, table, n,  # noqa: E731
+                                                      out_dtype=torch.float32)
+    clean, clean_lse = call(q, kp, vp, kc, vc)
+    nan, inf = float("nan"), float("inf")
+    where = (table[1, 0].item(), 3)  # a token of sequence 1 that counts
+
+    def same_but(got, rows, columns, lse_too):
+        """NaN (for a bad value: or infinite) in `rows` (sequence, head) and `columns`, the clean run's bits elsewhere."""
+        out, lse = got
+        hit = torch.zeros(B, Hq, D, dtype=torch.bool).cuda()
+        for b, h in rows:
+            hit[b, h, columns] = True
+        assert (out[hit].isnan() if lse_too else ~out[hit].isfinite()).all() and torch.equal(out[~hit], clean[~hit])
+        hit = hit.any(-1) if lse_too else torch.zeros_like(lse, dtype=torch.bool)
+        assert lse[hit].isnan().all() and torch.equal(lse[~hit], clean_lse[~hit])
+
+    every = slice(None)
+    x = q.clone()
+    x[1, 2, 7] = nan
+    same_but(call(x, kp, vp, kc, vc), [(1, 2)], every, True)
+    first = [(1, h) for h in range(group)]  # the rows of key head 0
+    x = kc.clone()
+    x[where[0], where[1], 0, 5] = nan
+    same_but(call(q, kp, vp, x, vc), first, every, True)
+    x[where[0], where[1], 0] = 0
+    x[where[0], where[1], 0, 5] = inf
+    y = q.clone()
+    y[1, :, 5] = 1.0  # a score of +infinity
+    out, lse = call(y, kp, vp, x, vc)
+    assert out[1, :group].isnan().all() and lse[1, :group].isnan().all()
+    assert torch.isfinite(out[:, group:]).all() and torch.isfinite(lse[:, group:]).all() and torch.isfinite(out[2:]).all()
+    for bad in (nan, inf, -inf):
+        x = vc.clone()
+        x[where[0], where[1], 0, 5] = bad
+        same_but(call(q, kp, vp, kc, x), first, [5], False)
+    if P:
+        x = kp.clone()
+        x[P - 1, 1, 0] = nan
+        same_but(call(q, x, vp, kc, vc), [(b, h) for b in range(B) for h in range(group, Hq)], every, True)
