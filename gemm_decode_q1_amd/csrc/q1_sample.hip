@@ -556,7 +556,8 @@ __global__ __launch_bounds__(kThreads, 8) void q1_sample_cut(const SampleArgs a,
     const bool low = e < r.mp;
     if (bin < sure && !low) sum += w;
     const ulonglong2 entry = {composite(clean(x), i), w | (low ? 1ull << 63 : 0)};
-    if (bin == c.bin_k) {
+    // (with top-p, elements without a weight are in no bin's count, and there may be any number of them)
+    if (bin == c.bin_k && (w != 0 || !r.use_p)) {
       const uint32_t at = atomicAdd(&ws.cut[b].got_k, 1u);
       if (at < kMost) ws.cand[(b * 2) * kMost + at] = entry;
     }

@@ -237,3 +237,23 @@ def test_offsets_past_32_bits():
     for filters in (dict(), dict(top_p=dev([0.8] * B)), dict(top_k=dev([30] * B, torch.int32))):
         a, b = Q.q1_sample(wide, u, **filters), Q.q1_sample(x, u, **filters)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_weightless_logits_beside_the_cut():
+    """A top-k cut among the smallest weights there are, with thousands of logits just below them that have
+    none: these are no candidates.  The sum of what top-k keeps decides here whether top-p keeps token 0."""
+    V, k, p = 20000, 400, np.float32(1 - 2.0 ** -24)
+    r = np.random.default_rng(3)
+    x = np.full(V, -100.0)
+    at = 2 + r.permutation(V - 3)[:16000]
+    x[at[:1000]] = -27.7245    # weight 1
+    x[at[1000:]] = -27.732     # weight 0
+    x[V - 1], x[1] = 0.0, -10.0
+    # top-p keeps token 0 if token 1 and the largest lie below p times the sum: by 50 units here, less than
+    # the units that top-k keeps
+    others = 2.0 ** 40 + np.floor(np.exp(-10.0) * 2.0 ** 40)
+    own = (others + 50) / float(p) - others - (k - 3)
+    x[0] = np.log(own / 2.0 ** 40)
+    row = torch.from_numpy(x).float().cuda()[None]
+    assert R.sample(row[0].cpu().numpy(), 0.0, 1.0, k, float(p))[0] == 0
+    check(row, [0.0], k=[k], p=[float(p)], what="weightless")
