@@ -12,9 +12,11 @@
 //
 // The state is held and returned in fp32 and nothing that reaches it may lose
 // that: an fp32 operand of a matrix-core product is taken as three bf16 parts
-// (8 significant bits each, exact), of which the products down to 2^-24 are
-// summed; k, q and v are exact (bf16, or two parts of an fp16 value).  What only
-// reaches the output (P, and S0 and V' as factors of it) has two parts, 2^-17.
+// (8 significant bits each, cut off, all 24 together), k, q and v as they are
+// (bf16, or two parts of an fp16 value: exact).  A product of two fp32 operands
+// (T R) sums the products of parts down to 2^-21: what it leaves out is below that
+// of the summed magnitudes.  Outputs in fp32 are made the same way; for those in 16
+// bits P, and S0 and V' as its factors, have two parts.
 // G is summed in 64 bits, so that a difference of two sums is as exact as the
 // decays between them whatever came before; the inverse is made by substitution
 // and fp32 products.
@@ -53,7 +55,7 @@ constexpr int C = kDeltaChunk;
 // walks through them; a chunk's heads together cost it a new page every chunk): T
 // and P in 10 tiles (it, jt <= it) of 64 lanes x 16 bytes -- T: row 16 it + l%16,
 // columns 16 jt + 4(l/16) .. +3 in fp32; P: the same elements as four high and four
-// low parts -- then the factors.  T as the three bf16 parts that the run takes it in,
+// low parts, or in fp32 for outputs in fp32 -- then the factors.  T as the three bf16 parts that the run takes it in,
 // and pairs of tiles with zeros, were 31 KB instead of 21.
 struct ChunkWs {
   f32x4 T[10][64];
@@ -262,8 +264,12 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
         qk[e] = i >= j0 + e ? qi * qk[e] * d : 0.f;
       }
       *reinterpret_cast<f32x4*>(&A[i * AS + j0]) = kk;
-      const u32x2 ph = part(qk), pl = part(qk);
-      w->P[it * (it + 1) / 2 + jt][lane] = u32x4{ph[0], ph[1], pl[0], pl[1]};
+      u32x4 pw = __builtin_bit_cast(u32x4, qk);
+      if (a.out_dtype != F32) {
+        const u32x2 ph = part(qk), pl = part(qk);
+        pw = u32x4{ph[0], ph[1], pl[0], pl[1]};
+      }
+      w->P[it * (it + 1) / 2 + jt][lane] = pw;
     };
     for (int jt = 0; jt <= it; ++jt) tile(jt);
   }
@@ -691,6 +697,30 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         f32x4 x = Vs[sl][2 * k][lane], y = Vs[sl][2 * k + 1][lane];
+        if constexpr (OUT32) {  // three parts of both, as in the state
+          u32x4 vp[3], pp[2][3];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const u32x2 xp = part(x), yp = part(y);
+            vp[p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            f32x4 px = __builtin_bit_cast(f32x4, P[i][2 * k]), py = __builtin_bit_cast(f32x4, P[i][2 * k + 1]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+              const u32x2 xp = part(px), yp = part(py);
+              pp[i][p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+            }
+          }
+#pragma unroll
+          for (int n = 2; n >= 0; --n)
+#pragma unroll
+            for (int p = 0; p <= n; ++p)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) o[i] = mma(vp[p], pp[i][n - p], o[i]);
+          continue;
+        }
         const u32x2 x0 = part(x), x1 = part(x), y0 = part(y), y1 = part(y);
         const u32x4 v0 = {x0[0], x0[1], y0[0], y0[1]}, v1 = {x1[0], x1[1], y1[0], y1[1]};
         u32x4 ph[2], pl[2];
@@ -745,7 +775,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       qs[0] = qs[1] = zero;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const u32x4 s0 = Ss[sl][s][0][lane], s1 = Ss[sl][s][1][lane];
+        const u32x4 s0 = Ss[sl][s][0][lane], s1 = Ss[sl][s][1][lane], s2 = Ss[sl][s][2][lane];
         u32x4 Q[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) Q[i] = *reinterpret_cast<const u32x4*>(&qt[(32 * hf + 16 * i + col) * KROW + 64 * s + 16 * grp]);
@@ -760,6 +790,12 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
               q0[i][e] = h0;
               q1[i][e] = h1;
             }
+          if constexpr (OUT32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qs[i] = mma(s2, q0[i], qs[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qs[i] = mma(s1, q1[i], qs[i]);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) qs[i] = mma(s0, q1[i], qs[i]);
 #pragma unroll
@@ -767,6 +803,10 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
 #pragma unroll
           for (int i = 0; i < 2; ++i) qs[i] = mma(s0, q0[i], qs[i]);
         } else {
+          if constexpr (OUT32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qs[i] = mma(s2, Q[i], qs[i]);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) qs[i] = mma(s1, Q[i], qs[i]);
 #pragma unroll
