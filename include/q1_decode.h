@@ -30,8 +30,9 @@ extern "C" {
  *   S_t = a_t S_{t-1} + k_t (x) beta_t (v_t - a_t S_{t-1}^T k_t)
  *   o_t = scale * S_t^T q_t
  * With l2norm = 1, q and k are first divided by sqrt(sum of squares + 1e-6).
- * State, sums and exponentials are fp32; outputs are rounded once.
- * g = -infinity (a = 0) forgets the state exactly.
+ * State, sums and exponentials are fp32; outputs are rounded once (of prompts
+ * with a 16-bit out_dtype, see q1_delta_prefill).
+ * g = -infinity (a = 0) forgets a finite state exactly.
  */
 typedef struct q1_delta {
   const void* q;           /* token t, key head j, element i: q[t*q_ld + j*Dk + i]; 16-byte aligned */
@@ -64,7 +65,9 @@ q1_status q1_delta_step(const q1_delta* d, int64_t B, int64_t T, void* stream);
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 (device int32 [nseq + 1], not decreasing,
  * from 0 to `tokens`; offsets outside [0, tokens] are clamped, an empty
  * sequence keeps its state, rows of no sequence are not written).  The same
- * result as q1_delta_step over the same tokens, to fp32 rounding.  A NaN or
+ * result as q1_delta_step over the same tokens, to fp32 rounding; outputs in a
+ * 16-bit type are rounded from sums that are up to 2^-13 of their terms' magnitudes
+ * off with bf16 operands, 2^-15 with fp16 ones.  A NaN or
  * infinity in q, k, v or beta spreads to the whole chunk of up to 64 tokens it is in
  * (and, as in the recurrence, to what follows).
  *   workspace  q1_delta_prefill_workspace_bytes(...) bytes, 256-byte aligned.
