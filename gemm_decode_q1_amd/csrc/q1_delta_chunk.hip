@@ -694,6 +694,21 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
         }
       }
     };
+    u32x4 Pp[2][2][OUT32 ? 3 : 1];  // P's parts, for outputs in fp32: made before the output needs them, where
+                                    // these waves wait (16384 tokens of 48 heads 774 us, with the output 821)
+    auto split_p = [&]() {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          f32x4 x = __builtin_bit_cast(f32x4, P[i][2 * k]), y = __builtin_bit_cast(f32x4, P[i][2 * k + 1]);
+#pragma unroll
+          for (int p = 0; p < (OUT32 ? 3 : 1); ++p) {
+            const u32x2 xp = part(x), yp = part(y);
+            Pp[i][k][p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
+          }
+        }
+    };
     const int o_off = live ? (32 * hf + col) * (int)o_ld + (c0 + 4 * grp) * esz : kNone;
     f32x4 qs[2] = {zero, zero};
     // O^T = scale s e^G (Q S0)^T + V'^T P^T; a lane has token 32 hf + 16 i + col
@@ -705,27 +720,18 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
       for (int k = 0; k < 2; ++k) {
         f32x4 x = Vs[sl][2 * k][lane], y = Vs[sl][2 * k + 1][lane];
         if constexpr (OUT32) {  // three parts of both, as in the state
-          u32x4 vp[3], pp[2][3];
+          u32x4 vp[3];
 #pragma unroll
           for (int p = 0; p < 3; ++p) {
             const u32x2 xp = part(x), yp = part(y);
             vp[p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            f32x4 px = __builtin_bit_cast(f32x4, P[i][2 * k]), py = __builtin_bit_cast(f32x4, P[i][2 * k + 1]);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-              const u32x2 xp = part(px), yp = part(py);
-              pp[i][p] = u32x4{xp[0], xp[1], yp[0], yp[1]};
-            }
-          }
-#pragma unroll
           for (int n = 2; n >= 0; --n)
 #pragma unroll
             for (int p = 0; p <= n; ++p)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) o[i] = mma(vp[p], pp[i][n - p], o[i]);
+              for (int i = 0; i < 2; ++i) o[i] = mma(vp[p], Pp[i][k][n - p], o[i]);
           continue;
         }
         const u32x2 x0 = part(x), x1 = F16 ? nearest(x) : part(x), y0 = part(y), y1 = F16 ? nearest(y) : part(y);
@@ -822,6 +828,7 @@ __global__ __launch_bounds__(kRunThreads) void q1_chunk_run(const DeltaArgs a, c
           for (int i = 0; i < 2; ++i) qs[i] = mma(s0, Q[i], qs[i]);
         }
       }
+      if constexpr (OUT32) split_p();
       __syncthreads();
       // while they make V' and half of the new state: the next keys, values and queries
       split_t();
