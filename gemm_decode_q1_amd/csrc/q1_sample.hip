@@ -23,7 +23,10 @@
 // composites differ; a cut is one composite, and kept are those not below it.
 //
 // Where a cut's bins hold more than kMost candidates (rows that are flat, or full
-// of equal logits) the draw falls back to a radix select over the row itself.
+// of equal logits), or a top-k bound leaves more (the logits above -infinity lie in
+// fewer groups than k), the draw falls back to a radix select over the row itself by
+// one workgroup: 0.8 ms for 1 or 8 flat rows of 152064, 0.43 for 8000 logits in a run
+// beside -infinity with top-k 200 (with top-k 100, 26 us).
 //
 // What bounds it: for many rows the first launch reads the logits at the rate of a
 // plain read (192 rows of 152064 in fp32, 117 MB: 19 us, 6.1 TB/s); the second and
@@ -128,7 +131,12 @@ __device__ __host__ __forceinline__ int groups(int S) { return S * kThreads / gr
 // few: all that top-k may keep are candidates (see q1_sample_hist).  The k-th largest of
 // the groups' largest logits is near the k-th of all as long as k is a small part of the
 // groups (at a quarter, about 1.15 k elements are above it, at all of them no bound is
-// left).  Rows of up to kMost elements fit as they are.
+// left).  Rows of up to kMost elements fit as they are.  It saves a pass over the row and
+// wins while one wave's select takes the candidates: k = 50, 152064 logits, 1 / 64 / 192
+// rows 15.6 / 33 / 60 us, with the histogram 18.2 / 39 / 80; k = 200, 20.6 / 35 / 61 and
+// 19.3 / 40 / 79.  Past that the select by all waves costs 11 us, k = 400, 33 / 47 / 72 and
+// 19.4 / 40 / 80, so only a batch whose pass takes longer does it (equal at 96 to 128 rows).
+constexpr int kFew = 256;  // candidates that one wave works on (see cut_candidates)
 __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b, int S) {
   Row r;
   r.T = a.temperature ? a.temperature[b] : 1.0f;
@@ -140,7 +148,8 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, int64_t b, int S) {
   r.mp = r.mp > 0.f ? fminf(r.mp, 1.f) : 0.f;
   r.use_k = !r.greedy && r.k > 0 && r.k < a.V;
   r.use_p = !r.greedy && r.p < 1.f;
-  r.few = r.use_k && (r.k <= groups(S) / 4 || a.V <= kMost);
+  const bool near = r.k <= groups(S) / 4 && (r.k <= kFew * 4 / 5 || a.B * a.V >= 1 << 24);
+  r.few = r.use_k && (near || a.V <= kMost);
   return r;
 }
 
@@ -600,7 +609,6 @@ __device__ __forceinline__ u64 wave_most(u64 v) {
 // wave up to kFew (every instruction costs the workgroup's 16 waves 16 cycles, and they
 // would wait for each other: a row with all filters took 12 us so, and 7 with one
 // wave), by all of them beyond.
-constexpr int kFew = 256;
 constexpr int kEach = 4;
 static_assert(kEach * 64 == kFew && kEach * kThreads == kMost, "four a thread");
 
