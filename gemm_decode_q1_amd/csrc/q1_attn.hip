@@ -588,10 +588,14 @@ int64_t up_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 }  // namespace
 
 // Few rows (up to 32 of them share a key/value head): items by tokens, all rows in
-// an item.  More: prefix items by rows, 64 a block (128 a block, two blocks a wave:
-// 62 against 45 us at 192 rows of D = 256 over 8201 tokens, where it leaves one
-// workgroup a CU, 41 against 38 us at 384 rows of D = 128 over 4000), suffix items
-// by tokens.
+// an item; more: prefix items by rows, 64 a block, suffix items by tokens.  Measured at
+// 32 rows, D = 128: over 65537 tokens by tokens 65 us, by rows 70 (8 heads, fp16, from
+// HBM), 25 and 35 (1 head); but over 8000 tokens that caches hold 20 and 16, and with
+// D = 256 and 30 rows 21 and 17.  Past 32, two blocks by tokens read the prefix twice:
+// 36 rows over 8000 tokens 21 us, by rows 17 (D = 256: 23 and 18); over 1000 tokens equal
+// (10.5), and at 64 rows 11 and 13.  (128 rows a block, two blocks a wave: 62 against
+// 45 us at 192 rows of D = 256 over 8201 tokens, where it leaves one workgroup a CU,
+// 41 against 38 us at 384 rows of D = 128 over 4000.)
 AttnPlan plan_prefix_attn(const q1_attn& a) {
   AttnPlan p = {};
   const int64_t group = a.Hq / a.Hkv, R = a.P > 0 ? a.B * group : group;
