@@ -61,6 +61,7 @@ class _Scratch(threading.local):
 
 
 _scratch = _Scratch()
+_KEEP = 64 << 20  # bytes that are kept; more is a call's own, whose time hides the allocator's
 _capturing = torch.cuda.is_current_stream_capturing
 
 
@@ -68,10 +69,11 @@ def _workspace(nbytes: int, index: int, stream: int) -> torch.Tensor:
     """Device workspace of these calls (no initial contents needed): one per
     (thread, device, stream), grown on demand.  A call is several launches that hand
     data on through it, and another thread's launches may come between them on the
-    same stream.  A call under graph capture gets one of its own, from the graph's
-    memory: a shared one would be freed as it grows, and be used by replays on other
-    streams."""
-    if _capturing():
+    same stream.  A large one (of a long prompt: 264 MB for 16384 tokens of 48 heads)
+    goes back to torch's allocator after the call.  A call under graph capture gets
+    one of its own, from the graph's memory: a shared one would be freed as it grows,
+    and be used by replays on other streams."""
+    if nbytes > _KEEP or _capturing():
         return _empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
     kept = _scratch.kept
     t = kept.get((index, stream))

@@ -130,6 +130,15 @@ def test_a_thread_has_a_workspace_of_its_own(monkeypatch):
     assert all(r() is None for r in made)
 
 
+def test_a_large_workspace_is_not_kept(monkeypatch):
+    monkeypatch.setattr(D, "_empty", lambda n, dtype, device: torch.empty(n, dtype=dtype))
+    monkeypatch.setattr(D, "_capturing", lambda: False)
+    D._workspace(4096, 0, 9)
+    large = weakref.ref(D._workspace(264 << 20, 0, 9))
+    gc.collect()
+    assert large() is None and D._scratch.kept.pop((0, 9)).numel() < 1 << 20
+
+
 def test_packed_calls_share_no_workspace_between_threads(monkeypatch):
     monkeypatch.setattr(B, "_stream", lambda device=None: ctypes.c_void_p(7))
     spaces, host, got = B._Workspaces(), torch.device("cpu"), []
