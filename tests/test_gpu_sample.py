@@ -257,3 +257,17 @@ def test_weightless_logits_beside_the_cut():
     row = torch.from_numpy(x).float().cuda()[None]
     assert R.sample(row[0].cpu().numpy(), 0.0, 1.0, k, float(p))[0] == 0
     check(row, [0.0], k=[k], p=[float(p)], what="weightless")
+
+
+@pytest.mark.parametrize("V,dt", [(100, "f32"), (139, "bf16"), (201, "f16"), (454, "f32")])
+def test_small_vocabularies(V, dt):
+    """Large batches of short rows, every fourth with all filters, with top-k, with top-p and with none."""
+    r = np.random.default_rng(V)
+    B = 145
+    x = logits_of(V + 5, B, V, dt)
+    f = lambda lo, hi: r.uniform(lo, hi, B).astype(np.float32)  # noqa: E731
+    row = np.arange(B) % 4
+    k = np.where(row <= 1, r.integers(1, 200, B), 0).tolist()
+    p = np.where(row % 2 == 0, f(0.7, 0.99), 1).astype(np.float32).tolist()
+    m = np.where(row == 0, f(0, 0.1), 0).astype(np.float32).tolist()
+    check(x, f(0, 1).tolist(), T=f(0.5, 1.3).tolist(), k=k, p=p, m=m, what="mixed")
