@@ -20,7 +20,7 @@
 //                 4(l/16)..+3 of both 16-token halves); values lie in LDS as rows
 //                 and come back transposed (ds_read_tr16).
 // Weights enter the second product as two 16-bit parts (high and remainder), so
-// that their rounding (2^-17) stays below the output's; their sum, the maximum
+// that their rounding (2^-17) stays below a 16-bit output's; their sum, the maximum
 // and the output are fp32.  A token that does not count (past the length, no such
 // page) has the score -infinity, whatever its key, and zeros for its values.
 //
@@ -29,7 +29,9 @@
 // of a plain read's 6.2, and 5 us for the join); 192 rows to a head of 256 (32
 // sequences over 8201 tokens, 77 MB), the products and softmax of a tile, one after the
 // other in each of two workgroups a CU (34 us, of which reading would be 12, and 7 us
-// for the join); a short prefix, the two launches (8 and 4 us).
+// for the join); a short prefix, the two launches (8 and 4 us).  Pages alone: 32
+// sequences of 2000 tokens (24 heads, 4 of keys, D = 128, bf16) 131 MB in 29 us, 8 of
+// 32000 524 MB in 106, one of 2000 4 MB in 9.4 (in a replayed graph).
 //
 // Loops have no branch around loads or products (a branch makes the compiler wait
 // for every load in flight where the paths join): loads past the end are dropped

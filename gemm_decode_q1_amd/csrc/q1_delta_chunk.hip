@@ -354,8 +354,9 @@ __global__ __launch_bounds__(256, 4) void q1_chunk_prep(const DeltaArgs a, Chunk
 // no other wave; the other half, W and half of the new state; the rest of it and its
 // parts.  Bound by this chain: 2.4 us a chunk (bf16, 128x128), of which the matrix
 // cores are busy 0.6 and the vector units 0.75; the output waves' work is dealt so
-// that none of the three waits for it (with the output made in the first part and
-// Q S0 in the second, 8192 tokens of 48 heads took 378 us instead of 362).  Three bf16
+// that the first two do not wait for it, and the third hardly (with the output made in
+// the first part and Q S0 in the second, 8192 tokens of 48 heads took 378 us instead of
+// 362; a product more in the third costs 2 %, in the first nothing).  Three bf16
 // parts keep the state in fp32.  Four waves with 16 columns and no division of labour
 // took 932 us for 16384 tokens when eight with 32 took 863.
 constexpr int kRunThreads = 512;

@@ -34,7 +34,8 @@
 // exponential, the exact quotient, the weight and its bin (31 and 24 us), which is why
 // elements that cannot matter are left out by one comparison before it; the draw is
 // one workgroup's chain of selects (16 us).  For one row all four are latency: 3 + 6 +
-// 2 + 9 us, near what four launches cost the caller (17 us).
+// 2 + 9 us, near what four launches cost the caller (17 us); in a replayed graph a row
+// takes 9 us greedy, 12 without a filter, 16 to 21 with top-k 50, 28 with top-p.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -55,8 +55,10 @@ typedef struct q1_delta {
 } q1_delta;
 
 /*
- * q1_delta_step -- T tokens (one, or a few drafted ones) of each of B sequences;
- * token t of sequence b is row b*T + t.  States are read and written once.
+ * q1_delta_step -- T tokens (one or a few) of each of B sequences; token t of
+ * sequence b is row b*T + t.  States are read and written once: they end after all
+ * T tokens, none between is kept.  A caller that may take drafted tokens back
+ * starts them from a copy of the state, in another slot.
  */
 q1_status q1_delta_step(const q1_delta* d, int64_t B, int64_t T, void* stream);
 
@@ -86,7 +88,8 @@ size_t q1_delta_prefill_workspace_bytes(const q1_delta* d, int64_t tokens, int64
  * page_table[b, t / page_size].  Lengths are clamped to [0, max_pages *
  * page_size]; a token whose page id is outside [0, pages) is left out.  A row
  * with no token at all gives zeros and lse = -infinity.  Rows past a length
- * are never used, whatever they hold.  Scores, softmax and sums are fp32.
+ * are never used, whatever they hold.  Scores, softmax and sums are fp32; the
+ * weights' products with the values take a weight as two 16-bit parts (2^-17).
  * A NaN or +infinite score of a token that counts makes its row's out and lse
  * NaN.  A NaN or infinite value of such a token makes its column of the row
  * NaN, or infinite where it is (weights enter the product in two parts, of which
