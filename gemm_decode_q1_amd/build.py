@@ -18,7 +18,9 @@ SOURCES = ([os.path.join(PKG, "csrc", "q1_api.cpp"), os.path.join(PKG, "csrc", "
             os.path.join(PKG, "csrc", "q1_gemv.hip"), os.path.join(PKG, "csrc", "q1_decode_api.cpp"),
             os.path.join(PKG, "csrc", "q1_delta.hip"),
             os.path.join(PKG, "csrc", "q1_delta_chunk.hip"), os.path.join(PKG, "csrc", "q1_attn.hip"),
-            os.path.join(PKG, "csrc", "q1_sample.hip")])
+            os.path.join(PKG, "csrc", "q1_sample.hip"), os.path.join(PKG, "csrc", "q1_memory_api.cpp"),
+            os.path.join(PKG, "csrc", "q1_kv.hip"), os.path.join(PKG, "csrc", "q1_kv_attn.hip"),
+            os.path.join(PKG, "csrc", "q1_conv.hip"), os.path.join(PKG, "csrc", "q1_scan.hip")])
 # Packed-FP32 instructions are disabled for all device code (see the design
 # notes): hipcc otherwise forms v_pk_*_f32 from plain float code.
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Xclang", "-target-feature", "-Xclang",

@@ -43,7 +43,9 @@ _lib_lock = threading.Lock()
 EXPORTS = ["q1_qmm", "q1_qmm_noalloc", "q1_qmm_workspace_bytes", "q1_dequantize", "q1_embed_rows", "q1_ffn", "q1_ffn_workspace_bytes",
            "q1_check_symmetric", "q1_pack_signs", "q1_stream_read", "q1_set_max_packed_rows", "q1_device_supported", "q1_last_error",
            "q1_version", "q1_delta_step", "q1_delta_prefill", "q1_delta_prefill_workspace_bytes", "q1_prefix_attn",
-           "q1_prefix_attn_workspace_bytes", "q1_sample", "q1_sample_workspace_bytes"]
+           "q1_prefix_attn_workspace_bytes", "q1_sample", "q1_sample_workspace_bytes",
+           "q1_kv_write", "q1_kv_read", "q1_kv_attn", "q1_kv_attn_workspace_bytes", "q1_conv_step", "q1_conv_prefill",
+           "q1_scan_step", "q1_scan_prefill", "q1_scan_prefill_workspace_bytes"]
 
 
 def load_library(path: str = LIB_PATH):
@@ -80,6 +82,15 @@ def load_library(path: str = LIB_PATH):
             "q1_prefix_attn_workspace_bytes": (sz, [vp]),
             "q1_sample": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
             "q1_sample_workspace_bytes": (sz, [i64, i64]),
+            "q1_kv_write": (i32, [vp, vp, vp, i32, i64, i64, i64, vp, vp]),
+            "q1_kv_read": (i32, [vp, vp, i64, vp, vp, i32, vp]),
+            "q1_kv_attn": (i32, [vp, vp, vp, sz, vp]),
+            "q1_kv_attn_workspace_bytes": (sz, [vp, vp]),
+            "q1_conv_step": (i32, [vp, i64, i64, vp]),
+            "q1_conv_prefill": (i32, [vp, i64, i64, vp, vp]),
+            "q1_scan_step": (i32, [vp, i64, i64, vp]),
+            "q1_scan_prefill": (i32, [vp, i64, i64, vp, vp, sz, vp]),
+            "q1_scan_prefill_workspace_bytes": (sz, [vp, i64, i64]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
