@@ -27,16 +27,11 @@ struct ConvArgs {
   q1_conv d;
   Ragged r;          // r.cu == nullptr: T rows a sequence
   int64_t per;       // tokens of a piece
+  Divider by;
   uint32_t n;        // lanes in all: pieces * C / 8
   uint32_t lanes;    // C / 8
   Divider per_row;   // by C / 8
 };
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) return f32_to_f16_bits(x) | f32_to_f16_bits(y) << 16;
-  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(kv_f32x2{x, y}, kv_bf16x2));
-}
 
 template <bool F16, int W>
 __global__ __launch_bounds__(kThreads) void q1_conv_kernel(const ConvArgs a) {
@@ -47,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void q1_conv_kernel(const ConvArgs a) {
   const uint32_t piece = divide(i, a.per_row), c0 = (i - piece * a.lanes) * 8;
   Piece p;
   if (a.r.cu != nullptr) {
-    p = find_piece(a.r, piece, a.per);
+    p = find_piece(a.r, piece, a.by, a.per);
     if (p.t0 >= p.t1) return;
   } else {
     p.seq = piece;
@@ -129,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void q1_conv_kernel(const ConvArgs a) {
           acc = __builtin_fmaf(w[W - 1][c], elem16<F16>(row[u][e], h), acc);
           s[h] = d.silu ? silu_fast(acc) : acc;
         }
-        o[e] = pack2<F16>(s[0], s[1]);
+        o[e] = pack16<F16>(s[0], s[1]);
       }
       if (t + u < p.t1) *reinterpret_cast<u32x4*>(out + (t + u) * d.C) = o;
 #pragma unroll
@@ -144,6 +139,7 @@ __global__ __launch_bounds__(kThreads) void q1_conv_kernel(const ConvArgs a) {
 hipError_t launch(ConvArgs a, int64_t pieces, hipStream_t s) {
   a.lanes = (uint32_t)(a.d.C / 8);
   a.per_row = divider(a.lanes);
+  a.by = divider((uint32_t)a.per);
   a.n = (uint32_t)(pieces * a.lanes);
   const dim3 grid((a.n + kThreads - 1) / kThreads), block(kThreads);
 #define Q1_CV(H, N) hipLaunchKernelGGL((q1_conv_kernel<H, N>), grid, block, 0, s, a)

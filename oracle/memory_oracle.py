@@ -9,8 +9,9 @@ Error bounds beside the values, u = 2^-24 being half a step of fp32:
   exponential is off by (2 |s|) u, so E by (2 |s| + 2) u, the quotient by that times
   E / (1 + E) <= 1, and sum, reciprocal and product by 4 u: |silu(s)| (2 |s| + 6) u.  Its
   slope is below 1.1.  (Where E overflows the value is 0, off by less than 1e-36.)
-* ``scan``: delta is softplus(s), s off by |s| u: by sigmoid(s) |s| u + 16 u delta (an
-  exponential within 3 u, eight multiply-adds, a reciprocal and four roundings).
+* ``scan``: delta is softplus(s), s off by |s| u and, in the exponential, by a quarter of that more:
+  by sigmoid(s) 1.25 |s| u + 16 u delta (an exponential within 3 u, some multiply-adds of falling
+  weight, a reciprocal and four roundings).
   a = exp(delta A) is off by a factor within |A| e_delta + |delta A| (3 + n) u + 2 u: A log2(e)
   and the product are rounded, and over a piece of n tokens the deltas are summed.
   A state's error obeys e' = a e + |a h| (that + 2 u) + |delta x B| (e_delta / delta + 3 u);
@@ -101,7 +102,7 @@ def scan(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, softplus=True, pie
     s = dt if dt_bias is None else dt + np.asarray(dt_bias, np.float64)
     if softplus:
         delta = np.maximum(s, 0) + np.log1p(np.exp(-np.abs(s)))
-        ed = np.abs(s) * U / (1 + np.exp(np.clip(-s, -700, 700))) + 16 * U * delta
+        ed = 1.25 * np.abs(s) * U / (1 + np.exp(np.clip(-s, -700, 700))) + 16 * U * delta
     else:
         delta, ed = s, np.abs(s) * U
     out, bound = np.zeros_like(x), np.zeros_like(x)

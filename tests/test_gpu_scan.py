@@ -104,7 +104,7 @@ def test_prefill(lens, Di, N, dt, dt32, full, out_dt):
 
 
 def test_many_whole_sequences():
-    """More sequences than fill the chip: none is cut into pieces."""
+    """More sequences than fill the chip, of a few tokens each: none is cut into pieces."""
     nseq, Di = 520, 512
     lens = [(7 * i) % 5 for i in range(nseq)]
     ops = draw(5, (sum(lens),), Di, 16, "bf16", False, nseq)
