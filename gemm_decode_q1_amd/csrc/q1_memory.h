@@ -20,7 +20,7 @@ hipError_t launch_kv_write(const q1_kv& c, const void* k, const void* v, bool f1
 hipError_t launch_kv_read(const q1_kv& c, const int32_t* slots, int64_t rows, void* k, void* v, int32_t out_dtype,
                           hipStream_t s);
 
-// Division of whole numbers below 2^31 by d >= 1: x / d = (x * mul) >> shift, shift >= 32.
+// Division of whole numbers below 2^31 by d >= 1: x / d = (2 x * mul) >> 32 >> shift.
 struct Divider {
   uint32_t mul;
   int32_t shift;
@@ -29,18 +29,21 @@ inline Divider divider(uint32_t d) {
   // 2^(31 + l) / d rounded up, l = ceil(log2 d): off by less than 2^l / d of a unit per 2^31
   int l = 0;
   while (((uint64_t)1 << l) < d) ++l;
-  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l};
 }
 
 // How a call is cut into work items (see q1_kv_attn.hip).
 struct KvPlan {
-  int32_t nm;             // blocks of 16 query rows of a wave
-  int32_t row_blocks;     // items along the rows of a key/value head
-  int32_t splits;         // items along the tokens
-  int64_t tokens;         // tokens of an item
-  int64_t wgs;
-  Divider page;           // by page_size
-  size_t ml_off, ws_bytes;
+  int32_t nm;              // blocks of 16 query rows of a wave
+  uint32_t heads_each, R;  // query heads and rows of a key/value head
+  uint32_t rows;           // rows of an item
+  uint32_t row_blocks;     // items along the rows
+  uint32_t entries;        // sequences times row_blocks
+  int32_t cut;             // 1: workgroups have equal shares of all tokens, else an item each
+  uint32_t wgs;
+  int32_t too_large;       // more units of work than are counted in 31 bits
+  Divider page, heads, queries, group, blocks, kv_heads, sequences;  // by page_size, Hq, T, heads_each, row_blocks, Hkv, B
+  size_t o_off, ml_off, ws_bytes;
 };
 
 KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a);

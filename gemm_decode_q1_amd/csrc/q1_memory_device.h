@@ -12,7 +12,7 @@
 namespace q1 {
 
 // x / d for x below 2^31.
-__device__ __forceinline__ uint32_t divide(uint32_t x, Divider d) { return (uint32_t)(((uint64_t)x * d.mul) >> d.shift); }
+__device__ __forceinline__ uint32_t divide(uint32_t x, Divider d) { return __umulhi(x << 1, d.mul) >> d.shift; }
 
 // The low or high element of a pair.
 template <bool F16>
