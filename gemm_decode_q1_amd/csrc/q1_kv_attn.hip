@@ -1,27 +1,32 @@
 // Attention over keys and values held in 4 or 8 bits (q1_memory.h).
 //
-// Two launches: q1_kv_main computes, per work item, the running maximum m, sum l and
-// unnormalised output o of a block of query rows (the T * Hq/Hkv rows that share a
-// key/value head of a sequence) over some tokens; q1_kv_join adds the items of a
-// row.  Where the tokens are not split, the item writes the row itself.
+// An item is a block of the T * Hq/Hkv query rows that share a key/value head of a
+// sequence, and some of its tokens: running maximum m, sum l and unnormalised output o of
+// each row.  The work, in units of 128 tokens, is cut evenly over as many workgroups as run
+// at a time, and q1_kv_join adds the parts of a row; or each workgroup has a whole item and
+// writes its rows itself (plan_kv_attn has the rule).  Codes go to bf16, which is exact, so
+// the products are the ones of 16-bit attention (see q1_attn.hip for their layouts):
+//   S^T = K Q^T     O^T = V^T P^T, values transposed on their way out of LDS.
+// fp16 queries enter as two bf16 parts (11 bits of significand are 8 and 3), weights as
+// two (2^-17: one would add an error of the size of the output's rounding).  The running
+// maximum stays where it is until a weight could pass 2^8, so o is rescaled rarely: a
+// power of two more in a weight costs no bits.
 //
-// In an item each of the 4 waves takes every fourth tile of 32 tokens, by itself, and
-// the waves are joined in LDS.  Codes go to bf16 in registers, which is exact, so the
-// products are the ones of 16-bit attention (see q1_attn.hip for their layouts):
-//   S^T = K Q^T   a lane has a quarter of the elements of one token in a row of bytes
-//                 (for D = 128 one block with its scale), 8 of them a product: the
-//                 order of the elements is free as long as the queries have it too.
-//   O^T = V^T P^T values are loaded as keys are, go to LDS as bf16 rows and come back
-//                 transposed.
-// fp16 queries enter as two bf16 parts (11 bits of significand are 8 and 3), weights
-// as two (2^-17).
+// By tokens (few rows): 4 waves, each with a quarter of the tokens and 16 or 32 rows,
+// joined in LDS; keys go from memory to the matrix core through registers alone.  Bound by
+// the bytes of the pages and by the vector instructions (98 a wave for 16 rows x 32 tokens).
+// By rows (prompts): 8 waves, each with 32 rows (16 of D 256); a tile of 64 tokens is
+// converted once for all of them.  Bound by the vector instructions of the softmax: the
+// matrix cores are busy for 42 % of the time.
+//
+// Measured (us): 32 sequences of 8201 tokens, D 256, 4 bits 50 (the pages at the rate of a copy:
+// 36); 8 of 65537, 3 queries each, D 128, 76 (70); 4 of 519 9.9; 2 x 1000 queries of 5003
+// tokens, 24 heads of D 128, 8 bits 220; 8000 queries of 8000 tokens 600 (1.3 PFLOP/s of
+// products with both parts of the weights).
 //
 // A token that a query does not see has the score -infinity, whatever its key.  Its
-// weight 0 would still make a NaN of a NaN value, so a tile with a NaN block of values
-// (a branch that hardly ever is taken) has zeros there, and the block's columns are
-// made NaN for the queries that see the token.
-//
-// Bound by the bytes of the pages where rows are few.
+// weight 0 would still make a NaN of a NaN value, so NaN blocks of values enter as
+// zeros, and their columns are made NaN at the end for the queries that see the token.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -84,6 +89,7 @@ struct Item {
 
 // The units before every entry, by the whole workgroup: returns all, and in *entry and
 // *inside the place of unit `start` (inside: units of that entry before it).
+template <int WAVES>
 __device__ __forceinline__ uint32_t scan_units(const KvArgs& g, uint32_t wgs, uint32_t* lds, Share* share, uint32_t* entry,
                                                uint32_t* inside) {
   if (g.p.entries <= 64) {  // (each wave for itself)
@@ -106,7 +112,7 @@ __device__ __forceinline__ uint32_t scan_units(const KvArgs& g, uint32_t wgs, ui
     }
     return total;
   }
-  const uint32_t tid = threadIdx.x, each = (g.p.entries + 64 * kWaves - 1) / (64 * kWaves), heads = (uint32_t)g.c.Hkv;
+  const uint32_t tid = threadIdx.x, each = (g.p.entries + 64 * WAVES - 1) / (64 * WAVES), heads = (uint32_t)g.c.Hkv;
   const uint32_t e0 = tid * each, e1 = e0 + each < g.p.entries ? e0 + each : g.p.entries;
   uint32_t sum = 0;
   for (uint32_t e = e0; e < e1; ++e) sum += units_of(g, e) * heads;
@@ -120,7 +126,7 @@ __device__ __forceinline__ uint32_t scan_units(const KvArgs& g, uint32_t wgs, ui
   __syncthreads();
   uint32_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     upto += w < (int)(tid >> 6) ? lds[w] : 0;
     total += lds[w];
   }
@@ -133,16 +139,16 @@ __device__ __forceinline__ uint32_t scan_units(const KvArgs& g, uint32_t wgs, ui
       const uint32_t u = units_of(g, e) * heads;
       if (blockIdx.x == 0) g.before[e] = at;
       if (mine && start >= at && start < at + u) {
-        lds[kWaves] = e;
-        lds[kWaves + 1] = start - at;
+        lds[WAVES] = e;
+        lds[WAVES + 1] = start - at;
       }
       at += u;
     }
-    if (blockIdx.x == 0 && tid == 64 * kWaves - 1) g.before[g.p.entries] = total;
+    if (blockIdx.x == 0 && tid == 64 * WAVES - 1) g.before[g.p.entries] = total;
   }
   __syncthreads();
-  *entry = __builtin_amdgcn_readfirstlane(lds[kWaves]);
-  *inside = __builtin_amdgcn_readfirstlane(lds[kWaves + 1]);
+  *entry = __builtin_amdgcn_readfirstlane(lds[WAVES]);
+  *inside = __builtin_amdgcn_readfirstlane(lds[WAVES + 1]);
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(total);
 }
@@ -164,7 +170,7 @@ __device__ __forceinline__ Item whole_item(const KvArgs& g, uint32_t i) {
 }
 
 // Calls f(item) for each of this workgroup's items.
-template <typename F>
+template <int WAVES, typename F>
 __device__ __forceinline__ void each_item(const KvArgs& g, uint32_t* lds, F f) {
   if (!g.p.cut) {
     f(whole_item(g, blockIdx.x));
@@ -172,7 +178,7 @@ __device__ __forceinline__ void each_item(const KvArgs& g, uint32_t* lds, F f) {
   }
   Share share(0, 1);
   uint32_t entry, inside;
-  const uint32_t total = scan_units(g, gridDim.x, lds, &share, &entry, &inside);
+  const uint32_t total = scan_units<WAVES>(g, gridDim.x, lds, &share, &entry, &inside);
   const uint32_t first = share.first(blockIdx.x), end = __builtin_amdgcn_readfirstlane(share.first(blockIdx.x + 1));
   if (first >= total) return;
   uint32_t unit = __builtin_amdgcn_readfirstlane(first);
@@ -287,18 +293,23 @@ struct Tile {
   static __device__ __forceinline__ uint32_t byte(uint32_t s, int j) { return NB == 2 ? s >> (8 * j) & 255u : s; }
 };
 
+// Products of this lane's 8 tokens: those of `vis` (by token of the tile) count.
+__device__ __forceinline__ void hide(f32x4* S, uint32_t vis, int grp) {
+  const uint32_t mine = (vis >> (4 * grp) & 15u) | (vis >> (16 + 4 * grp) & 15u) << 4;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) S[j >> 2][j & 3] = (mine >> j) & 1u ? S[j >> 2][j & 3] : -INFINITY;
+}
+
 // The softmax of one tile for a block of 16 queries: products of this lane's 8 tokens in,
 // weights out as two operands; m, l and the output so far are brought to a new maximum
-// where a product is so far above the old one that a weight could pass 2^8.  With ALL,
-// every token counts, else those of `mine`.
-template <bool ALL, int DT>
-__device__ __forceinline__ void soften(const f32x4* S, uint32_t mine, float sc, float& m, float& l, f32x4* O, int stride,
-                                       u32x4& hi, u32x4& lo) {
+// where a product is so far above the old one that a weight could pass 2^8.  (One call for
+// all tiles: where it was one of two, the output was copied at each, a quarter of the time.)
+template <int DT>
+__device__ __forceinline__ void soften(const f32x4* S, float sc, float& m, float& l, f32x4* O, int stride, u32x4& hi, u32x4& lo) {
   float s[8], top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     s[j] = S[j >> 2][j & 3];
-    if constexpr (!ALL) s[j] = (mine >> j) & 1u ? s[j] : -INFINITY;
     top = fmaxf(top, s[j]);
   }
   if (__any((top - m) * sc > 8.0f)) {  // (the first tile: m is -infinity)
@@ -408,9 +419,11 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
 
   f32x4 O[DT][NM];
   float m[NM], l[NM];
-  int32_t lim[NM];  // tokens that this lane's query sees
+  int32_t lim[NM];    // tokens that this lane's query sees
+  uint32_t lost[NM];  // blocks of 32 columns of it that are NaN
 #pragma unroll
   for (int x = 0; x < NM; ++x) {
+    lost[x] = 0;
     m[x] = -INFINITY;
     l[x] = 0.f;
     const uint32_t r = it.row0 + 16 * x + col;
@@ -492,18 +505,16 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
     ids_of(id, place);
     u32x4 hi[NM], lo[NM];
     uint32_t vis[NM];
-    if (plain && t + kTile <= least) {
-#pragma unroll
-      for (int q = 0; q < NM; ++q) soften<true, DT>(S[q], 0, sc, m[q], l[q], &O[0][q], NM, hi[q], lo[q]);
-    } else {
+    if (!plain || t + kTile > least) {
 #pragma unroll
       for (int q = 0; q < NM; ++q) {
         const int32_t d = lim[q] - t;
         vis[q] = in & (d >= 32 ? ~0u : d <= 0 ? 0u : ~0u >> (32 - d));
-        const uint32_t mine = (vis[q] >> (4 * grp) & 15u) | (vis[q] >> (16 + 4 * grp) & 15u) << 4;
-        soften<false, DT>(S[q], mine, sc, m[q], l[q], &O[0][q], NM, hi[q], lo[q]);
+        hide(S[q], vis[q], grp);
       }
     }
+#pragma unroll
+    for (int q = 0; q < NM; ++q) soften<DT>(S[q], sc, m[q], l[q], &O[0][q], NM, hi[q], lo[q]);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -515,12 +526,11 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
     }
     if (!plain) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const int blk = d / 2, sh = 16 * (D == 64 ? 2 * blk : blk / NB), j = blk % NB;
+      for (int blk = 0; blk < D / kKvBlock; ++blk) {
+        const int sh = 16 * (D == 64 ? 2 * blk : blk / NB), j = blk % NB;
         const uint32_t bad = (uint32_t)(nan[0][j] >> sh & 0xffffu) | (uint32_t)(nan[1][j] >> sh & 0xffffu) << 16;
 #pragma unroll
-        for (int q = 0; q < NM; ++q)
-          if (vis[q] & bad) O[d][q] = f32x4{NAN, NAN, NAN, NAN};
+        for (int q = 0; q < NM; ++q) lost[q] |= vis[q] & bad ? 1u << blk : 0u;
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -553,7 +563,8 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
     const float sum = sum_groups(l[q]);
     if (grp == 0) sml[r] = float2{m[q] == -INFINITY ? m[q] : m[q] * sc, sum};
 #pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = O[d][q];
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = lost[q] >> (d / 2) & 1u ? f32x4{NAN, NAN, NAN, NAN} : O[d][q];
   }
   __syncthreads();
   for (int x = threadIdx.x; x < 16 * NM * (D / 4); x += 64 * kWaves) {
@@ -576,115 +587,387 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
   __syncthreads();
 }
 
+// What one thread stages of a tile for the whole workgroup: an eighth of one token.
+constexpr int kRowWaves = 8, kRowTile = 64, kParts = 64 * kRowWaves / kRowTile;
+
+template <int BITS, int D>
+struct Staged {
+  static constexpr int EP = D / kParts, W = EP * BITS / 32;  // elements and dwords of a part
+  static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 32, kFlags = kRowTile * (KROW + VROW);
+  static constexpr int kBytes = kFlags + kRowTile * kParts;
+  uint32_t k[W], v[W], ks, vs;
+  bool ok;  // the token counts
+
+  static __device__ __forceinline__ void take(const unsigned char* p, uint32_t* to) {
+    if constexpr (W == 1) {
+      to[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (W == 2) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      to[0] = w.x, to[1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const u32x4 w = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[4 * i + j] = w[j];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void load(const q1_kv& c, uint64_t at) {
+    take(static_cast<const unsigned char*>(c.k) + at, k);
+    take(static_cast<const unsigned char*>(c.v) + at, v);
+    ks = static_cast<const unsigned char*>(c.k_scales)[at / (4 * BITS)];
+    vs = static_cast<const unsigned char*>(c.v_scales)[at / (4 * BITS)];
+  }
+
+  // Pieces of 16 bytes that lie x apart, in each other's places.
+  static __device__ __forceinline__ void swap(uint32_t* w, int x, bool yes) {
+    constexpr int N = BITS / 4;  // dwords of codes a piece
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (!(i / N & x)) {
+        const uint32_t one = w[i], two = w[i + x * N];
+        w[i] = yes ? two : one;
+        w[i + x * N] = yes ? one : two;
+      }
+  }
+
+  // To a buffer: keys, values (those of tokens that do not count, and NaN blocks, as zeros; in
+  // every other four rows with neighbouring 16 bytes in each other's places, see item_by_tokens)
+  // and a byte for each part: 1 where the token counts, and 2 where its values are a NaN block.
+  // The parts of a row write their pieces in an order in which eight of them meet all banks.
+  __device__ __forceinline__ void put(unsigned char* buf, int token, int part) {
+    constexpr int NP = EP / 8;  // pieces of a part
+    const bool bad = vs == 255u, use = ok && !bad;
+    const float kscale = kv_scale(ks), vscale = use ? __uint_as_float(vs << 23) : 1.0f;
+    unsigned char* const kr = buf + token * KROW;
+    unsigned char* const vr = buf + kRowTile * KROW + token * VROW;
+    const int turn = part * NP / 8;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = use ? v[i] : 0u;
+#pragma unroll
+    for (int x = 1; x < NP; x *= 2) {
+      swap(k, x, turn & x);
+      swap(v, x, turn & x);
+    }
+#pragma unroll
+    for (int s = 0; s < NP; ++s) {
+      const int piece = part * NP + (s ^ turn);
+      *reinterpret_cast<u32x4*>(kr + 16 * piece) = kv_bf16<BITS>(&k[s * (BITS / 4)], kscale);
+      *reinterpret_cast<u32x4*>(vr + 16 * (piece ^ (token >> 2 & 1))) = kv_bf16<BITS>(&v[s * (BITS / 4)], vscale);
+    }
+    buf[kFlags + token * kParts + part] = (ok ? 1 : 0) | (ok && bad ? 2 : 0);
+  }
+};
+
+// An item by rows: each of 8 waves has 16 NM rows, the tiles of 64 tokens are converted once for
+// all waves and lie in LDS, two in turn.  Against 16 rows a wave and two workgroups a compute
+// unit, 32 rows and one workgroup halve what is converted, and what is read from LDS
+// for each product.  2 x 1000 queries of 5003 tokens (D 128, 4 bits): 197 | 192 us, fp16 137 | 130.
+template <bool F16, int BITS, int D, int NM>
+__device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, unsigned char* lds) {
+  constexpr int QP = F16 ? 2 : 1, KS = D / 32, DT = D / 16;
+  using T = Staged<BITS, D>;
+  constexpr int KROW = T::KROW, VROW = T::VROW;
+  const q1_kv& c = g.c;
+  const q1_kv_query& a = g.a;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int token = tid / kParts, part = tid % kParts;
+  const uint32_t first = it.row0 + 16 * NM * wave, last = first + 16 * NM < g.p.R ? first + 16 * NM : g.p.R;  // of the wave
+  const int32_t end = (int32_t)it.t1;
+
+  u32x4 Q[NM][KS][QP];
+  f32x4 O[NM][DT];
+  float m[NM], l[NM];
+  int32_t lim[NM];    // tokens that this lane's query sees
+  uint32_t lost[NM];  // blocks of 32 columns of this lane's query that are NaN
+#pragma unroll
+  for (int y = 0; y < NM; ++y) {
+    const uint32_t r = first + 16 * y + col;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) load_q<F16, QP>(g, it, r, 32 * s + 8 * grp, Q[y][s]);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) O[y][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    m[y] = -INFINITY;
+    l[y] = 0.f;
+    lim[y] = (int32_t)seen_by(g, it.n, r < g.p.R ? r : g.p.R - 1);
+    lost[y] = 0;
+  }
+  // all of the wave's queries see `least` tokens, none more than `most`
+  const int32_t least = (int32_t)seen_by(g, it.n, first < g.p.R ? first : g.p.R - 1);
+  const int32_t most = first < g.p.R ? (int32_t)seen_by(g, it.n, last - 1) : 0;
+  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e;
+
+  // This thread's token of the tile whose page id is fetched next, as in item_by_tokens.
+  const uint32_t ps = (uint32_t)c.page_size, more_pg = kRowTile / ps, more_off = kRowTile - more_pg * ps;
+  const uint32_t last_pg = it.t1 > 0 ? divide(it.t1 - 1, g.p.page) : 0;
+  uint32_t pg = divide(it.t0 + token, g.p.page), off = it.t0 + token - pg * ps;
+  int32_t id = 0;
+  uint32_t place = 0;
+  auto id_of = [&] {
+    id = (a.page_table + it.b * a.max_pages)[pg < last_pg ? pg : last_pg];
+    place = off;
+    pg += more_pg;
+    off += more_off;
+    const bool over = off >= ps;
+    pg += over ? 1 : 0;
+    off -= over ? ps : 0;
+  };
+  const uint32_t page_bytes = (uint32_t)(c.Hkv * c.page_size * (D * BITS / 8));
+  const uint32_t lane_bytes = it.hk * (uint32_t)(c.page_size * (D * BITS / 8)) + part * (T::EP * BITS / 8);
+  T x;
+  auto fetch = [&](int32_t t) {
+    const bool in = (uint32_t)id < (uint32_t)c.pages;
+    x.ok = in && t + token < end;
+    x.load(c, (uint64_t)(in ? (uint32_t)id : 0u) * page_bytes + (place * (uint32_t)(D * BITS / 8) + lane_bytes));
+  };
+
+  const int32_t t0 = (int32_t)it.t0;
+  if (t0 < end) {
+    id_of();
+    fetch(t0);
+    id_of();
+  }
+  int turn = 0;
+  for (int32_t t = t0; t < end; t += kRowTile, turn ^= 1) {
+    unsigned char* const buf = lds + turn * T::kBytes;
+    x.put(buf, token, part);
+    __syncthreads();
+    fetch(t + kRowTile);
+    id_of();
+    const uint2 flags = reinterpret_cast<const uint2*>(buf + T::kFlags)[lane];  // of token t + lane
+    const bool plain = __ballot(flags.x == 0x01010101u && flags.y == 0x01010101u) == ~0ull;
+#pragma unroll
+    for (int sub = 0; sub < kRowTile / kTile; ++sub) {
+      const int32_t ts = t + kTile * sub;
+      if (ts >= most) break;
+      const unsigned char* const kb = buf + (kTile * sub + col) * KROW + 16 * grp;
+      const unsigned char* const vb = buf + kRowTile * KROW + (kTile * sub + 4 * grp + col / 4) * VROW +
+                                      ((16 * (col >> 1 & 1)) ^ (16 * (grp & 1))) + 8 * (col & 1);
+      f32x4 S[NM][2];
+#pragma unroll
+      for (int y = 0; y < NM; ++y) S[y][0] = S[y][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 K = *reinterpret_cast<const u32x4*>(kb + 16 * h * KROW + 64 * s);
+#pragma unroll
+          for (int y = 0; y < NM; ++y)
+#pragma unroll
+            for (int q = 0; q < QP; ++q) S[y][h] = mma<false>(K, Q[y][s][q], S[y][h]);
+        }
+      u32x4 hi[NM], lo[NM];
+      uint32_t vis[NM];
+#pragma unroll
+      for (int y = 0; y < NM; ++y) vis[y] = ~0u;
+      if (!plain || ts + kTile > least) {
+        const uint32_t count = (uint32_t)(__ballot(flags.x & 1u) >> (kTile * sub));
+#pragma unroll
+        for (int y = 0; y < NM; ++y) {
+          const int32_t d = lim[y] - ts;
+          vis[y] = count & (d >= 32 ? ~0u : d <= 0 ? 0u : ~0u >> (32 - d));
+          hide(S[y], vis[y], grp);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < NM; ++y) soften<DT>(S[y], sc, m[y], l[y], O[y], 1, hi[y], lo[y]);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const u32x4 v = transposed(vb + 32 * d, 16 * VROW);
+#pragma unroll
+        for (int y = 0; y < NM; ++y) {
+          O[y][d] = mma<false>(v, hi[y], O[y][d]);
+          O[y][d] = mma<false>(v, lo[y], O[y][d]);
+        }
+      }
+      if (!plain) {
+#pragma unroll
+        for (int blk = 0; blk < D / kKvBlock; ++blk) {
+          const int p = blk * kKvBlock / T::EP;  // its (first) part
+          const uint32_t bad = (uint32_t)(__ballot((p < 4 ? flags.x : flags.y) >> (8 * (p % 4) + 1) & 1u) >> (kTile * sub));
+#pragma unroll
+          for (int y = 0; y < NM; ++y) lost[y] |= vis[y] & bad ? 1u << blk : 0u;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < NM; ++y) {
+    const uint32_t r = first + 16 * y + col;
+    const float sum = sum_groups(l[y]), top = m[y] == -INFINITY ? m[y] : m[y] * sc;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      if (r < g.p.R) put_row(g, it, r, 16 * d + 4 * grp, lost[y] >> (d / 2) & 1u ? f32x4{NAN, NAN, NAN, NAN} : O[y][d], top, sum);
+  }
+  __syncthreads();
+}
+
+template <bool F16, int BITS, int D, int NM>
+__global__ __launch_bounds__(64 * kRowWaves, 2) void q1_kv_rows(const KvArgs g) {
+  extern __shared__ unsigned char lds[];
+  each_item<kRowWaves>(g, reinterpret_cast<uint32_t*>(lds), [&](const Item& it) { item_by_rows<F16, BITS, D, NM>(g, it, lds); });
+}
+
 template <bool F16, int BITS, int D, int NM>
 __global__ __launch_bounds__(64 * kWaves, 2) void q1_kv_tokens(const KvArgs g) {
   extern __shared__ unsigned char lds[];
-  each_item(g, reinterpret_cast<uint32_t*>(lds), [&](const Item& it) { item_by_tokens<F16, BITS, D, NM>(g, it, lds); });
+  each_item<kWaves>(g, reinterpret_cast<uint32_t*>(lds), [&](const Item& it) { item_by_tokens<F16, BITS, D, NM>(g, it, lds); });
 }
 
-// The rows whose tokens several workgroups had, and those that see none: a row has R of a
-// workgroup's 4 waves, of which each sums every R-th part.
-template <int D, int R>
-__global__ __launch_bounds__(64 * kWaves) void q1_kv_join(const KvArgs g) {
-  constexpr int E = D / 64, U = 8;  // elements a lane, parts in flight
-  typedef float vec __attribute__((ext_vector_type(E)));
-  __shared__ vec so[kWaves][64];
-  const q1_kv_query& a = g.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t rows = (uint32_t)(a.B * a.T * a.Hq), row = blockIdx.x * (kWaves / R) + wave / R;
-  if (row >= rows) return;
-  const uint32_t bt = divide(row, g.p.heads), h = row - bt * (uint32_t)a.Hq, b = divide(bt, g.p.queries);
-  const uint32_t t = bt - b * (uint32_t)a.T, hk = divide(h, g.p.group);
-  const uint32_t r = t * g.p.heads_each + (h - hk * g.p.heads_each), rb = r / g.p.rows, entry = b * g.p.row_blocks + rb;
-  const uint32_t units = __builtin_amdgcn_readfirstlane(units_of(g, entry));
-  uint32_t w0 = 0, parts = 0, second = 0;
-  if (units > 0) {
+// Where the parts of an item's rows are: of workgroups w0 .. w0 + count - 1, each of which had it
+// as its first item, but for one that began with another.  One alone has written the rows.
+struct Parts {
+  uint32_t w0, count, second, units;
+  __device__ __forceinline__ Parts(const KvArgs& g, uint32_t entry, uint32_t hk) : w0(0), count(0), second(0) {
+    units = __builtin_amdgcn_readfirstlane(units_of(g, entry));
+    if (units == 0) return;
     const Share share(__builtin_amdgcn_readfirstlane(g.before[g.p.entries]), g.p.wgs);
     const uint32_t first = __builtin_amdgcn_readfirstlane(g.before[entry]) + hk * units;
     w0 = share.owner(first);
-    parts = share.owner(first + units - 1) - w0 + 1;
-    if (parts == 1) return;  // whole: its workgroup wrote the row
+    count = share.owner(first + units - 1) - w0 + 1;
     second = share.first(w0) != first ? 1 : 0;
   }
-  // part s, of workgroup w0 + s: its first item, but for one that began with another entry or head
-  auto at = [&](uint32_t s) { return (int64_t)(2 * (w0 + s) + (s == 0 ? second : 0)) * g.p.rows + (r - rb * g.p.rows); };
-  vec o = 0.f;
-  float top = -INFINITY, sum = 0.f;
-  for (uint32_t c0 = 0; c0 < parts; c0 += 64) {  // 64 parts: their factors, one a lane, then every R-th of them
-    const float2 ml = c0 + lane < parts ? g.part_ml[at(c0 + lane)] : float2{-INFINITY, 0.f};
-    float now = fmaxf(top, ml.x);
+  // Row `row` of the item in part s.
+  __device__ __forceinline__ int64_t at(const KvArgs& g, uint32_t s, uint32_t row) const {
+    return (int64_t)(2 * (w0 + s) + (s == 0 ? second : 0)) * g.p.rows + row;
+  }
+};
+
+// The rows whose tokens several workgroups had, and those that see none.  A wave has J rows of
+// an item, and R waves of a workgroup the same ones, of which each sums every R-th part.
+template <int D, int R, int J>
+__global__ __launch_bounds__(64 * kWaves) void q1_kv_join(const KvArgs g) {
+  constexpr int E = D / 64, U = 8 / J;  // elements a lane, parts in flight
+  typedef float vec __attribute__((ext_vector_type(E)));
+  __shared__ vec so[kWaves][J][64];
+  const q1_kv_query& a = g.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t i = blockIdx.x * (kWaves / R) + wave / R;  // of groups of J rows: of an item, then head, entry
+  const uint32_t item = divide(i, g.p.groups), row0 = (i - item * g.p.groups_each) * J;
+  const uint32_t entry = divide(item, g.p.kv_heads), hk = item - entry * (uint32_t)g.c.Hkv;
+  if (entry >= g.p.entries) return;
+  const uint32_t b = divide(entry, g.p.blocks), first = (entry - b * g.p.row_blocks) * g.p.rows + row0;
+  if (first >= g.p.R) return;
+  const Parts parts(g, entry, hk);
+  if (parts.count == 1) return;
+  vec o[J];
+  float top[J], sum[J];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) now = fmaxf(now, __shfl_xor(now, off));
-    const float base = now == -INFINITY ? 0.f : now, keep = __builtin_amdgcn_exp2f(top - base);
-    const float f = __builtin_amdgcn_exp2f(ml.x - base);
-    const uint32_t left = parts - c0 < 64 ? parts - c0 : 64;
-    o = keep * o;
-    sum = keep * sum + f * ml.y;  // (of this lane's parts)
+  for (int j = 0; j < J; ++j) {
+    o[j] = 0.f;
+    top[j] = -INFINITY;
+    sum[j] = 0.f;
+  }
+  for (uint32_t c0 = 0; c0 < parts.count; c0 += 64) {  // 64 parts: their factors, one a lane, then every R-th of them
+    const uint32_t left = parts.count - c0 < 64 ? parts.count - c0 : 64;
+    float f[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float2 ml = c0 + lane < parts.count ? g.part_ml[parts.at(g, c0 + lane, row0 + j)] : float2{-INFINITY, 0.f};
+      float now = fmaxf(top[j], ml.x);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) now = fmaxf(now, __shfl_xor(now, off));
+      const float base = now == -INFINITY ? 0.f : now, keep = __builtin_amdgcn_exp2f(top[j] - base);
+      f[j] = __builtin_amdgcn_exp2f(ml.x - base);
+      o[j] = keep * o[j];
+      sum[j] = keep * sum[j] + f[j] * ml.y;  // (of this lane's parts)
+      top[j] = now;
+    }
     for (uint32_t s0 = wave % R; s0 < left; s0 += U * R) {
-      vec x[U];
+      vec x[U][J];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint32_t s = s0 + u * R < left ? s0 + u * R : left - 1;
-        x[u] = reinterpret_cast<const vec*>(g.part_o + at(c0 + s) * D)[lane];
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[u][j] = reinterpret_cast<const vec*>(g.part_o + parts.at(g, c0 + s, row0 + j) * D)[lane];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint32_t s = s0 + u * R;
-        const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s & 63));
-        o = s < left ? o + fs * x[u] : o;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[j]), s & 63));
+          o[j] = s < left ? o[j] + fs * x[u][j] : o[j];
+        }
       }
     }
-    top = now;
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   if constexpr (R > 1) {  // (every wave has the same top and sum)
-    so[wave][lane] = o;
+#pragma unroll
+    for (int j = 0; j < J; ++j) so[wave][j][lane] = o[j];
     __syncthreads();
     if (wave % R != 0) return;
 #pragma unroll
-    for (int w = 1; w < R; ++w) o = o + so[wave + w][lane];
-  }
-  const bool nothing = sum == 0.f;  // no token, or none above -infinity (a NaN stays one)
-  const float inv = nothing ? 0.f : 1.0f / sum;
+    for (int w = 1; w < R; ++w)
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float v;
-    if constexpr (E == 1) v = o[0];
-    else v = o[e];
-    store_out(a.out, a.out_dtype, (int64_t)row * D + lane * E + e, nothing ? 0.f : v * inv);
+      for (int j = 0; j < J; ++j) o[j] = o[j] + so[wave + w][j][lane];
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = nothing ? -INFINITY : top * 0.69314718055994530942f + logf(sum);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const uint32_t r = first + j;
+    if (r >= g.p.R) break;
+    const uint32_t t = divide(r, g.p.group), h = hk * g.p.heads_each + (r - t * g.p.heads_each);
+    const int64_t row = ((int64_t)b * a.T + t) * a.Hq + h;
+    float all = sum[j];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) all += __shfl_xor(all, off);
+    const bool nothing = all == 0.f;  // no token, or none above -infinity (a NaN stays one)
+    const float inv = nothing ? 0.f : 1.0f / all;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float v;
+      if constexpr (E == 1) v = o[j][0];
+      else v = o[j][e];
+      store_out(a.out, a.out_dtype, row * D + lane * E + e, nothing ? 0.f : v * inv);
+    }
+    if (lane == 0 && a.lse != nullptr) a.lse[row] = nothing ? -INFINITY : top[j] * 0.69314718055994530942f + logf(all);
+  }
 }
 
 template <int D>
 hipError_t launch_join(const KvArgs& g, hipStream_t s) {
-  // a wave a row where that fills the chip, else four
-  const int64_t rows = g.a.B * g.a.T * g.a.Hq;
-  if (rows < (int64_t)device_cus() * 4)
-    hipLaunchKernelGGL((q1_kv_join<D, kWaves>), dim3((unsigned)rows), dim3(64 * kWaves), 0, s, g);
+  const int64_t groups = (int64_t)g.p.entries * g.c.Hkv * g.p.groups_each;
+  if (g.p.join_rows == 1)
+    hipLaunchKernelGGL((q1_kv_join<D, kWaves, 1>), dim3((unsigned)groups), dim3(64 * kWaves), 0, s, g);
   else
-    hipLaunchKernelGGL((q1_kv_join<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, s, g);
+    hipLaunchKernelGGL((q1_kv_join<D, 1, 4>), dim3((unsigned)((groups + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0, s, g);
   return hipGetLastError();
 }
 
-template <bool F16, int BITS, int D, int NM>
-hipError_t launch(const KvArgs& g, hipStream_t s) {
-  constexpr int bytes = kTokenLds<D, NM, F16 ? 2 : 1>();
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_kv_tokens<F16, BITS, D, NM>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <int D, typename K>
+hipError_t launch(K kernel, int waves, int bytes, hipError_t attr, const KvArgs& g, hipStream_t s) {
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((q1_kv_tokens<F16, BITS, D, NM>), dim3((unsigned)g.p.wgs), dim3(64 * kWaves), bytes, s, g);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)g.p.wgs), dim3(64 * waves), bytes, s, g);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess || !g.p.cut ? e : launch_join<D>(g, s);
 }
 
+template <bool F16, int BITS, int D, int NM>
+hipError_t launch_tokens(const KvArgs& g, hipStream_t s) {
+  constexpr int bytes = kTokenLds<D, NM, F16 ? 2 : 1>();
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_kv_tokens<F16, BITS, D, NM>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return launch<D>(q1_kv_tokens<F16, BITS, D, NM>, kWaves, bytes, attr, g, s);
+}
+
+template <bool F16, int BITS, int D>
+hipError_t launch_rows(const KvArgs& g, hipStream_t s) {
+  constexpr int bytes = 2 * Staged<BITS, D>::kBytes, NM = D < 256 ? 2 : 1;
+  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q1_kv_rows<F16, BITS, D, NM>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return launch<D>(q1_kv_rows<F16, BITS, D, NM>, kRowWaves, bytes, attr, g, s);
+}
+
 template <bool F16, int BITS, int D>
 hipError_t launch_n(const KvArgs& g, hipStream_t s) {
+  if (g.p.by_rows) return launch_rows<F16, BITS, D>(g, s);
   if constexpr (D < 256) {
-    if (g.p.nm == 2) return launch<F16, BITS, D, 2>(g, s);
+    if (g.p.nm == 2) return launch_tokens<F16, BITS, D, 2>(g, s);
   }
-  return launch<F16, BITS, D, 1>(g, s);
+  return launch_tokens<F16, BITS, D, 1>(g, s);
 }
 
 template <bool F16, int BITS>
@@ -701,14 +984,25 @@ KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a) {
   KvPlan p = {};
   p.heads_each = (uint32_t)(a.Hq / c.Hkv);
   p.R = (uint32_t)(a.T * p.heads_each);
-  p.nm = p.R > 16 && c.D < 256 ? 2 : 1;
-  p.rows = 16 * p.nm;
+  p.nm = p.R > 16 && c.D < 256 ? 2 : 1;  // groups of 16 rows a wave: 256 registers hold two of D 128
+  const int64_t cus = device_cus(), units = up_div(a.max_pages * c.page_size, kStep);
+  // By rows where that form has a full item for half of the compute units, and many tokens.  D 128,
+  // group 6, 4 heads of keys, tokens | rows: 8000 queries of 8000 tokens 905 | 599 us, 2 x 1000 of
+  // 5003 276 | 216; few tokens or few items: 2048 of 2048 70 | 96, 512 of 512 16 | 29.
+  const int64_t row_items = a.B * (p.R / (16 * p.nm * kRowWaves)) * c.Hkv;
+  p.by_rows = 2 * row_items >= cus && units >= 32;
+  p.rows = 16 * p.nm * (p.by_rows ? kRowWaves : 1);
   p.row_blocks = (uint32_t)up_div(p.R, p.rows);
-  const int64_t items = a.B * p.row_blocks * c.Hkv, units = up_div(a.max_pages * c.page_size, kStep);
+  const int64_t items = a.B * p.row_blocks * c.Hkv;
   p.too_large = items >= (int64_t)1 << 31 || (units > 0 && items >= ((int64_t)1 << 31) / units);
   p.entries = p.too_large ? 0 : (uint32_t)(a.B * p.row_blocks);
-  const int64_t slots = (int64_t)device_cus() * 2;
-  p.cut = units > 8 + items / 8 && items < slots * 4;
+  // Whole items, or an even cut of all of their units over the workgroups that run at a time:
+  // where the last round of whole items would leave more units of time unused than joining costs
+  // (a unit of an item by rows takes 4.7 us, one by tokens 1 to 2).  Whole | cut by tokens: 128
+  // items of 16 units 20.3 | 22.0 us, 304 of 40 90 | 54, 752 of 40 139 | 145, 16 of 5 12.6 | 16.1;
+  // by rows: 192 of 40 231 | 216, 188 of 40 (D 256) 247 | 214, 752 of 63 599 | 798.
+  const int64_t slots = cus * (p.by_rows ? 1 : 2), room = up_div(items, slots) * slots;
+  p.cut = !p.too_large && units * (room - items) > (p.by_rows ? 4 : 10 + items / 64) * room;
   if (!p.cut) {
     p.too_large |= items > (1 << 24) - 1;
     p.wgs = (uint32_t)items;
@@ -723,10 +1017,13 @@ KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a) {
     p.ws_bytes = p.ml_off + up256(rows * 8);
   }
   p.page = divider((uint32_t)c.page_size);
-  p.heads = divider((uint32_t)a.Hq);
-  p.queries = divider((uint32_t)a.T);
   p.group = divider(p.heads_each);
   p.blocks = divider(p.row_blocks);
+  // joining: four waves a row where rows are few, else a wave four rows
+  p.join_rows = items * p.rows < (int64_t)device_cus() * 16 ? 1 : 4;
+  const uint32_t used = p.rows < p.R ? p.rows : p.R;  // rows of an item
+  p.groups_each = (uint32_t)up_div(used, p.join_rows);
+  p.groups = divider(p.groups_each);
   p.kv_heads = divider((uint32_t)c.Hkv);
   p.sequences = divider((uint32_t)a.B);
   return p;

@@ -35,6 +35,7 @@ inline Divider divider(uint32_t d) {
 // How a call is cut into work items (see q1_kv_attn.hip).
 struct KvPlan {
   int32_t nm;              // blocks of 16 query rows of a wave
+  int32_t by_rows;         // 1: waves of an item share its tokens
   uint32_t heads_each, R;  // query heads and rows of a key/value head
   uint32_t rows;           // rows of an item
   uint32_t row_blocks;     // items along the rows
@@ -42,7 +43,8 @@ struct KvPlan {
   int32_t cut;             // 1: workgroups have equal shares of all tokens, else an item each
   uint32_t wgs;
   int32_t too_large;       // more units of work than are counted in 31 bits
-  Divider page, heads, queries, group, blocks, kv_heads, sequences;  // by page_size, Hq, T, heads_each, row_blocks, Hkv, B
+  uint32_t join_rows, groups_each;  // rows of a wave that joins, and such groups of an item
+  Divider page, group, blocks, kv_heads, sequences, groups;  // by page_size, heads_each, row_blocks, Hkv, B, groups_each
   size_t o_off, ml_off, ws_bytes;
 };
 

@@ -217,7 +217,7 @@ q1_status q1_kv_attn(const q1_kv* c, const q1_kv_query* a, void* workspace, size
   if (!aligned(a->page_table, 4) || !aligned(a->lens, 4) || !aligned(a->lse, 4))
     return fail(Q1_ERR_INVALID_ARG, "page_table, lens and lse must be 4-byte aligned");
   const KvPlan plan = plan_kv_attn(*c, *a);
-  if (plan.too_large || a->B * a->T * a->Hq > kMaxGrid * 4) return fail(Q1_ERR_UNSUPPORTED, "call too large");
+  if (plan.too_large) return fail(Q1_ERR_UNSUPPORTED, "call too large");
   const size_t need = plan.ws_bytes;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(Q1_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", need, workspace ? workspace_bytes : 0);
