@@ -1004,7 +1004,7 @@ KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a) {
   const int64_t slots = cus * (p.by_rows ? 1 : 2), room = up_div(items, slots) * slots;
   p.cut = !p.too_large && units * (room - items) > (p.by_rows ? 4 : 10 + items / 64) * room;
   if (!p.cut) {
-    p.too_large |= items > (1 << 24) - 1;
+    p.too_large |= items >= ((int64_t)1 << 32) / (64 * (p.by_rows ? kRowWaves : kWaves));  // lanes of a launch
     p.wgs = (uint32_t)items;
   } else {  // as many as run at a time, at most 64 for an item's rows on average, and one a unit
     int64_t wgs = slots;

@@ -97,7 +97,7 @@ typedef struct q1_kv_query {
   int32_t Hq;                 /* Hq % Hkv == 0 */
   int32_t dtype;              /* of q: Q1_BF16 or Q1_F16 */
   int32_t out_dtype;          /* Q1_F32, Q1_F16 or Q1_BF16 */
-  float scale;
+  float scale;                /* finite */
 } q1_kv_query;
 
 q1_status q1_kv_attn(const q1_kv* c, const q1_kv_query* a, void* workspace, size_t workspace_bytes, void* stream);
