@@ -148,9 +148,9 @@ q1_status check_scan(const q1_scan* d, int64_t tokens, int64_t nseq) {
   return Q1_OK;
 }
 
-// Whether a launch of the prompt's scan would have too many workgroups, of one wave or (joining) four.
+// Whether a launch of the prompt's scan would have too many workgroups.
 bool scan_too_large(const q1_scan& d, int64_t tokens, int64_t nseq) {
-  return scan_pieces(d, tokens, nseq) > kMaxGrid * 4 / ((d.Di + 63) / 64) || nseq >= k31 / (d.Di * d.N);
+  return scan_pieces(d, tokens, nseq) > kMaxGrid / ((d.Di + 63) / 64) || nseq >= k31 / (d.Di * d.N);
 }
 
 }  // namespace

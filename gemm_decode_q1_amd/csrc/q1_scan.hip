@@ -3,24 +3,21 @@
 // Single tokens: four lanes have a channel, a quarter of its states each, so that a
 // state is read and written in whole lines and one sequence fills some hundred waves.
 //
-// Prompts: a lane has a channel and all of its states in registers; B and C are the
-// same for all channels and come through scalar loads, a token ahead.  A prompt is cut
-// into pieces so that the waves fill the chip, in three launches:
-//   q1_scan_state  the state at the end of each piece from a zero state, and the sum
-//                  of its deltas (the decay over the piece is exp(A * sum));
-//   q1_scan_join   each piece's first state, one after the other;
-//   q1_scan_out    the outputs, and from a sequence's last piece its final state.
-// A sequence's last piece needs no q1_scan_state, so short sequences have none.  (Both
-// are q1_scan_kernel, without and with outputs.)
+// Prompts: the same, four waves for 64 channels.  A prompt is cut into pieces so that the
+// waves fill the chip, in three launches:
+//   q1_scan_kernel<.., false>  the state at the end of each piece from a zero state, and the
+//                              sum of its deltas (the decay over the piece is exp(A * sum));
+//   q1_scan_join               each piece's first state, one after the other;
+//   q1_scan_kernel<.., true>   the outputs, and from a sequence's last piece its final state.
+// A sequence's last piece needs no first walk, so short sequences have none.
 //
-// Bound by the vector units (93 % busy): a state costs a product, an exponential (8 cycles
-// a wave, the others 4), a product and two multiply-adds a token, and without outputs one
-// less, so that one walk over 16384 tokens of 5120 channels of 16 states cannot take less
-// than 235 us at 2.15 GHz, both 430; with deltas, skip and gate they take 356 and 267, the
-// join 27 (100 MB).  Reading and writing rows would take 136.
-// Walking once would leave 80 waves for one sequence (9 ms), or, with a state a lane, 1280
-// whose outputs need a sum over 16 lanes a token: by count of instructions no less than
-// these, on 1024 SIMDs.
+// Bound by the vector units (busy throughout): a state costs a product, an exponential (8
+// cycles a wave, the others 4), a product and two multiply-adds a token, and without outputs
+// one less, so that one walk over 16384 tokens of 5120 channels of 16 states cannot take less
+// than 235 us at 2.15 GHz, both 430; with deltas, skip and gate 544 are measured.  Reading and
+// writing rows would take 136.  A lane with all states of a channel, B and C in scalar
+// registers, needs a tenth fewer instructions but four times the pieces: 602 us, 4099 tokens of 7
+// sequences 206 | 164, 16000 of 60 (whole, but for very long ones) 572 | 410, 77 of one 24 | 16.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -37,7 +34,6 @@ constexpr int kThreads = 256;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef const __attribute__((address_space(4))) uint32_t* scalar_words;  // read through scalar loads
 
 template <bool F16>
 __device__ __forceinline__ float elem(uint32_t b) {
@@ -74,17 +70,10 @@ __device__ __forceinline__ float delta_of(const q1_scan& d, uint32_t raw, float 
   return d.softplus ? softplus(s) : s;
 }
 
-// An element of a pair, times x (fp16: with the conversion in the multiply-add).
-template <bool F16>
-__device__ __forceinline__ float times(uint32_t w, int hi, float x) {
-  if constexpr (F16) return __builtin_fmaf(elem16<F16>(w, hi), x, 0.f);
-  else return elem16<F16>(w, hi) * x;
-}
-
 // The sum of four neighbouring lanes' values.
 __device__ __forceinline__ float sum_quad(float v) {
-  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, false));
-  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, false));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, true));
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, true));
   return v;
 }
 
@@ -148,57 +137,77 @@ struct PromptArgs {
   float* sum;      // [pieces, Di]
 };
 
-constexpr int kBlock = 8;  // tokens of a block
+// Eight outputs of a row.
+__device__ __forceinline__ void store_row(const q1_scan& d, int64_t at, const float* o) {
+  if (d.out_dtype == F32) {
+    f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(d.out) + at);
+    p[0] = f32x4{o[0], o[1], o[2], o[3]};
+    p[1] = f32x4{o[4], o[5], o[6], o[7]};
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = d.out_dtype == F16 ? pack16<true>(o[2 * e], o[2 * e + 1]) : pack16<false>(o[2 * e], o[2 * e + 1]);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(d.out) + at) = w;
+  }
+}
 
-// A wave's part of the LDS: a block's deltas, deltas times x, and sums over the states.
+__device__ __forceinline__ int64_t slot_of(const q1_scan& d, int64_t seq) {
+  const int64_t slot = d.slot_ids ? d.slot_ids[seq] : seq;
+  return slot >= 0 && slot < d.slots ? slot : -1;
+}
+
+// A workgroup's walk over the rows [t0, t1) of a piece, 64 channels from `first` on.  Rows come
+// in and go out by blocks of 32 tokens in which a lane has 8 channels of one token (16
+// bytes): so it makes the deltas and applies skip and gate.  Between these, through LDS, four
+// lanes have a channel, a quarter of its states each, token by token; B and C come from LDS
+// as fp32.  (Without the places of `pair` and `four` the LDS, busy for 81 % of the time with a third
+// of that conflicts, was the bound: 16384 tokens 613 us, with them 544.)
+constexpr int kBlock = 32;
+
+template <int N>
 struct BlockLds {
-  float delta[kBlock][64], dx[kBlock][64], y[kBlock][64];
+  alignas(16) float2 dd[kBlock][64];  // delta, and delta times x, of the channel at pair(c)
+  alignas(16) float y[kBlock][64];    // of the channel at four(c)
+  alignas(16) float bc[kBlock][2 * N];
+  // Places of a row's channels: eight lanes that write or read 8 channels each, 16 bytes at a
+  // time, meet all banks.
+  static __device__ __forceinline__ int pair(int c) { return c ^ (c >> 3 & 6); }
+  static __device__ __forceinline__ int four(int c) { return c ^ (c >> 3 & 4); }
 };
 
-// B and C of a token, in scalar registers.
-template <int N, bool OUT>
-struct Shared {
-  uint32_t b[N / 2], c[OUT ? N / 2 : 1];
-};
-
-// A wave's walk over the rows [t0, t1) of a piece, 64 channels from c0 on.  Rows come in
-// and go out by blocks of 8 tokens in which a lane has 8 channels of one token (16 bytes):
-// so it makes the deltas and applies skip and gate.  Between these, through LDS, a lane
-// has one channel and its states, token by token.
 template <bool F16, bool DT32, int N, bool OUT>
 struct Walk {
-  static constexpr bool kPrefetch = N <= 16;  // (two tokens of more states do not fit the scalar registers)
+  static constexpr int M = N / 4;  // states of a lane
   const q1_scan& d;
-  BlockLds& m;
+  BlockLds<N>& m;
   const int64_t t1;
-  const int lane, row;         // this lane's token of a block
-  const uint32_t ch, c8;       // this lane's channel; first of its 8 channels of a row
-  float h[N], A[N], bias[8], skip[OUT ? 8 : 1], sum = 0.f;
+  const int row, part;    // this thread's token of a block, and eighth of it
+  const int c, quad;      // this lane's channel of the 64, and quarter of its states
+  const uint32_t first, c8;
+  float h[M], A[M], bias[8], skip[OUT ? 8 : 1], sum = 0.f;
   u32x4 x, z, dt[DT32 ? 2 : 1];
+  uint16_t b[N / 8], cc[OUT ? N / 8 : 1];
 
-  __device__ __forceinline__ Walk(const q1_scan& d, BlockLds& m, int64_t t1, uint32_t c0)
-      : d(d), m(m), t1(t1), lane(threadIdx.x & 63), row(lane >> 3), ch(least(c0 + lane, (uint32_t)d.Di - 1)),
-        c8(least(c0 + 8 * (lane & 7), (uint32_t)d.Di - 8)) {
-    take(d.A + (int64_t)ch * N, A);
+  __device__ __forceinline__ Walk(const q1_scan& d, BlockLds<N>& m, int64_t t1, uint32_t first)
+      : d(d), m(m), t1(t1), row(threadIdx.x >> 3), part(threadIdx.x & 7), c(threadIdx.x >> 2), quad(threadIdx.x & 3), first(first),
+        c8(first + 8 * part < (uint32_t)d.Di ? first + 8 * part : (uint32_t)d.Di - 8) {
+    const uint32_t ch = channel();
 #pragma unroll
-    for (int n = 0; n < N; ++n) A[n] *= kLog2e;
+    for (int n = 0; n < M; ++n) A[n] = d.A[(int64_t)ch * N + quad * M + n] * kLog2e;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       bias[e] = d.dt_bias ? d.dt_bias[c8 + e] : 0.f;
       if constexpr (OUT) skip[e] = d.D ? d.D[c8 + e] : 0.f;
     }
   }
+  __device__ __forceinline__ bool live() const { return first + c < (uint32_t)d.Di; }
+  __device__ __forceinline__ uint32_t channel() const { return live() ? first + c : (uint32_t)d.Di - 1; }
 
-  static __device__ __forceinline__ void take(const float* from, float* to) {
-#pragma unroll
-    for (int n = 0; n < N / 4; ++n) {
-      const f32x4 v = reinterpret_cast<const f32x4*>(from)[n];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) to[4 * n + j] = v[j];
-    }
+  template <typename T, int K>
+  static __device__ __forceinline__ void take(const void* from, T (&to)[K]) {
+    __builtin_memcpy(to, __builtin_assume_aligned(from, sizeof(T) * K), sizeof(T) * K);
   }
-
-  static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
   // The block of rows from t on (the last row again past the end).
   __device__ __forceinline__ void load(int64_t t) {
@@ -211,168 +220,129 @@ struct Walk {
     } else {
       dt[0] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(d.dt) + at * d.dt_ld + c8);
     }
+    take(static_cast<const uint16_t*>(d.B) + at * d.b_ld + part * (N / 8), b);
     if constexpr (OUT) {
+      take(static_cast<const uint16_t*>(d.C) + at * d.c_ld + part * (N / 8), cc);
       z = u32x4{0u, 0u, 0u, 0u};
       if (d.z != nullptr) z = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(d.z) + at * d.z_ld + c8);
     }
   }
 
   __device__ __forceinline__ void put_deltas() {
-    float delta[8], dx[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = (DT32 ? __uint_as_float(dt[DT32 ? e >> 2 : 0][e & 3]) : elem16<F16>(dt[0][e >> 1], e & 1)) + bias[e];
-      const float soft = softplus(s);
-      delta[e] = d.softplus ? soft : s;
-      dx[e] = delta[e] * elem16<F16>(x[e >> 1], e & 1);
+    for (int e = 0; e < 8; e += 2) {
+      f32x4 w;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float s = (DT32 ? __uint_as_float(dt[DT32 ? e >> 2 : 0][(e + j) & 3]) : elem16<F16>(dt[0][e >> 1], j)) + bias[e + j];
+        const float soft = softplus(s);
+        w[2 * j] = d.softplus ? soft : s;
+        w[2 * j + 1] = w[2 * j] * elem16<F16>(x[e >> 1], j);
+      }
+      *reinterpret_cast<f32x4*>(&m.dd[row][m.pair(8 * part + e)]) = w;
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      *reinterpret_cast<f32x4*>(&m.delta[row][8 * (lane & 7) + 4 * q]) = f32x4{delta[4 * q], delta[4 * q + 1], delta[4 * q + 2], delta[4 * q + 3]};
-      *reinterpret_cast<f32x4*>(&m.dx[row][8 * (lane & 7) + 4 * q]) = f32x4{dx[4 * q], dx[4 * q + 1], dx[4 * q + 2], dx[4 * q + 3]};
-    }
-  }
-
-  // B and C of the row `u` behind those at bp and cp.
-  __device__ __forceinline__ void load_shared(const char* bp, const char* cp, uint32_t u, Shared<N, OUT>& s) const {
-    const scalar_words b = (scalar_words)(uintptr_t)(bp + u * (uint32_t)(d.b_ld * 2));
-    const scalar_words c = (scalar_words)(uintptr_t)(cp + u * (uint32_t)(d.c_ld * 2));
-#pragma unroll
-    for (int n = 0; n < N / 2; ++n) s.b[n] = b[n];
-    if constexpr (OUT) {
-#pragma unroll
-      for (int n = 0; n < N / 2; ++n) s.c[n] = c[n];
+    for (int n = 0; n < N / 8; ++n) {
+      m.bc[row][part * (N / 8) + n] = elem<F16>(b[n]);
+      if constexpr (OUT) m.bc[row][N + part * (N / 8) + n] = elem<F16>(cc[n]);
     }
   }
 
-  // Scalar loads come back in any order: what waits for one waits for all of them.  So
-  // these are waited for here, before the next ones are issued.
-  __device__ __forceinline__ void arrived(Shared<N, OUT>& s) const {
+  // Token u of the block: its states, and this lane's part of the output.
+  __device__ __forceinline__ float token(int u) {
+    const float2 w = m.dd[u][m.pair(c)];
+    if constexpr (!OUT) sum += w.x;
+    float y = 0.f;
 #pragma unroll
-    for (int n = 0; n < N / 2; ++n) {
-      asm volatile("" : "+s"(s.b[n]));
-      if constexpr (OUT) asm volatile("" : "+s"(s.c[n]));
+    for (int n = 0; n < M; ++n) {
+      h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(w.x * A[n]), h[n], w.y * m.bc[u][quad * M + n]);
+      if constexpr (OUT) y = __builtin_fmaf(m.bc[u][N + quad * M + n], h[n], y);
     }
-    __builtin_amdgcn_sched_barrier(0);
+    return y;
   }
 
-  __device__ __forceinline__ void token(int u, const Shared<N, OUT>& w) {
-    const float delta = m.delta[u][lane], dx = m.dx[u][lane];
-    if constexpr (!OUT) sum += delta;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A[n]), h[n], times<F16>(w.b[n / 2], n & 1, dx));
-      if constexpr (OUT) y[n & 3] = __builtin_fmaf(elem16<F16>(w.c[n / 2], n & 1), h[n], y[n & 3]);
-    }
-    if constexpr (OUT) m.y[u][lane] = (y[0] + y[1]) + (y[2] + y[3]);
+  static __device__ __forceinline__ float from1(float v) {  // of the lane whose number differs in bit 0
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, true));
+  }
+  static __device__ __forceinline__ float from2(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, true));
   }
 
-  __device__ __forceinline__ void put_rows(int64_t t, uint32_t first, u32x4 x, u32x4 z) const {
+  __device__ __forceinline__ void put_rows(int64_t t, u32x4 x, u32x4 z) const {
     float o[8];
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(&m.y[row][8 * (lane & 7)]);
-    const f32x4 hi = *reinterpret_cast<const f32x4*>(&m.y[row][8 * (lane & 7) + 4]);
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&m.y[row][m.four(8 * part)]);
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&m.y[row][m.four(8 * part + 4)]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       o[e] = __builtin_fmaf(skip[e], elem16<F16>(x[e >> 1], e & 1), e < 4 ? lo[e & 3] : hi[e & 3]);
       const float gate = silu_fast(elem16<F16>(z[e >> 1], e & 1));
       o[e] = d.z != nullptr ? o[e] * gate : o[e];
     }
-    if (t + row >= t1 || first + 8 * (lane & 7) >= d.Di) return;
-    const int64_t at = (t + row) * d.Di + c8;
-    if (d.out_dtype == F32) {
-      f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(d.out) + at);
-      p[0] = f32x4{o[0], o[1], o[2], o[3]};
-      p[1] = f32x4{o[4], o[5], o[6], o[7]};
-    } else {
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = d.out_dtype == F16 ? pack16<true>(o[2 * e], o[2 * e + 1]) : pack16<false>(o[2 * e], o[2 * e + 1]);
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(d.out) + at) = w;
-    }
+    if (t + row < t1 && first + 8 * part < d.Di) store_row(d, (t + row) * d.Di + c8, o);
   }
 
-  __device__ __forceinline__ void run(int64_t t0, uint32_t first) {
+  __device__ __forceinline__ void run(int64_t t0) {
     load(t0);
-    Shared<N, OUT> s[2];
-    const char* bp = reinterpret_cast<const char*>(d.B) + t0 * d.b_ld * 2;
-    const char* cp = reinterpret_cast<const char*>(d.C) + t0 * d.c_ld * 2;
-    if constexpr (kPrefetch) load_shared(bp, cp, 0, s[0]);
     for (int64_t t = t0; t < t1; t += kBlock) {
       put_deltas();
-      __builtin_amdgcn_wave_barrier();
+      __syncthreads();
       const u32x4 xc = x, zc = z;
       load(t + kBlock);
-      if (t + kBlock <= t1) {
+      const int left = (int)(t1 - t < kBlock ? t1 - t : kBlock);
+      int u = 0;
+#pragma clang loop unroll_count(2)
+      for (; u + 4 <= left; u += 4) {  // the sums of four tokens, one to each of a channel's lanes
+        float y[4];
 #pragma unroll
-        for (int u = 0; u < kBlock; ++u) {
-          if constexpr (kPrefetch) {
-            arrived(s[u & 1]);
-            load_shared(bp, cp, u + 1 < kBlock || t + kBlock < t1 ? u + 1 : u, s[(u + 1) & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-          } else {
-            load_shared(bp, cp, u, s[u & 1]);
-          }
-          token(u, s[u & 1]);
-        }
-      } else {  // a sequence's last few
-        const int left = (int)(t1 - t);
-#pragma clang loop unroll(disable)
-        for (int u = 0; u < left; ++u) {
-          load_shared(bp, cp, u, s[0]);
-          token(u, s[0]);
+        for (int j = 0; j < 4; ++j) y[j] = token(u + j);
+        if constexpr (OUT) {
+          const bool odd = quad & 1, high = quad & 2;
+          const float r0 = (odd ? y[1] : y[0]) + from1(odd ? y[0] : y[1]), r1 = (odd ? y[3] : y[2]) + from1(odd ? y[2] : y[3]);
+          m.y[u + quad][m.four(c)] = (high ? r1 : r0) + from2(high ? r0 : r1);
         }
       }
-      bp += kBlock * d.b_ld * 2;
-      cp += kBlock * d.c_ld * 2;
-      __builtin_amdgcn_wave_barrier();
-      if constexpr (OUT) put_rows(t, first, xc, zc);
+      for (; u < left; ++u) {
+        const float y = token(u);
+        if constexpr (OUT) m.y[u][m.four(c)] = sum_quad(y);  // (the four write one value)
+      }
+      __syncthreads();
+      if constexpr (OUT) put_rows(t, xc, zc);
     }
   }
 };
 
-__device__ __forceinline__ int64_t slot_of(const q1_scan& d, int64_t seq) {
-  const int64_t slot = d.slot_ids ? d.slot_ids[seq] : seq;
-  return slot >= 0 && slot < d.slots ? slot : -1;
-}
-
 template <bool F16, bool DT32, int N, bool OUT>
-__global__ __launch_bounds__(64) void q1_scan_kernel(const PromptArgs a) {
+__global__ __launch_bounds__(kThreads) void q1_scan_kernel(const PromptArgs a) {
+  constexpr int M = N / 4;
   const q1_scan& d = a.d;
-  const int64_t piece = blockIdx.x / a.blocks, c0 = (blockIdx.x - piece * a.blocks) * 64 + threadIdx.x;
+  const int64_t piece = blockIdx.x / a.blocks;
+  const uint32_t first = (uint32_t)(blockIdx.x - piece * a.blocks) * 64;
   const Piece p = scalar(find_piece_wave(a.r, piece, a.by, a.per));
   if (p.t0 >= p.t1) return;
   if (!OUT && p.last()) return;
-  const bool live = c0 < d.Di;
-  const int64_t ch = live ? c0 : d.Di - 1, slot = scalar(slot_of(d, p.seq));
+  const int64_t slot = scalar(slot_of(d, p.seq));
   if (slot < 0) {
-    if (OUT && live)
-      for (int64_t t = p.t0; t < p.t1; ++t) store_out(d.out, d.out_dtype, t * d.Di + ch, 0.f);
+    const uint32_t ch = first + (threadIdx.x & 63);
+    if (OUT && ch < d.Di)
+      for (int64_t t = p.t0 + (threadIdx.x >> 6); t < p.t1; t += kThreads / 64) store_out(d.out, d.out_dtype, t * d.Di + ch, 0.f);
     return;
   }
-  __shared__ BlockLds m;
-  const uint32_t first = (uint32_t)(blockIdx.x - piece * a.blocks) * 64;
+  __shared__ BlockLds<N> m;
   Walk<F16, DT32, N, OUT> w(d, m, p.t1, first);
+  const int64_t ch = w.channel();
+  float* const st = d.state + (slot * d.Di + ch) * N + w.quad * M;
+  float* const at = a.h + (piece * N + w.quad * M) * d.Di + ch;
+#pragma unroll
+  for (int n = 0; n < M; ++n) w.h[n] = !OUT ? 0.f : p.first() ? st[n] : at[(n - N) * d.Di];
+  w.run(p.t0);
+  if (!w.live()) return;
   if constexpr (!OUT) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) w.h[n] = 0.f;
-  } else if (p.first()) {
-    w.take(d.state + (slot * d.Di + ch) * N, w.h);
-  } else {
-#pragma unroll
-    for (int n = 0; n < N; ++n) w.h[n] = a.h[((piece - 1) * N + n) * d.Di + ch];
-  }
-  w.run(p.t0, first);
-  if (!live) return;
-  if constexpr (!OUT) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) a.h[(piece * N + n) * d.Di + ch] = w.h[n];
-    a.sum[piece * d.Di + ch] = w.sum;
+    for (int n = 0; n < M; ++n) at[n * d.Di] = w.h[n];
+    if (w.quad == 0) a.sum[piece * d.Di + ch] = w.sum;
   } else if (p.last()) {
 #pragma unroll
-    for (int n = 0; n < N / 4; ++n)
-      reinterpret_cast<f32x4*>(d.state + (slot * d.Di + ch) * N)[n] = f32x4{w.h[4 * n], w.h[4 * n + 1], w.h[4 * n + 2], w.h[4 * n + 3]};
+    for (int n = 0; n < M; ++n) st[n] = w.h[n];
   }
 }
 
@@ -414,7 +384,7 @@ template <bool F16, bool DT32, int N>
 hipError_t launch_prompt(const PromptArgs& a, int64_t pieces, hipStream_t s) {
   const dim3 grid((unsigned)(pieces * a.blocks));
   if (a.h != nullptr) {
-    hipLaunchKernelGGL((q1_scan_kernel<F16, DT32, N, false>), grid, dim3(64), 0, s, a);
+    hipLaunchKernelGGL((q1_scan_kernel<F16, DT32, N, false>), grid, dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t n = a.r.nseq * a.d.Di * N;
@@ -422,7 +392,7 @@ hipError_t launch_prompt(const PromptArgs& a, int64_t pieces, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((q1_scan_kernel<F16, DT32, N, true>), grid, dim3(64), 0, s, a);
+  hipLaunchKernelGGL((q1_scan_kernel<F16, DT32, N, true>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -438,17 +408,18 @@ size_t sums_at(const q1_scan& d, int64_t pieces) { return ((size_t)pieces * d.N 
 
 }  // namespace
 
-// About three pieces for each wave that the chip holds at a time (four a SIMD), as they
-// differ in length and the first to end make room; at least 24 tokens, or 16 where those
-// would not be a wave a SIMD.  5120 channels of 16 states, us: 16384 tokens in pieces
-// of 112 570, of 328 (one for each wave) 630, of 32 621, whole 8985; 4099 tokens of 7 sequences
-// by 32 190, by 96 214, by 16 232; 8000 of 32 by 48 305, whole 618; 600 of one by 24 48, by 64 66;
-// 77 of one by 16 24, by 24 29, whole 37.
+// Tokens of a piece, so that there are about seven workgroups a compute unit, but 64 to 256, and 32
+// for little work.  Where the sequences alone are 16 workgroups a unit, only those that have more
+// than an eighth of all tokens are cut.  5120 channels of 16 states, us: 16384 tokens by 128 553, by
+// 256 544, whole 2356; 4099 tokens of 7 sequences by 64 180, 192 164, 320 181; 600 of one by 32 45, 64 44, 128
+// 54; 300 by 32 29, 64 33; 77 by 32 20, whole 16; 8000 of 32 by 256 271, whole 262; 16000 of 60 by 256 516, whole 407.
 int64_t scan_chunk(const q1_scan& d, int64_t tokens, int64_t nseq) {
-  const int64_t blocks = (d.Di + 63) / 64, simds = (int64_t)device_cus() * 4;
-  int64_t per = (tokens * blocks / (12 * simds) + kBlock - 1) / kBlock * kBlock;
-  if (per < 24) per = tokens * blocks < 24 * simds ? 16 : 24;
-  return tokens <= per ? 0 : per;  // (no sequence has a second piece)
+  const int64_t blocks = (d.Di + 63) / 64, cus = device_cus(), work = tokens * blocks;
+  int64_t per = (work / (7 * cus) + kBlock / 2) / kBlock * kBlock;
+  if (per > 256) per = 256;
+  if (per < 64) per = work < 96 * cus ? 32 : 64;
+  if (nseq * blocks >= 16 * cus && per < tokens / 8) per = (tokens / 8 + kBlock - 1) / kBlock * kBlock;
+  return tokens <= (per > 96 ? per : 96) ? 0 : per;  // (no sequence has a second piece)
 }
 
 int64_t scan_pieces(const q1_scan& d, int64_t tokens, int64_t nseq) {
