@@ -16,13 +16,13 @@
 // joined in LDS; keys go from memory to the matrix core through registers alone.  Bound by
 // the bytes of the pages and by the vector instructions (98 a wave for 16 rows x 32 tokens).
 // By rows (prompts): 8 waves, each with 32 rows (16 of D 256); a tile of 64 tokens is
-// converted once for all of them.  Bound by the vector instructions of the softmax: the
-// matrix cores are busy for 42 % of the time.
+// converted once for all of them.  Bound by the products, where there is much to do: 8000
+// queries of 8000 tokens take 543 us for 590 Gflop (both parts of the weights), nine tenths of
+// the rate of a large library product (1.22 PFLOP/s).
 //
 // Measured (us): 32 sequences of 8201 tokens, D 256, 4 bits 50 (the pages at the rate of a copy:
 // 36); 8 of 65537, 3 queries each, D 128, 76 (70); 4 of 519 9.9; 2 x 1000 queries of 5003
-// tokens, 24 heads of D 128, 8 bits 220; 8000 queries of 8000 tokens 600 (1.3 PFLOP/s of
-// products with both parts of the weights).
+// tokens, 24 heads of D 128, 8 bits 181 (129 at that rate; the join and the parts it reads 20).
 //
 // A token that a query does not see has the score -infinity, whatever its key.  Its
 // weight 0 would still make a NaN of a NaN value, so NaN blocks of values enter as
@@ -664,7 +664,9 @@ struct Staged {
 // An item by rows: each of 8 waves has 16 NM rows, the tiles of 64 tokens are converted once for
 // all waves and lie in LDS, two in turn.  Against 16 rows a wave and two workgroups a compute
 // unit, 32 rows and one workgroup halve what is converted, and what is read from LDS
-// for each product.  2 x 1000 queries of 5003 tokens (D 128, 4 bits): 197 | 192 us, fp16 137 | 130.
+// for each product.  2 x 1000 queries of 5003 tokens (D 128, 4 bits): 197 | 192 us, fp16 137 |
+// 130; with loads a step ahead of their products and the priority 206 | 194 (8 bits, without
+// and with), 8000 of 8000 563 | 543.
 template <bool F16, int BITS, int D, int NM>
 __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, unsigned char* lds) {
   constexpr int QP = F16 ? 2 : 1, KS = D / 32, DT = D / 16;
@@ -749,16 +751,25 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
       f32x4 S[NM][2];
 #pragma unroll
       for (int y = 0; y < NM; ++y) S[y][0] = S[y][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // what the next products take is loaded before these: the compiler would load it after them
+      u32x4 K[2][2];
+      auto load_k = [&](int s) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+        for (int h = 0; h < 2; ++h) K[s & 1][h] = *reinterpret_cast<const u32x4*>(kb + 16 * h * KROW + 64 * s);
+      };
+      load_k(0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 K = *reinterpret_cast<const u32x4*>(kb + 16 * h * KROW + 64 * s);
+      for (int s = 0; s < KS; ++s) {
+        if (s + 1 < KS) load_k(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int y = 0; y < NM; ++y)
 #pragma unroll
-            for (int q = 0; q < QP; ++q) S[y][h] = mma<false>(K, Q[y][s][q], S[y][h]);
-        }
+            for (int q = 0; q < QP; ++q) S[y][h] = mma<false>(K[s & 1][h], Q[y][s][q], S[y][h]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       u32x4 hi[NM], lo[NM];
       uint32_t vis[NM];
 #pragma unroll
@@ -772,16 +783,22 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
           hide(S[y], vis[y], grp);
         }
       }
+      __builtin_amdgcn_s_setprio(1);  // the other wave's products need few instructions
 #pragma unroll
       for (int y = 0; y < NM; ++y) soften<DT>(S[y], sc, m[y], l[y], O[y], 1, hi[y], lo[y]);
+      __builtin_amdgcn_s_setprio(0);
+      u32x4 v[2];
+      v[0] = transposed(vb, 16 * VROW);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        const u32x4 v = transposed(vb + 32 * d, 16 * VROW);
+        if (d + 1 < DT) v[(d + 1) & 1] = transposed(vb + 32 * (d + 1), 16 * VROW);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int y = 0; y < NM; ++y) {
-          O[y][d] = mma<false>(v, hi[y], O[y][d]);
-          O[y][d] = mma<false>(v, lo[y], O[y][d]);
+          O[y][d] = mma<false>(v[d & 1], hi[y], O[y][d]);
+          O[y][d] = mma<false>(v[d & 1], lo[y], O[y][d]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (!plain) {
 #pragma unroll

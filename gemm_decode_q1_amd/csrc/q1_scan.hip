@@ -1,7 +1,8 @@
 // Selective state space scan (q1_memory.h), single tokens and prompts.
 //
 // Single tokens: four lanes have a channel, a quarter of its states each, so that a
-// state is read and written in whole lines and one sequence fills some hundred waves.
+// state is read and written in whole lines and one sequence fills some hundred waves.  One
+// token of 5120 channels of 16 states takes 3.4 us in a graph, a launch's length.
 //
 // Prompts: the same, four waves for 64 channels.  A prompt is cut into pieces so that the
 // waves fill the chip, in three launches:
