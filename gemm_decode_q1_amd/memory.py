@@ -300,8 +300,8 @@ def q1_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, bia
 
     x ``[B, T, C]`` bf16 or fp16 (rows evenly spaced), weight ``[C, W]`` (W 2 to 4, the
     last for the token itself), bias ``[C]`` and state ``[slots, W - 1, C]`` (the last
-    rows, oldest first) of the same dtype; slots int32 ``[B]`` (default: sequence b
-    uses state b)."""
+    rows, oldest first) of the same dtype; slots int32 ``[B]``, distinct (default: sequence b
+    uses state b; outside the states: zeros, and no state touched)."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, C]")
     d, out, index = _conv(x, weight, state, bias, slots, x.shape[0], silu, out, None)
@@ -391,7 +391,8 @@ def q1_scan_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Te
     x, z ``[B, T, Di]`` and B, C ``[B, T, N]`` bf16 or fp16, dt ``[B, T, Di]`` of their
     dtype or fp32 (rows evenly spaced: slices of one projection's rows will do); A
     fp32 ``[Di, N]`` (negative), D and dt_bias fp32 ``[Di]``; state fp32 ``[slots, Di,
-    N]``; slots int32 ``[B]`` (default: sequence b uses state b)."""
+    N]``; slots int32 ``[B]``, distinct (default: sequence b uses state b; outside the
+    states: zeros, and no state touched)."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, Di]")
     d, out, index, _ = _scan(x, dt, A, B, C, state, D, z, dt_bias, softplus, slots, x.shape[0], out, out_dtype, None)
