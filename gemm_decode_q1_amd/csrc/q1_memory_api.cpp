@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;  // workgroups of one launch (2^32 lanes)
 constexpr int64_t kMost = (int64_t)1 << 46;     // elements of one operand
 constexpr int64_t k31 = (int64_t)1 << 31;
+constexpr int64_t kMostTokens = k31 - (1 << 16);  // of a sequence: the tile behind its last one is still counted in 31 bits
 
 // Shapes of the pages (what the workspace query needs).
 q1_status check_kv_shape(const q1_kv* c) {
@@ -52,7 +53,7 @@ q1_status check_kv_query(const q1_kv* c, const q1_kv_query* a) {
   if (a->B < 0 || a->T < 0 || a->max_pages < 0) return fail(Q1_ERR_INVALID_ARG, "B, T and max_pages must be >= 0");
   if (a->q_ld < (int64_t)a->Hq * c->D) return fail(Q1_ERR_INVALID_ARG, "q_ld must cover the heads (got %lld)", (long long)a->q_ld);
   if (a->q_ld % 8 != 0) return fail(Q1_ERR_INVALID_ARG, "q_ld must be a multiple of 8 elements");
-  if (a->max_pages >= k31 || a->max_pages * c->page_size >= k31 || a->B >= k31 || a->T >= k31 / a->Hq ||
+  if (a->max_pages >= k31 || a->max_pages * c->page_size > kMostTokens || a->B >= k31 || a->T >= k31 / a->Hq ||
       (a->T > 0 && a->B >= k31 / (a->T * a->Hq)) || a->q_ld > kMost / (a->B * a->T + 1) ||
       (a->max_pages > 0 && a->B > kMost / a->max_pages))
     return fail(Q1_ERR_UNSUPPORTED, "call too large");

@@ -93,7 +93,7 @@ typedef struct q1_kv_query {
   void* out;                  /* [B, T, Hq, D] in out_dtype; 16-byte aligned */
   float* lse;                 /* [B, T, Hq], or NULL */
   int64_t q_ld;               /* a multiple of 8 */
-  int64_t B, T, max_pages;    /* max_pages * page_size below 2^31 */
+  int64_t B, T, max_pages;    /* max_pages * page_size up to 2^31 - 2^16 */
   int32_t Hq;                 /* Hq % Hkv == 0 */
   int32_t dtype;              /* of q: Q1_BF16 or Q1_F16 */
   int32_t out_dtype;          /* Q1_F32, Q1_F16 or Q1_BF16 */

@@ -187,3 +187,16 @@ def test_scan_without_gate_needs_no_stride():
     assert L.q1_scan_prefill(d, 5000, 1, FAKE, FAKE + 128, need, None) == -1 and "256-byte" in said()
     assert L.q1_scan_prefill_workspace_bytes(scan(N=12), 100, 1) == 0 and "N must be" in said()
     assert L.q1_scan_prefill_workspace_bytes(d, -1, 1) == 0 and L.q1_scan_prefill_workspace_bytes(d, 1 << 31, 1) == 0
+
+
+@pytest.mark.parametrize("page_size,pages_", [(1, (1 << 31) - 1), (1, (1 << 31) - (1 << 16) + 1), (16, 1 << 27), (1 << 16, (1 << 15) - 1)])
+def test_tokens_of_a_sequence(page_size, pages_):
+    """A table may have room for 2^31 - 2^16 tokens: the kernels count the tile behind the last one in 31 bits."""
+    c = kv(pages=3, page_size=page_size, Hkv=1)
+    room = page_size * pages_
+    L = B.load_library()
+    status = L.q1_kv_attn(c, query(B=1, max_pages=pages_, q=None), None, 0, None)
+    if room > (1 << 31) - (1 << 16):
+        assert status == -2 and "too large" in said()
+    else:
+        assert status == -1 and "NULL" in said()
