@@ -6,11 +6,14 @@
 //
 // Prompts: the same, four waves for 64 channels.  A prompt is cut into pieces so that the
 // waves fill the chip, in three launches:
-//   q1_scan_kernel<.., false>  the state at the end of each piece from a zero state, and the
-//                              sum of its deltas (the decay over the piece is exp(A * sum));
-//   q1_scan_join               each piece's first state, one after the other;
-//   q1_scan_kernel<.., true>   the outputs, and from a sequence's last piece its final state.
-// A sequence's last piece needs no first walk, so short sequences have none.
+//   q1_scan_kernel<.., false>  a sequence's first piece with its outputs; for the others the
+//                              state at the end from a zero state, and the sum of the deltas
+//                              (the decay over the piece is exp(A * sum));
+//   q1_scan_join               the state before each piece, one after the other;
+//   q1_scan_kernel<.., true>   the other outputs, and from a last piece the final state.
+// A sequence's last piece needs no first walk, so short sequences have none.  (First pieces
+// in the second launch, walked twice: 8000 tokens of 32 sequences 271 | 248 us, 4099 of 7 189 | 178,
+// one long sequence the same.)
 //
 // Bound by the vector units (busy throughout): a state costs a product, an exponential (8
 // cycles a wave, the others 4), a product and two multiply-adds a token, and without outputs
@@ -312,23 +315,11 @@ struct Walk {
   }
 };
 
+// A piece, from the state before it (or, without outputs, from zeros).
 template <bool F16, bool DT32, int N, bool OUT>
-__global__ __launch_bounds__(kThreads) void q1_scan_kernel(const PromptArgs a) {
+__device__ __forceinline__ void walk_piece(const PromptArgs& a, const Piece& p, int64_t piece, int64_t slot, uint32_t first, BlockLds<N>& m) {
   constexpr int M = N / 4;
   const q1_scan& d = a.d;
-  const int64_t piece = blockIdx.x / a.blocks;
-  const uint32_t first = (uint32_t)(blockIdx.x - piece * a.blocks) * 64;
-  const Piece p = scalar(find_piece_wave(a.r, piece, a.by, a.per));
-  if (p.t0 >= p.t1) return;
-  if (!OUT && p.last()) return;
-  const int64_t slot = scalar(slot_of(d, p.seq));
-  if (slot < 0) {
-    const uint32_t ch = first + (threadIdx.x & 63);
-    if (OUT && ch < d.Di)
-      for (int64_t t = p.t0 + (threadIdx.x >> 6); t < p.t1; t += kThreads / 64) store_out(d.out, d.out_dtype, t * d.Di + ch, 0.f);
-    return;
-  }
-  __shared__ BlockLds<N> m;
   Walk<F16, DT32, N, OUT> w(d, m, p.t1, first);
   const int64_t ch = w.channel();
   float* const st = d.state + (slot * d.Di + ch) * N + w.quad * M;
@@ -337,18 +328,40 @@ __global__ __launch_bounds__(kThreads) void q1_scan_kernel(const PromptArgs a) {
   for (int n = 0; n < M; ++n) w.h[n] = !OUT ? 0.f : p.first() ? st[n] : at[(n - N) * d.Di];
   w.run(p.t0);
   if (!w.live()) return;
-  if constexpr (!OUT) {
-#pragma unroll
-    for (int n = 0; n < M; ++n) at[n * d.Di] = w.h[n];
-    if (w.quad == 0) a.sum[piece * d.Di + ch] = w.sum;
-  } else if (p.last()) {
+  if (OUT && p.last()) {
 #pragma unroll
     for (int n = 0; n < M; ++n) st[n] = w.h[n];
+  } else if (!OUT || p.first()) {
+#pragma unroll
+    for (int n = 0; n < M; ++n) at[n * d.Di] = w.h[n];
+    if (!OUT && w.quad == 0) a.sum[piece * d.Di + ch] = w.sum;
   }
 }
 
-// A lane has one state of one channel of a sequence: from the ends of its pieces to
-// their first states, in place.
+// LAST: the second walk.  The first piece of a sequence of several needs no state of another: the
+// first walk makes its outputs.
+template <bool F16, bool DT32, int N, bool LAST>
+__global__ __launch_bounds__(kThreads) void q1_scan_kernel(const PromptArgs a) {
+  const q1_scan& d = a.d;
+  const int64_t piece = blockIdx.x / a.blocks;
+  const uint32_t first = (uint32_t)(blockIdx.x - piece * a.blocks) * 64;
+  const Piece p = scalar(find_piece_wave(a.r, piece, a.by, a.per));
+  if (p.t0 >= p.t1) return;
+  if (LAST ? p.first() && !p.last() : p.last()) return;
+  const int64_t slot = scalar(slot_of(d, p.seq));
+  if (slot < 0) {
+    const uint32_t ch = first + (threadIdx.x & 63);
+    if ((LAST || p.first()) && ch < d.Di)
+      for (int64_t t = p.t0 + (threadIdx.x >> 6); t < p.t1; t += kThreads / 64) store_out(d.out, d.out_dtype, t * d.Di + ch, 0.f);
+    return;
+  }
+  __shared__ BlockLds<N> m;
+  if (LAST || p.first()) walk_piece<F16, DT32, N, true>(a, p, piece, slot, first, m);
+  else walk_piece<F16, DT32, N, false>(a, p, piece, slot, first, m);
+}
+
+// A lane has one state of one channel of a sequence: from the ends of its pieces (the first
+// one's as it is, the others' from a zero state) to the states before the next ones, in place.
 __global__ __launch_bounds__(kThreads) void q1_scan_join(const PromptArgs a) {
   constexpr int U = 16;  // pieces in flight
   const q1_scan& d = a.d;
@@ -356,16 +369,15 @@ __global__ __launch_bounds__(kThreads) void q1_scan_join(const PromptArgs a) {
   const int64_t seq = divide(i, a.per_seq);
   if (seq >= a.r.nseq) return;
   const uint32_t w = i - (uint32_t)seq * per, n = divide(w, a.channels), ch = w - n * (uint32_t)d.Di;
-  const int64_t slot = slot_of(d, seq);
   const uint32_t begin = cu_at(a.r, seq), end = cu_at(a.r, seq + 1);
-  if (slot < 0 || end <= begin) return;
+  if (end <= begin || slot_of(d, seq) < 0) return;
   const int64_t more = divide(end - begin - 1, a.by), first = divide(begin, a.by) + seq;  // pieces but the last one
-  if (more == 0) return;
+  if (more < 2) return;
   const float A = d.A[(int64_t)ch * d.N + n] * kLog2e;
-  float h = d.state[(slot * d.Di + ch) * d.N + n];
   float* hp = a.h + (first * d.N + n) * d.Di + ch;
   const float* sp = a.sum + first * d.Di + ch;
-  for (int64_t j = 0; j < more; j += U) {
+  float h = hp[0];
+  for (int64_t j = 1; j < more; j += U) {
     float e[U], s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
