@@ -117,6 +117,31 @@ def test_many_whole_sequences():
         check(ops, slice(t, t + lens[s]), before[s], out[t:t + lens[s]], state[s], "f32", True, PIECE, f"sequence {s}")
 
 
+def test_one_long_sequence_among_many():
+    """Of so many sequences that none need be cut only the one with most of the tokens is; the same rows
+    alone, in other pieces, and with no state of its own."""
+    nseq, Di = 520, 512
+    lens = [(5 * i) % 4 for i in range(nseq)]
+    lens[300] = 1700
+    ops = draw(12, (sum(lens),), Di, 16, "bf16", False, nseq)
+    x, dts, A, B, C, state, kw = ops
+    before, alone = state.clone(), state.clone()
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32).cuda()
+    out = Q.q1_scan_prefill(x, dts, A, B, C, state, cu, out_dtype=torch.float32, **kw)
+    for s in (1, 299, 300, 301, 519):
+        t = int(cu[s])
+        check(ops, slice(t, t + lens[s]), before[s], out[t:t + lens[s]], state[s], "f32", True, PIECE, f"sequence {s}")
+    t = int(cu[300])
+    rows = slice(t, t + 1700)
+    z, rest = kw["z"], {k: v for k, v in kw.items() if k != "z"}
+    one = lambda slot: Q.q1_scan_prefill(x[rows], dts[rows], A, B[rows], C[rows], alone, cu[:1].new_tensor([0, 1700]), z=z[rows],  # noqa: E731
+                                         slots=cu[:1].new_tensor([slot]), out_dtype=torch.float32, **rest)
+    got = one(300)
+    check(ops, rows, before[300], got, alone[300], "f32", True, PIECE, "alone")
+    kept = alone.clone()
+    assert not one(nseq).any() and torch.equal(alone, kept)
+
+
 def test_prompt_continues_as_steps_do():
     ops = draw(6, (90,), 48, 16, "f16", False, 2)
     x, dts, A, B, C, state, kw = ops
