@@ -20,9 +20,10 @@
 // queries of 8000 tokens take 543 us for 590 Gflop (both parts of the weights), nine tenths of
 // the rate of a large library product (1.22 PFLOP/s).
 //
-// Measured (us): 32 sequences of 8201 tokens, D 256, 4 bits 50 (the pages at the rate of a copy:
-// 36); 8 of 65537, 3 queries each, D 128, 76 (70); 4 of 519 9.9; 2 x 1000 queries of 5003
-// tokens, 24 heads of D 128, 8 bits 181 (129 at that rate; the join and the parts it reads 20).
+// Measured (us): 32 sequences of up to 8201 tokens, D 256, 4 bits 50, 44 in a graph (the pages at
+// the rate of a copy: 35); 8 of up to 65537, 3 queries each, D 128, 76 (66); 4 of up to 519 8.8;
+// 2 x 1000 queries of up to 5003 tokens, 24 heads of D 128, 8 bits 169 to 181 (129 at the rate
+// above; the join and the parts it reads 20).
 //
 // A token that a query does not see has the score -infinity, whatever its key.  Its
 // weight 0 would still make a NaN of a NaN value, so NaN blocks of values enter as
