@@ -25,9 +25,12 @@
 // 2 x 1000 queries of up to 5003 tokens, 24 heads of D 128, 8 bits 169 to 181 (129 at the rate
 // above; the join and the parts it reads 20).
 //
-// A token that a query does not see has the score -infinity, whatever its key.  Its
-// weight 0 would still make a NaN of a NaN value, so NaN blocks of values enter as
-// zeros, and their columns are made NaN at the end for the queries that see the token.
+// A token that a query does not see has the score -infinity, whatever its key.  Its weight 0
+// would still make a NaN of a value that is not finite, so NaN blocks of values enter as zeros,
+// and their columns are made NaN at the end for the queries that see the token.  In tiles that
+// some query of the item does not see to their end, blocks with a NaN code, or a code that its
+// scale carries out of bf16's range, are treated alike; elsewhere each such value makes its
+// own column what it is.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -294,6 +297,14 @@ struct Tile {
   static __device__ __forceinline__ uint32_t byte(uint32_t s, int j) { return NB == 2 ? s >> (8 * j) & 255u : s; }
 };
 
+// Whether one of 8 bf16 values is infinite or NaN.
+__device__ __forceinline__ bool not_finite(u32x4 w) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t |= (w[j] & 0x7f807f80u) + 0x00800080u;
+  return (t & 0x80008000u) != 0;
+}
+
 // Products of this lane's 8 tokens: those of `vis` (by token of the tile) count.
 __device__ __forceinline__ void hide(f32x4* S, uint32_t vis, int grp) {
   const uint32_t mine = (vis >> (4 * grp) & 15u) | (vis >> (16 + 4 * grp) & 15u) << 4;
@@ -455,17 +466,21 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
         most = most > ke ? most : ke;
         most = most > ve ? most : ve;
       }
-    // Every token counts, and no block is a NaN: else which do, and which blocks of values are, by token
-    const bool plain = __ballot(x.ok[0] && x.ok[1] && most != 255u) == ~0ull;
+    // Every token counts, no block is a NaN and all queries see all tokens: else which tokens
+    // count, and which blocks of values are not finite, by token
+    const bool edge = __ballot(x.ok[0] && x.ok[1] && most != 255u) != ~0ull || t + kTile > least;
     uint32_t in = ~0u;
     uint64_t nan[2][NB];
-    if (!plain) {
+    if (edge) {
       in = (uint32_t)(__ballot(x.ok[0]) & 0xffffu) | (uint32_t)(__ballot(x.ok[1]) & 0xffffu) << 16;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const bool bad = T::byte(x.vs[h], j) == 255u;
+          bool bad = T::byte(x.vs[h], j) == 255u;
+#pragma unroll
+          for (int s = 0; s < KS / NB; ++s)
+            bad |= not_finite(kv_bf16<BITS>(&x.v[h][(j * (KS / NB) + s) * (BITS / 4)], vs[h][j]));
           nan[h][j] = __ballot(x.ok[h] && bad);
           ks[h][j] = T::byte(x.ks[h], j) == 255u ? NAN : ks[h][j];
           vs[h][j] = x.ok[h] && !bad ? vs[h][j] : 1.0f;
@@ -506,7 +521,7 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
     ids_of(id, place);
     u32x4 hi[NM], lo[NM];
     uint32_t vis[NM];
-    if (!plain || t + kTile > least) {
+    if (edge) {
 #pragma unroll
       for (int q = 0; q < NM; ++q) {
         const int32_t d = lim[q] - t;
@@ -525,11 +540,13 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
 #pragma unroll
       for (int q = 0; q < NM; ++q) O[d][q] = mma<false>(v, lo[q], O[d][q]);
     }
-    if (!plain) {
+    if (edge) {
 #pragma unroll
       for (int blk = 0; blk < D / kKvBlock; ++blk) {
         const int sh = 16 * (D == 64 ? 2 * blk : blk / NB), j = blk % NB;
-        const uint32_t bad = (uint32_t)(nan[0][j] >> sh & 0xffffu) | (uint32_t)(nan[1][j] >> sh & 0xffffu) << 16;
+        uint64_t n0 = nan[0][j], n1 = nan[1][j];
+        if constexpr (D == 64) n0 |= n0 >> 16, n1 |= n1 >> 16;  // (two lanes have a block)
+        const uint32_t bad = (uint32_t)(n0 >> sh & 0xffffu) | (uint32_t)(n1 >> sh & 0xffffu) << 16;
 #pragma unroll
         for (int q = 0; q < NM; ++q) lost[q] |= vis[q] & bad ? 1u << blk : 0u;
       }
@@ -634,13 +651,15 @@ struct Staged {
       }
   }
 
-  // To a buffer: keys, values (those of tokens that do not count, and NaN blocks, as zeros; in
-  // every other four rows with neighbouring 16 bytes in each other's places, see item_by_tokens)
-  // and a byte for each part: 1 where the token counts, and 2 where its values are a NaN block.
+  // To a buffer: keys, values (those of tokens that do not count, NaN blocks, and on an `edge`
+  // pieces with a value that is not finite, as zeros; in every other four rows with neighbouring
+  // 16 bytes in each other's places, see item_by_tokens) and a byte for each part: 1 where the
+  // token counts, and 2 where such values of it were left out.
   // The parts of a row write their pieces in an order in which eight of them meet all banks.
-  __device__ __forceinline__ void put(unsigned char* buf, int token, int part) {
+  __device__ __forceinline__ void put(unsigned char* buf, int token, int part, bool edge) {
     constexpr int NP = EP / 8;  // pieces of a part
-    const bool bad = vs == 255u, use = ok && !bad;
+    bool bad = vs == 255u;
+    const bool use = ok && !bad;
     const float kscale = kv_scale(ks), vscale = use ? __uint_as_float(vs << 23) : 1.0f;
     unsigned char* const kr = buf + token * KROW;
     unsigned char* const vr = buf + kRowTile * KROW + token * VROW;
@@ -656,7 +675,14 @@ struct Staged {
     for (int s = 0; s < NP; ++s) {
       const int piece = part * NP + (s ^ turn);
       *reinterpret_cast<u32x4*>(kr + 16 * piece) = kv_bf16<BITS>(&k[s * (BITS / 4)], kscale);
-      *reinterpret_cast<u32x4*>(vr + 16 * (piece ^ (token >> 2 & 1))) = kv_bf16<BITS>(&v[s * (BITS / 4)], vscale);
+      u32x4 w = kv_bf16<BITS>(&v[s * (BITS / 4)], vscale);
+      if (edge) {
+        const bool no = not_finite(w);
+        bad |= no;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = no ? 0u : w[j];
+      }
+      *reinterpret_cast<u32x4*>(vr + 16 * (piece ^ (token >> 2 & 1))) = w;
     }
     buf[kFlags + token * kParts + part] = (ok ? 1 : 0) | (ok && bad ? 2 : 0);
   }
@@ -701,6 +727,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
   // all of the wave's queries see `least` tokens, none more than `most`
   const int32_t least = (int32_t)seen_by(g, it.n, first < g.p.R ? first : g.p.R - 1);
   const int32_t most = first < g.p.R ? (int32_t)seen_by(g, it.n, last - 1) : 0;
+  const int32_t all = (int32_t)seen_by(g, it.n, it.row0);  // all queries of the item see these
   const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e;
 
   // This thread's token of the tile whose page id is fetched next, as in item_by_tokens.
@@ -736,7 +763,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
   int turn = 0;
   for (int32_t t = t0; t < end; t += kRowTile, turn ^= 1) {
     unsigned char* const buf = lds + turn * T::kBytes;
-    x.put(buf, token, part);
+    x.put(buf, token, part, t + kRowTile > all);
     __syncthreads();
     fetch(t + kRowTile);
     id_of();
@@ -804,8 +831,10 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
       if (!plain) {
 #pragma unroll
         for (int blk = 0; blk < D / kKvBlock; ++blk) {
-          const int p = blk * kKvBlock / T::EP;  // its (first) part
-          const uint32_t bad = (uint32_t)(__ballot((p < 4 ? flags.x : flags.y) >> (8 * (p % 4) + 1) & 1u) >> (kTile * sub));
+          constexpr int PB = kKvBlock / T::EP;  // its parts, p the first of them
+          constexpr uint32_t two = PB == 4 ? 0x02020202u : PB == 2 ? 0x0202u : 0x02u;
+          const int p = blk * PB;
+          const uint32_t bad = (uint32_t)(__ballot(((p < 4 ? flags.x : flags.y) >> (8 * (p % 4)) & two) != 0) >> (kTile * sub));
 #pragma unroll
           for (int y = 0; y < NM; ++y) lost[y] |= vis[y] & bad ? 1u << blk : 0u;
         }
