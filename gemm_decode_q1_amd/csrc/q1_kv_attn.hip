@@ -651,15 +651,21 @@ struct Staged {
       }
   }
 
-  // To a buffer: keys, values (those of tokens that do not count, NaN blocks, and on an `edge`
-  // pieces with a value that is not finite, as zeros; in every other four rows with neighbouring
-  // 16 bytes in each other's places, see item_by_tokens) and a byte for each part: 1 where the
-  // token counts, and 2 where such values of it were left out.
+  // A part with a value that is not finite is taken for one of a NaN block.
+  __device__ __forceinline__ void mark_not_finite() {
+    bool no = false;
+#pragma unroll
+    for (int s = 0; s < EP / 8; ++s) no |= not_finite(kv_bf16<BITS>(&v[s * (BITS / 4)], kv_scale(vs)));
+    vs = no ? 255u : vs;
+  }
+
+  // To a buffer: keys, values (those of tokens that do not count, and NaN blocks, as zeros; in
+  // every other four rows with neighbouring 16 bytes in each other's places, see item_by_tokens)
+  // and a byte for each part: 1 where the token counts, and 2 where its values are a NaN block.
   // The parts of a row write their pieces in an order in which eight of them meet all banks.
-  __device__ __forceinline__ void put(unsigned char* buf, int token, int part, bool edge) {
+  __device__ __forceinline__ void put(unsigned char* buf, int token, int part) {
     constexpr int NP = EP / 8;  // pieces of a part
-    bool bad = vs == 255u;
-    const bool use = ok && !bad;
+    const bool bad = vs == 255u, use = ok && !bad;
     const float kscale = kv_scale(ks), vscale = use ? __uint_as_float(vs << 23) : 1.0f;
     unsigned char* const kr = buf + token * KROW;
     unsigned char* const vr = buf + kRowTile * KROW + token * VROW;
@@ -675,14 +681,7 @@ struct Staged {
     for (int s = 0; s < NP; ++s) {
       const int piece = part * NP + (s ^ turn);
       *reinterpret_cast<u32x4*>(kr + 16 * piece) = kv_bf16<BITS>(&k[s * (BITS / 4)], kscale);
-      u32x4 w = kv_bf16<BITS>(&v[s * (BITS / 4)], vscale);
-      if (edge) {
-        const bool no = not_finite(w);
-        bad |= no;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = no ? 0u : w[j];
-      }
-      *reinterpret_cast<u32x4*>(vr + 16 * (piece ^ (token >> 2 & 1))) = w;
+      *reinterpret_cast<u32x4*>(vr + 16 * (piece ^ (token >> 2 & 1))) = kv_bf16<BITS>(&v[s * (BITS / 4)], vscale);
     }
     buf[kFlags + token * kParts + part] = (ok ? 1 : 0) | (ok && bad ? 2 : 0);
   }
@@ -763,7 +762,8 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
   int turn = 0;
   for (int32_t t = t0; t < end; t += kRowTile, turn ^= 1) {
     unsigned char* const buf = lds + turn * T::kBytes;
-    x.put(buf, token, part, t + kRowTile > all);
+    if (t + kRowTile > all) x.mark_not_finite();
+    x.put(buf, token, part);
     __syncthreads();
     fetch(t + kRowTile);
     id_of();

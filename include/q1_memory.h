@@ -84,7 +84,10 @@ q1_status q1_kv_read(const q1_kv* c, const int32_t* slots, int64_t rows, void* k
  * lse = -infinity.  Rows that a query does not see are never used, whatever they
  * hold.  Scores, softmax and sums are fp32; keys, values and queries enter the
  * products as they are, a weight as two bf16 parts (2^-17).  A NaN block of a key that
- * a query sees makes its row and its lse NaN, one of a value its 32 columns.
+ * a query sees makes its row and its lse NaN, one of a value its 32 columns.  Bytes that
+ * q1_kv_write does not make (the codes 0x7f and 0xff of 8 bits, larger scales) may stand
+ * for a NaN or for more than bf16 holds: of a value, that makes at least its own column
+ * NaN or infinite for the queries that see it, and at most the block's 32.
  */
 typedef struct q1_kv_query {
   const void* q;              /* [B, T, Hq, D], q_ld elements between tokens (b*T + t); 16-byte aligned */
