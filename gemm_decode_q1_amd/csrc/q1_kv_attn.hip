@@ -9,8 +9,10 @@
 //   S^T = K Q^T     O^T = V^T P^T, values transposed on their way out of LDS.
 // fp16 queries enter as two bf16 parts (11 bits of significand are 8 and 3), weights as
 // two (2^-17: one would add an error of the size of the output's rounding).  The running
-// maximum stays where it is until a weight could pass 2^8, so o is rescaled rarely: a
-// power of two more in a weight costs no bits.
+// maximum stays where it is until a token is 2^8 above it, so o is rescaled rarely, and for n
+// tokens weights are relative to 2^8 2^bits(n) times the kept maximum: their sum is below 1, so o
+// is finite wherever the values are (a power of two in a weight costs no bits; weights below
+// n 2^-117 of the largest may become 0).
 //
 // By tokens (few rows): 4 waves, each with a quarter of the tokens and 16 or 32 rows,
 // joined in LDS; keys go from memory to the matrix core through registers alone.  Bound by
@@ -173,6 +175,9 @@ __device__ __forceinline__ Item whole_item(const KvArgs& g, uint32_t i) {
   return it;
 }
 
+// Weights of a sequence of n tokens are smaller than those relative to the kept maximum by 2^this.
+__device__ __forceinline__ int down_of(uint32_t n) { return 8 + 32 - __builtin_clz(n | 1u); }
+
 // Calls f(item) for each of this workgroup's items.
 template <int WAVES, typename F>
 __device__ __forceinline__ void each_item(const KvArgs& g, uint32_t* lds, F f) {
@@ -314,10 +319,10 @@ __device__ __forceinline__ void hide(f32x4* S, uint32_t vis, int grp) {
 
 // The softmax of one tile for a block of 16 queries: products of this lane's 8 tokens in,
 // weights out as two operands; m, l and the output so far are brought to a new maximum
-// where a product is so far above the old one that a weight could pass 2^8.  (One call for
-// all tiles: where it was one of two, the output was copied at each, a quarter of the time.)
+// where a product is over 2^8 above the old one.  (One call for all tiles: where it was one of
+// two, the output was copied at each, a quarter of the time.)
 template <int DT>
-__device__ __forceinline__ void soften(const f32x4* S, float sc, float& m, float& l, f32x4* O, int stride, u32x4& hi, u32x4& lo) {
+__device__ __forceinline__ void soften(const f32x4* S, float sc, float down, float& m, float& l, f32x4* O, int stride, u32x4& hi, u32x4& lo) {
   float s[8], top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -332,7 +337,7 @@ __device__ __forceinline__ void soften(const f32x4* S, float sc, float& m, float
     for (int d = 0; d < DT; ++d) O[d * stride] *= keep;
     m = mn;
   }
-  const float base = m == -INFINITY ? 0.f : -m * sc;
+  const float base = m == -INFINITY ? 0.f : __builtin_fmaf(-m, sc, -down);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], sc, base));
@@ -344,6 +349,11 @@ __device__ __forceinline__ void soften(const f32x4* S, float sc, float& m, float
     hi[j] = round2<false>(s[2 * j], s[2 * j + 1], &rx, &ry);
     lo[j] = round2<false>(rx, ry, &r0, &r1);
   }
+}
+
+// log(sum 2^top), of weights smaller by 2^down.
+__device__ __forceinline__ float lse_of(float top, float sum, int down) {
+  return (top - (float)down) * 0.69314718055994530942f + logf(__builtin_ldexpf(sum, down));
 }
 
 // Four elements of a row: the row itself, or its part of it.
@@ -358,7 +368,7 @@ __device__ __forceinline__ void put_row(const KvArgs& g, const Item& it, uint32_
     if (g.a.out_dtype == F32) *reinterpret_cast<f32x4*>(static_cast<float*>(g.a.out) + at) = o;
     else if (g.a.out_dtype == F16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.a.out) + at) = uint2{pack16<true>(o[0], o[1]), pack16<true>(o[2], o[3])};
     else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.a.out) + at) = uint2{pack16<false>(o[0], o[1]), pack16<false>(o[2], o[3])};
-    if (e == 0 && g.a.lse != nullptr) g.a.lse[row] = nothing ? -INFINITY : top * 0.69314718055994530942f + logf(sum);
+    if (e == 0 && g.a.lse != nullptr) g.a.lse[row] = nothing ? -INFINITY : lse_of(top, sum, down_of(it.n));
   } else {
     const int64_t at = (int64_t)it.part * g.p.rows + (r - it.row0);
     *reinterpret_cast<f32x4*>(g.part_o + at * g.c.D + e) = o;
@@ -450,7 +460,7 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
   const int swap = 16 * (col >> 2 & 1);
   unsigned char* const vw = vt + col * VROW + grp * (D / 2);
   const unsigned char* const vr = vt + (4 * grp + col / 4) * VROW + ((16 * (col >> 1 & 1)) ^ (16 * (grp & 1))) + 8 * (col & 1);
-  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e;
+  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e, down = (float)down_of(it.n);
 
   // One tile; the next one's loads start as soon as this one's registers are free.
   auto work = [&](int32_t t, T& x, int32_t* id, uint32_t* place) {
@@ -530,7 +540,7 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
       }
     }
 #pragma unroll
-    for (int q = 0; q < NM; ++q) soften<DT>(S[q], sc, m[q], l[q], &O[0][q], NM, hi[q], lo[q]);
+    for (int q = 0; q < NM; ++q) soften<DT>(S[q], sc, down, m[q], l[q], &O[0][q], NM, hi[q], lo[q]);
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -579,7 +589,7 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
   for (int q = 0; q < NM; ++q) {
     const int r = wave * 16 * NM + 16 * q + col;
     const float sum = sum_groups(l[q]);
-    if (grp == 0) sml[r] = float2{m[q] == -INFINITY ? m[q] : m[q] * sc, sum};
+    if (grp == 0) sml[r] = float2{m[q] == -INFINITY ? m[q] : __builtin_fmaf(m[q], sc, down), sum};
 #pragma unroll
     for (int d = 0; d < DT; ++d)
       *reinterpret_cast<f32x4*>(so + r * OROW + 16 * d + 4 * grp) = lost[q] >> (d / 2) & 1u ? f32x4{NAN, NAN, NAN, NAN} : O[d][q];
@@ -727,7 +737,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
   const int32_t least = (int32_t)seen_by(g, it.n, first < g.p.R ? first : g.p.R - 1);
   const int32_t most = first < g.p.R ? (int32_t)seen_by(g, it.n, last - 1) : 0;
   const int32_t all = (int32_t)seen_by(g, it.n, it.row0);  // all queries of the item see these
-  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e;
+  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e, down = (float)down_of(it.n);
 
   // This thread's token of the tile whose page id is fetched next, as in item_by_tokens.
   const uint32_t ps = (uint32_t)c.page_size, more_pg = kRowTile / ps, more_off = kRowTile - more_pg * ps;
@@ -813,7 +823,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
       }
       __builtin_amdgcn_s_setprio(1);  // the other wave's products need few instructions
 #pragma unroll
-      for (int y = 0; y < NM; ++y) soften<DT>(S[y], sc, m[y], l[y], O[y], 1, hi[y], lo[y]);
+      for (int y = 0; y < NM; ++y) soften<DT>(S[y], sc, down, m[y], l[y], O[y], 1, hi[y], lo[y]);
       __builtin_amdgcn_s_setprio(0);
       u32x4 v[2];
       v[0] = transposed(vb, 16 * VROW);
@@ -844,7 +854,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
 #pragma unroll
   for (int y = 0; y < NM; ++y) {
     const uint32_t r = first + 16 * y + col;
-    const float sum = sum_groups(l[y]), top = m[y] == -INFINITY ? m[y] : m[y] * sc;
+    const float sum = sum_groups(l[y]), top = m[y] == -INFINITY ? m[y] : __builtin_fmaf(m[y], sc, down);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
       if (r < g.p.R) put_row(g, it, r, 16 * d + 4 * grp, lost[y] >> (d / 2) & 1u ? f32x4{NAN, NAN, NAN, NAN} : O[y][d], top, sum);
@@ -970,7 +980,7 @@ __global__ __launch_bounds__(64 * kWaves) void q1_kv_join(const KvArgs g) {
       else v = o[j][e];
       store_out(a.out, a.out_dtype, row * D + lane * E + e, nothing ? 0.f : v * inv);
     }
-    if (lane == 0 && a.lse != nullptr) a.lse[row] = nothing ? -INFINITY : top[j] * 0.69314718055994530942f + logf(all);
+    if (lane == 0 && a.lse != nullptr) a.lse[row] = nothing ? -INFINITY : lse_of(top[j], all, down_of(length_of(g, b)));
   }
 }
 

@@ -83,7 +83,8 @@ q1_status q1_kv_read(const q1_kv* c, const int32_t* slots, int64_t rows, void* k
  * is outside [0, pages) is left out.  A query that sees no token gives zeros and
  * lse = -infinity.  Rows that a query does not see are never used, whatever they
  * hold.  Scores, softmax and sums are fp32; keys, values and queries enter the
- * products as they are, a weight as two bf16 parts (2^-17).  A NaN block of a key that
+ * products as they are, a weight as two bf16 parts (2^-17); of n tokens, those whose
+ * weight is below n 2^-117 of the largest may be left out.  A NaN block of a key that
  * a query sees makes its row and its lse NaN, one of a value its 32 columns.  Bytes that
  * q1_kv_write does not make (the codes 0x7f and 0xff of 8 bits, larger scales) may stand
  * for a NaN or for more than bf16 holds: of a value, that makes at least its own column
