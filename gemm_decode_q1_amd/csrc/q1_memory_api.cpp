@@ -3,6 +3,8 @@
 // device.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
 #include "../../include/q1_memory.h"
 #include "q1_internal.h"
 #include "q1_memory.h"
@@ -53,6 +55,7 @@ q1_status check_kv_query(const q1_kv* c, const q1_kv_query* a) {
   if (a->B < 0 || a->T < 0 || a->max_pages < 0) return fail(Q1_ERR_INVALID_ARG, "B, T and max_pages must be >= 0");
   if (a->q_ld < (int64_t)a->Hq * c->D) return fail(Q1_ERR_INVALID_ARG, "q_ld must cover the heads (got %lld)", (long long)a->q_ld);
   if (a->q_ld % 8 != 0) return fail(Q1_ERR_INVALID_ARG, "q_ld must be a multiple of 8 elements");
+  if (!std::isfinite(a->scale)) return fail(Q1_ERR_INVALID_ARG, "scale must be finite");
   if (a->max_pages >= k31 || a->max_pages * c->page_size > kMostTokens || a->B >= k31 || a->T >= k31 / a->Hq ||
       (a->T > 0 && a->B >= k31 / (a->T * a->Hq)) || a->q_ld > kMost / (a->B * a->T + 1) ||
       (a->max_pages > 0 && a->B > kMost / a->max_pages))
