@@ -205,7 +205,10 @@ q1_status q1_kv_read(const q1_kv* c, const int32_t* slots, int64_t rows, void* k
 size_t q1_kv_attn_workspace_bytes(const q1_kv* c, const q1_kv_query* a) {
   if (check_kv_query(c, a) != Q1_OK) return 0;
   ok();
-  return a->B == 0 || a->T == 0 ? 0 : plan_kv_attn(*c, *a).ws_bytes;
+  if (a->B == 0 || a->T == 0) return 0;
+  const KvPlan plan = plan_kv_attn(*c, *a);
+  if (plan.too_large) fail(Q1_ERR_UNSUPPORTED, "call too large");
+  return plan.ws_bytes;
 }
 
 q1_status q1_kv_attn(const q1_kv* c, const q1_kv_query* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -273,12 +276,13 @@ size_t q1_scan_prefill_workspace_bytes(const q1_scan* d, int64_t tokens, int64_t
     fail(Q1_ERR_INVALID_ARG, "tokens and nseq must be >= 0");
     return 0;
   }
-  if (tokens >= k31 || nseq >= k31 / (4 * d->Di)) {
+  ok();
+  if (tokens == 0 || nseq == 0) return 0;
+  if (tokens >= k31 || nseq >= k31 / (4 * d->Di) || scan_too_large(*d, tokens, nseq)) {
     fail(Q1_ERR_UNSUPPORTED, "call too large");
     return 0;
   }
-  ok();
-  return tokens == 0 || nseq == 0 ? 0 : scan_ws_bytes(*d, tokens, nseq);
+  return scan_ws_bytes(*d, tokens, nseq);
 }
 
 q1_status q1_scan_prefill(const q1_scan* d, int64_t tokens, int64_t nseq, const int32_t* cu_seqlens, void* workspace,

@@ -8,8 +8,9 @@
  * argument checks before any HIP call, then the workspace check, then the device
  * check; calls only enqueue work on `stream`, allocate nothing, keep nothing
  * between calls, and can be captured in a HIP graph.  Workspaces need no initial
- * contents; calls that may run at the same time need separate ones.  Outputs must
- * not overlap inputs, but for states, which are updated in place.
+ * contents; calls that may run at the same time need separate ones.  A workspace
+ * query returns 0 for a call that needs none, and with an error text for one that is
+ * refused.  Outputs must not overlap inputs, but for states, which are updated in place.
  *
  * Numbers the kernels read from device memory (lengths, offsets, page and slot
  * ids) cannot be checked by the call; each one below says what an id outside
