@@ -37,3 +37,12 @@ def test_workspace_of_a_refused_attention():
     a = dict(B=1 << 18, max_pages=1 << 20, Hq=64, q_ld=64 * 64)
     assert L.q1_kv_attn(c, query(**a), FAKE, 1 << 50, None) == -2 and "too large" in said()
     assert L.q1_kv_attn_workspace_bytes(c, query(**a)) == 0 and "too large" in said()
+
+
+@pytest.mark.parametrize("tokens,nseq,Di", [(16895, 512, 512), (16384 + 255, 256, 1024), (8480, 61, 5120), (1 << 20, 5000, 64)])
+def test_a_long_sequence_among_many_is_cut(tokens, nseq, Di):
+    """Whatever the batch, a piece of a prompt's scan has at most 512 tokens: one sequence that has nearly all
+    tokens would else be left to few workgroups.  The workspace has N + 1 numbers for each channel of each piece."""
+    kw = dict(Di=Di, x_ld=Di, dt_ld=Di, z_ld=Di, slots=nseq)
+    got = B.load_library().q1_scan_prefill_workspace_bytes(scan(**kw), tokens, nseq)
+    assert got >= (tokens // 512 + nseq) * Di * 17 * 4
