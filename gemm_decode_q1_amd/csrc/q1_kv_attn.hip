@@ -178,6 +178,12 @@ __device__ __forceinline__ Item whole_item(const KvArgs& g, uint32_t i) {
 // Weights of a sequence of n tokens are smaller than those relative to the kept maximum by 2^this.
 __device__ __forceinline__ int down_of(uint32_t n) { return 8 + 32 - __builtin_clz(n | 1u); }
 
+// What products are multiplied by (of queries with the scale's sign, see load_q): finite, so
+// that a product of 0 is a score of 0 at any scale.
+__device__ __forceinline__ float factor_of(float scale) {
+  return scale == 0.f ? 1.0f : fminf(fabsf(scale) * kLog2e, 0x1.fffffep127f);
+}
+
 // Calls f(item) for each of this workgroup's items.
 template <int WAVES, typename F>
 __device__ __forceinline__ void each_item(const KvArgs& g, uint32_t* lds, F f) {
@@ -460,7 +466,7 @@ __device__ __forceinline__ void item_by_tokens(const KvArgs& g, const Item& it, 
   const int swap = 16 * (col >> 2 & 1);
   unsigned char* const vw = vt + col * VROW + grp * (D / 2);
   const unsigned char* const vr = vt + (4 * grp + col / 4) * VROW + ((16 * (col >> 1 & 1)) ^ (16 * (grp & 1))) + 8 * (col & 1);
-  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e, down = (float)down_of(it.n);
+  const float sc = factor_of(a.scale), down = (float)down_of(it.n);
 
   // One tile; the next one's loads start as soon as this one's registers are free.
   auto work = [&](int32_t t, T& x, int32_t* id, uint32_t* place) {
@@ -737,7 +743,7 @@ __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, un
   const int32_t least = (int32_t)seen_by(g, it.n, first < g.p.R ? first : g.p.R - 1);
   const int32_t most = first < g.p.R ? (int32_t)seen_by(g, it.n, last - 1) : 0;
   const int32_t all = (int32_t)seen_by(g, it.n, it.row0);  // all queries of the item see these
-  const float sc = a.scale == 0.f ? 1.0f : fabsf(a.scale) * kLog2e, down = (float)down_of(it.n);
+  const float sc = factor_of(a.scale), down = (float)down_of(it.n);
 
   // This thread's token of the tile whose page id is fetched next, as in item_by_tokens.
   const uint32_t ps = (uint32_t)c.page_size, more_pg = kRowTile / ps, more_off = kRowTile - more_pg * ps;

@@ -102,3 +102,14 @@ def test_a_few_large_values(seed, n, T, Hq, Hkv, D, room, bits):
     q = torch.from_numpy(2 * r.standard_normal((T, Hq, D))).bfloat16()
     out, lse, hk, hv = run(k, torch.from_numpy(v).bfloat16(), q, bits, page=64, room=room)
     check(out, lse, hk, hv, q, sorted({0, T // 2, max(0, T - 2), T - 1}))
+
+
+@pytest.mark.parametrize("T,Hkv,room", [(1, 1, 0), (1024, 32, 4096)])
+def test_the_largest_scale(T, Hkv, room):
+    """Scores of 0 are 0 at any scale: a row is the mean of what it sees."""
+    D, n = 64, max(T, 70)
+    k, v = torch.ones(n, Hkv, D).bfloat16(), torch.arange(n).remainder(7)[:, None, None].expand(n, Hkv, D).bfloat16()
+    q = torch.zeros(T, Hkv, D).bfloat16()
+    for scale in (3.4e38, -3.4e38, 1e-45):
+        out, lse, hk, hv = run(k, v, q, 8, room=room, scale=scale)
+        check(out, lse, hk, hv, q, sorted({0, T // 2, T - 1}), scale=scale)
