@@ -58,7 +58,7 @@ typedef struct q1_kv {
  * distinct (of one that comes twice, the row is a mixture of both); a row whose
  * slot is outside [0, pages * page_size) is not written.
  *   k, v   token t, head j, element i: k[t*k_ld + j*D + i], in dtype (Q1_BF16 or
- *          Q1_F16); 16-byte aligned, k_ld and v_ld multiples of 8
+ *          Q1_F16); 16-byte aligned, k_ld and v_ld multiples of 8, below 2^23
  *   slots  device int32 [tokens]
  */
 q1_status q1_kv_write(const q1_kv* c, const void* k, const void* v, int32_t dtype, int64_t k_ld, int64_t v_ld,
