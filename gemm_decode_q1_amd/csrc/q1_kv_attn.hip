@@ -19,13 +19,13 @@
 // the bytes of the pages and by the vector instructions (98 a wave for 16 rows x 32 tokens).
 // By rows (prompts): 8 waves, each with 32 rows (16 of D 256); a tile of 64 tokens is
 // converted once for all of them.  Bound by the products, where there is much to do: 8000
-// queries of 8000 tokens take 543 us for 590 Gflop (both parts of the weights), nine tenths of
-// the rate of a large library product (1.22 PFLOP/s).
+// queries of 8000 tokens of 8 bits take 540 to 557 us for 590 Gflop (both parts of the weights),
+// nine tenths of the rate of a large library product (1.11 to 1.22 PFLOP/s), fp16 ones 647 for 786.
 //
-// Measured (us): 32 sequences of up to 8201 tokens, D 256, 4 bits 50, 44 in a graph (the pages at
-// the rate of a copy: 35); 8 of up to 65537, 3 queries each, D 128, 76 (66); 4 of up to 519 8.8;
-// 2 x 1000 queries of up to 5003 tokens, 24 heads of D 128, 8 bits 169 to 181 (129 at the rate
-// above; the join and the parts it reads 20).
+// Measured (us): 32 sequences of up to 8201 tokens, D 256, 4 bits 51, 45 in a graph (the pages at
+// the rate of a copy: 35); 8 of up to 65537, 3 queries each, D 128, 76 (66); 4 of up to 519 9.1;
+// 2 x 1000 queries of 4525 and 5003 tokens, 24 heads of D 128, 8 bits 170 to 180 (129 at the rate
+// above; the join and the parts it reads 20), of 3531 and 5003 176, of 4 bits 160, fp16 186 and 179.
 //
 // A token that a query does not see has the score -infinity, whatever its key.  Its weight 0
 // would still make a NaN of a value that is not finite, so NaN blocks of values enter as zeros,
@@ -706,9 +706,9 @@ struct Staged {
 // An item by rows: each of 8 waves has 16 NM rows, the tiles of 64 tokens are converted once for
 // all waves and lie in LDS, two in turn.  Against 16 rows a wave and two workgroups a compute
 // unit, 32 rows and one workgroup halve what is converted, and what is read from LDS
-// for each product.  2 x 1000 queries of 5003 tokens (D 128, 4 bits): 197 | 192 us, fp16 137 |
-// 130; with loads a step ahead of their products and the priority 206 | 194 (8 bits, without
-// and with), 8000 of 8000 563 | 543.
+// for each product.  2 x 1000 queries of 3531 and 5003 tokens, D 128, 8 bits: 181 | 176 us, fp16 213
+// | 186, of 4 bits 165 | 160 and 194 | 179; 8000 of 8000 558 | 541, of 4 bits 532 | 552.  Loads a
+// step ahead of their products and the priority, without and with: 186 | 176, 8000 566 | 541.
 template <bool F16, int BITS, int D, int NM>
 __device__ __forceinline__ void item_by_rows(const KvArgs& g, const Item& it, unsigned char* lds) {
   constexpr int QP = F16 ? 2 : 1, KS = D / 32, DT = D / 16;
@@ -1050,8 +1050,11 @@ KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a) {
   p.nm = p.R > 16 && c.D < 256 ? 2 : 1;  // groups of 16 rows a wave: 256 registers hold two of D 128
   const int64_t cus = device_cus(), units = up_div(a.max_pages * c.page_size, kStep);
   // By rows where that form has a full item for half of the compute units, and many tokens.  D 128,
-  // group 6, 4 heads of keys, tokens | rows: 8000 queries of 8000 tokens 905 | 599 us, 2 x 1000 of
-  // 5003 276 | 216; few tokens or few items: 2048 of 2048 70 | 96, 512 of 512 16 | 29.
+  // group 6, 4 heads of keys, 4 bits, tokens | rows: 8000 queries of 8000 tokens 729 | 552 us, 2 x 1000
+  // of 3531 and 5003 199 | 163; few tokens or few items: 2048 of 2048 64 | 91, 512 of 512 14 | 30.
+  // Lengths are on the device, so `units` is what the table has room for: a wide table of short
+  // sequences is taken for long ones (4 x 512 queries of 512 in a table for 4096 or more 35 | 46,
+  // 2048 of 2048 64 | 97; single tokens are cut then, 4 x 519 9.8 | 11, 32 x 2000 21 | 18).
   const int64_t row_items = a.B * (p.R / (16 * p.nm * kRowWaves)) * c.Hkv;
   p.by_rows = 2 * row_items >= cus && units >= 32;
   p.rows = 16 * p.nm * (p.by_rows ? kRowWaves : 1);
@@ -1061,9 +1064,12 @@ KvPlan plan_kv_attn(const q1_kv& c, const q1_kv_query& a) {
   p.entries = p.too_large ? 0 : (uint32_t)(a.B * p.row_blocks);
   // Whole items, or an even cut of all of their units over the workgroups that run at a time:
   // where the last round of whole items would leave more units of time unused than joining costs
-  // (a unit of an item by rows takes 4.7 us, one by tokens 1 to 2).  Whole | cut by tokens: 128
-  // items of 16 units 20.3 | 22.0 us, 304 of 40 90 | 54, 752 of 40 139 | 145, 16 of 5 12.6 | 16.1;
-  // by rows: 192 of 40 231 | 216, 188 of 40 (D 256) 247 | 214, 752 of 63 599 | 798.
+  // (a unit of an item by rows takes 4.7 us, one by tokens 1 to 2).  Whole | cut by tokens, 4 bits:
+  // 304 items of 40 units 64 | 54 us, 752 of 40 90 | 106, 600 of 16 38 | 51, 512 of 16 33 | 35, 16 of 5
+  // 10.2 | 11.5, and at the border 128 of 16 21.8 | 18.8; by rows: 192 of 40 213 | 174, 188 of 40
+  // (D 256) 224 | 195, 752 of 63 543 | 748.  Two workgroups by tokens are counted for a compute unit;
+  // of D 64 and 128 with 16 rows three or four would fit, of fp16 and D 256 only one does (86 KB of
+  // LDS): 32 sequences of 6000 to 8201 tokens 73 us, of bf16 49.
   const int64_t slots = cus * (p.by_rows ? 1 : 2), room = up_div(items, slots) * slots;
   p.cut = !p.too_large && units * (room - items) > (p.by_rows ? 4 : 10 + items / 64) * room;
   if (!p.cut) {

@@ -18,10 +18,10 @@
 // Bound by the vector units (busy throughout): a state costs a product, an exponential (8
 // cycles a wave, the others 4), a product and two multiply-adds a token, and without outputs
 // one less, so that one walk over 16384 tokens of 5120 channels of 16 states cannot take less
-// than 235 us at 2.15 GHz, both 430; with deltas, skip and gate 544 to 578 are measured.  Reading and
+// than 235 us at 2.15 GHz, both 430; with deltas, skip and gate 544 to 593 are measured.  Reading and
 // writing rows would take 136.  A lane with all states of a channel, B and C in scalar
 // registers, needs a tenth fewer instructions but four times the pieces: 602 us, 4099 tokens of 7
-// sequences 206 | 164, 16000 of 60 (whole, but for very long ones) 572 | 410, 77 of one 24 | 16.
+// sequences 206 | 164, 16000 of 60 (whole) 572 | 408, 77 of one 24 | 16.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
