@@ -422,20 +422,23 @@ size_t sums_at(const q1_scan& d, int64_t pieces) { return ((size_t)pieces * d.N 
 }  // namespace
 
 // Tokens of a piece, so that there are about seven workgroups a compute unit, but 64 to 256, and 32
-// for little work.  Where the sequences alone are 16 workgroups a unit, 512: few of them have a second
-// piece, but one that has nearly all tokens is still cut.  5120 channels of 16 states, us: 16384 tokens by
-// 128 566, by 256 558, by 512 570, whole 2374; 4099 of 7 sequences by 64 167, 128 156, 192 162, 256 160, 512
-// 225; 8000 of 32 by 128 251, 256 239, 512 282, whole 260; 600 of one by 32 45, 64 44, 128 50; 300 by 32 30,
-// 64 32; 77 by 32 20, whole 16.  Sequences that fill the chip: 16000 of 60 by 256 426, 512 408, whole 408; 60
-// of 267 by 256 374, 512 351, whole 344; 60 of 8 and one of 8000 by 256 336, 512 376, an eighth of all tokens
-// 478, whole 1229; of 512 channels 600 of 27 by 64 94, 256 89, 512 87, whole 71, and 511 of one token and one
-// of 16384 by 64 138, 256 144, 512 201, an eighth 638, whole 2399.
+// for little work.  Where the sequences alone are 16 workgroups a unit, an eighth of all tokens, up to
+// 512: few of them have a second piece, but one that has nearly all tokens is still cut.  5120 channels
+// of 16 states, us: 16384 tokens by 128 566, by 256 558, by 512 570, whole 2374; 4099 of 7 sequences by 64
+// 167, 128 156, 192 162, 256 160, 512 225; 8000 of 32 by 128 251, 256 239, 512 282, whole 260; 600 of one by
+// 32 45, 64 44, 128 50; 300 by 32 30, 64 32; 77 by 32 20, whole 16.  Sequences that fill the chip: 16000 of 60
+// by 256 426, 512 408, whole 408; 60 of 267 by 256 374, 512 351, whole 344; 60 of 8 and one of 8000 by 256
+// 336, 512 376, 1060 478, whole 1229; of 512 channels 600 of 27 by 64 94, 256 89, 512 87, whole 71, and 511
+// of one token and one of 16384 by 64 138, 256 144, 512 201, 2112 638, whole 2399.
 int64_t scan_chunk(const q1_scan& d, int64_t tokens, int64_t nseq) {
   const int64_t blocks = (d.Di + 63) / 64, cus = device_cus(), work = tokens * blocks;
   int64_t per = (work / (7 * cus) + kBlock / 2) / kBlock * kBlock;
   if (per > 256) per = 256;
   if (per < 64) per = work < 96 * cus ? 32 : 64;
-  if (nseq * blocks >= 16 * cus) per = 512;
+  if (nseq * blocks >= 16 * cus && per < tokens / 8) {
+    per = (tokens / 8 + kBlock - 1) / kBlock * kBlock;
+    if (per > 512) per = 512;
+  }
   return tokens <= (per > 96 ? per : 96) ? 0 : per;  // (no sequence has a second piece)
 }
 

@@ -46,3 +46,11 @@ def test_a_long_sequence_among_many_is_cut(tokens, nseq, Di):
     kw = dict(Di=Di, x_ld=Di, dt_ld=Di, z_ld=Di, slots=nseq)
     got = B.load_library().q1_scan_prefill_workspace_bytes(scan(**kw), tokens, nseq)
     assert got >= (tokens // 512 + nseq) * Di * 17 * 4
+
+
+def test_pieces_of_a_small_batch():
+    """Sequences that fill the chip but have few tokens are cut as a single one is, not less."""
+    L = B.load_library()
+    for tokens, most in ((400, 64), (1000, 128), (3000, 384)):
+        kw = dict(Di=5120, x_ld=5120, dt_ld=5120, z_ld=5120, slots=64)
+        assert L.q1_scan_prefill_workspace_bytes(scan(**kw), tokens, 64) >= (tokens // most + 64) * 5120 * 17 * 4
